@@ -57,6 +57,15 @@ SIGNATURES = {
     "fp8_mqa_topk": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _P]),
     "fp8_mqa_topk_windowed": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _I32, _P, _P, _P]),
     "fp8_mqa_topk_ex": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _I32, _I32, _P, _P, _P]),
+    "fp8_mqa_cache_write": (ctypes.c_int, [_P, _I64, _I32, _P, _I64, _I64, _P, _P, _I64, _I64, _P,
+                                           _P]),
+    "fp8_mqa_cache_read": (ctypes.c_int, [_P, _P, _I64, _I32, _P, _I64, _I64, _I32, _P, _P, _P]),
+    "fp8_mqa_logits_paged": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _I64, _I32, _P,
+                                            _P, _I64, _I64, _I32, _P]),
+    "fp8_mqa_attention_paged_workspace_bytes": (ctypes.c_uint64, [_I32, _I32]),
+    "fp8_mqa_attention_paged": (ctypes.c_int, [_P, _I32, _I64, _I32, _I64, _I64, _P, _P, _P, _I64,
+                                               _I32, _P, _P, _I64, _I32, ctypes.c_float, _P, _P,
+                                               _P, _U64, _P]),
 }
 
 TOPK_MAX_K = 2048
@@ -298,3 +307,7 @@ def fp8_mqa_logits_host(q, k, kv_scale, w, ks, ke, out, workspace: torch.Tensor,
              _stream_ptr(stream, workspace.device))
     if rc != 0:
         raise Fp8MqaError(rc, "fp8_mqa_logits_host")
+
+
+# The paged-cache operators are part of the same namespace.
+from .paged import attention_paged, cache_read, cache_write, logits_paged  # noqa: E402,F401

@@ -1,0 +1,75 @@
+// What the paged-cache kernels share: the device's view of a cache, finding a position's row,
+// and conversions.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+
+namespace fp8mqa {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kTinyMax = 1e-30f;  // the least row maximum that a scale is made from
+
+// A cache as a kernel sees it; data strides in bytes.
+struct PagedView {
+    uint8_t* data;
+    float* scale;
+    int64_t page_stride, row_stride, head_stride;
+    int64_t scale_page_stride, scale_row_stride, scale_head_stride;
+    int32_t pages, page_size, heads;
+};
+
+struct PageTable {
+    const int32_t* ids;
+    int64_t stride;
+    int32_t cols;
+};
+
+// The page and row of position n of sequence b; false if it is not there.
+__device__ __forceinline__ bool locate(const PagedView& c, const PageTable& t, int64_t b, int32_t n,
+                                       int32_t* page, int32_t* row)
+{
+    const int32_t col = int32_t(uint32_t(n) / uint32_t(c.page_size));
+    if (n < 0 || col >= t.cols) return false;
+    *page = __ldg(t.ids + b * t.stride + col);
+    *row = n - col * c.page_size;
+    return uint32_t(*page) < uint32_t(c.pages);
+}
+
+__device__ __forceinline__ float e4m3_to_float(uint8_t v)
+{
+    __nv_fp8_e4m3 x;
+    x.__x = v;
+    return float(x);
+}
+
+template <class T>
+__device__ __forceinline__ float to_float(T x) { return float(x); }
+template <>
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float to_float(__nv_fp8_e4m3 x) { return float(x); }
+
+template <class T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
+
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+}  // namespace fp8mqa

@@ -14,7 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, "fp8_mqa_logits.cu")]
+SOURCES = [os.path.join(CSRC, "fp8_mqa_logits.cu"), os.path.join(CSRC, "paged.cu")]
 LIB = os.path.join(HERE, "libfp8mqa.so")
 # The same library built with FP8MQA_DEBUG_BOUNDS: every global access and TMA coordinate
 # of the kernel is checked first, and a violation is recorded in the status word

@@ -260,6 +260,149 @@ FP8MQA_API int fp8_mqa_topk_ex(const float* logits, int64_t M, int64_t N, int64_
                                const int32_t* ks, const int32_t* ke, int32_t k, int32_t flags,
                                int32_t* indices, float* values, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Paged caches: the operators of a serving step around the logits.  New key and value rows
+ * are quantised into pages as they are written, packed back for a prompt chunk, scored for
+ * the newest tokens straight from the pages, and attended to -- all of them, or the entries
+ * that fp8_mqa_topk selected.
+ *
+ * A cache is `pages` pages of `page_size` token rows of `heads` heads of `dim` values:
+ * element (p, r, h, d) of the data lies at data + p*page_stride + r*row_stride +
+ * h*head_stride + d (in elements; the values of a row are contiguous), and for E4M3 the row's
+ * scale at scale + p*scale_page_stride + r*scale_row_stride + h*scale_head_stride.  An E4M3 row
+ * stands for data * scale.  The strides are free, so keys and values may share one tensor
+ * ([pages, 2, page_size, heads, dim]) and heads may come before rows.
+ *
+ * Position n of sequence b lies in page table[b*table_stride + n / page_size], row
+ * n % page_size.  A table entry outside [0, pages) is a page that is not there: its positions
+ * are never read.  Table entries past a sequence's length are not read either.
+ *
+ * Limits: dim is 64 or 128; data 16-byte aligned with strides of a multiple of 16 bytes;
+ * pages * page_size < 2^31.  Byte offsets are 64-bit throughout.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Element types. */
+#define FP8MQA_E4M3 0
+#define FP8MQA_BF16 1
+#define FP8MQA_F16 2
+#define FP8MQA_F32 3
+
+typedef struct fp8mqa_cache {
+    void* data;          /* DEVICE */
+    float* scale;        /* DEVICE; NULL unless type is FP8MQA_E4M3 */
+    int64_t pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t dim;
+    int32_t type;        /* FP8MQA_E4M3, FP8MQA_BF16 or FP8MQA_F16 */
+    int64_t page_stride, row_stride, head_stride;                    /* elements of data */
+    int64_t scale_page_stride, scale_row_stride, scale_head_stride;  /* elements of scale */
+} fp8mqa_cache;
+
+/*
+ * fp8_mqa_cache_write -- quantises T token rows and writes them into one or two E4M3 caches.
+ *
+ * For each token t and head h, with x its `dim` values in fp32:
+ *     a = max(max_d |x_d|, 1e-30);  data_d = e4m3(x_d * (448 / a));  scale = a * (1 / 448)
+ * each step rounded to fp32, e4m3() to the nearest even, within +-448.  A row that holds a NaN
+ * or an infinity reads back as NaN, so that it does not pass for data.
+ *
+ *   slots    DEVICE int32 [T]: page * page_size + row.  A slot outside [0, pages * page_size)
+ *            is skipped (padding).  Two tokens with one slot: one of them is written whole.
+ *   x        DEVICE [T, heads, dim] of x_type (BF16, F16 or F32), element (t, h, d) at
+ *            t*x_row_stride + h*x_head_stride + d; aligned to its type.
+ *   cache    where x goes.
+ *   x2, cache2   NULL, or a second tensor (values next to keys) of x's type and its cache,
+ *            with cache's page_size, heads and dim and the same slots: one launch writes both.
+ * T = 0 enqueues nothing.  No workspace, no allocation; may be captured into a graph.
+ */
+FP8MQA_API int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const void* x,
+                                   int64_t x_row_stride, int64_t x_head_stride,
+                                   const fp8mqa_cache* cache, const void* x2,
+                                   int64_t x2_row_stride, int64_t x2_head_stride,
+                                   const fp8mqa_cache* cache2, void* stream);
+
+/*
+ * fp8_mqa_cache_read -- packs the rows of B sequences, one after the other, out of an E4M3 cache.
+ *
+ *   table, table_stride, table_cols   DEVICE int32 page table, B rows of table_cols entries.
+ *   starts     DEVICE int32 [B + 1], ascending from 0: sequence b's positions 0, 1, ... go to
+ *              output rows starts[b] .. starts[b + 1] - 1.
+ *   total      output rows (the caller's copy of starts[B]).  Rows past starts[B] are zeroed.
+ *   out        DEVICE [total, heads, dim] of out_type, contiguous, 16-byte aligned:
+ *              FP8MQA_E4M3: the stored values, with their scales in out_scale [total, heads]
+ *              (with heads = 1 the k_fp8 and kv_scale that fp8_mqa_logits takes);
+ *              BF16, F16 or F32: data * scale in fp32, rounded to the type (out_scale is NULL).
+ * Positions on pages that are not there, or past the table, are zero (and their scale).
+ */
+FP8MQA_API int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table,
+                                  int64_t table_stride, int32_t table_cols, const int32_t* starts,
+                                  int64_t B, int64_t total, int32_t out_type, void* out,
+                                  float* out_scale, void* stream);
+
+/*
+ * fp8_mqa_logits_paged -- the indexer logits of each sequence's T newest tokens, from the pages:
+ *
+ *   out[b*T + t, n] = scale[n] * sum_h relu(q[b,t,h,:] . k[n,:]) * w[b,t,h]
+ *                     for n in [0, lens[b] - (T - 1 - t)),   -inf elsewhere (clean_logits = 1)
+ *
+ * with k and scale the rows of sequence b (token t of the T newest sees the cache up to itself).
+ * Positions on pages that are not there are -inf with either clean_logits.
+ *
+ *   q_fp8     DEVICE [B, T, H, D] E4M3, contiguous, 16-byte aligned; H = 32, D = 128.
+ *   w         DEVICE [B, T, H] float32, contiguous, 16-byte aligned.
+ *   keys      the E4M3 cache, heads = 1, dim = 128.
+ *   lens      DEVICE int32 [B]: length with the T newest tokens included; <= 0 is an empty
+ *             sequence.  Lengths are clamped to N and to table_cols * page_size.
+ *   out       DEVICE float32, row r at out + r * ld, N entries a row, 4-byte aligned.
+ *             clean_logits = 0: out-of-window entries are not written.
+ * The result feeds fp8_mqa_topk as it is.  No workspace, no allocation.
+ */
+FP8MQA_API int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_t T,
+                                    int32_t H, int32_t D, const fp8mqa_cache* keys,
+                                    const int32_t* table, int64_t table_stride,
+                                    int32_t table_cols, const int32_t* lens, float* out,
+                                    int64_t ld, int64_t N, int32_t clean_logits, void* stream);
+
+/*
+ * fp8_mqa_attention_paged -- attention of one new token per row over a paged cache:
+ *
+ *   x_n = sm_scale * q[b,h,:] . k[n,g,:],  out[b,h,:] = sum_n softmax(x)_n v[n,g,:],
+ *   lse[b,h] = log sum_n exp(x_n),   g = h / (q_heads / heads)
+ *
+ * over the positions n in [0, lens[b]), or over those that `indices` lists.  Products are
+ * fp32-accumulated; the softmax is fp32; weights are rounded to 16 bits for the second product.
+ * A row with no position: out is 0 and lse is -inf.
+ *
+ *   q         DEVICE [B, q_heads, dim] of q_type (BF16 or F16), element (b, h, d) at
+ *             b*q_row_stride + h*q_head_stride + d; 16-byte aligned, strides too.  q_heads is a
+ *             multiple of the cache's heads.
+ *   k, v      caches of one type, page_size, heads and dim, over one page table: E4M3, or q's type.
+ *   lens      DEVICE int32 [B]; clamped to [0, table_cols * page_size].
+ *   n_indices -1: each row attends to all of its positions.  Otherwise `indices` is DEVICE int32
+ *   indices   with n_indices entries a row, row b at indices + b*indices_stride: the positions that
+ *             row b attends to, for all its heads, in any order; entries outside [0, lens[b]) are
+ *             ignored (the -1 of fp8_mqa_topk's padding), a position listed twice counts twice.
+ *             With a table_stride of 0 the rows share one sequence.
+ *   out       DEVICE [B, q_heads, dim] of q_type, contiguous, 16-byte aligned.
+ *   lse       NULL, or DEVICE float32 [B, q_heads].
+ *   workspace DEVICE, 256-byte aligned, at least fp8_mqa_attention_paged_workspace_bytes(...) bytes;
+ *             its content does not matter before or after the call, and calls that may overlap on
+ *             the GPU need one each.
+ */
+FP8MQA_API int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_heads,
+                                       int64_t q_row_stride, int64_t q_head_stride,
+                                       const fp8mqa_cache* k, const fp8mqa_cache* v,
+                                       const int32_t* table, int64_t table_stride,
+                                       int32_t table_cols, const int32_t* lens,
+                                       const int32_t* indices, int64_t indices_stride,
+                                       int32_t n_indices, float sm_scale, void* out, float* lse,
+                                       void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* fp8_mqa_attention_paged_workspace_bytes -- the workspace of a call with q_heads query heads of
+ * width dim, on the current device (0 when there is none of compute capability 10.3). */
+FP8MQA_API uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t dim);
+
 /* fp8_mqa_logits_strerror -- a static, human-readable name for a status code. */
 FP8MQA_API const char* fp8_mqa_logits_strerror(int status);
 
