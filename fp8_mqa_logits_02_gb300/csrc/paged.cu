@@ -2,6 +2,7 @@
 // checks, the choice of kernel, and the launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <mutex>
@@ -15,11 +16,17 @@ namespace fp8mqa {
 namespace {
 
 constexpr int kPagedMaxDevices = 64;
+// Attention counters: a ring for direct launches, and one of its own for every launch captured
+// into a CUDA graph (a graph's kernel keeps it for every replay).
+constexpr uint32_t kAttnRing = 256, kAttnGraph = 1024;
+
 
 struct PagedDevice {
     std::once_flag once;
     int status = FP8MQA_OK;
     int sm_count = 0;
+    AttnCounters* counters = nullptr;  // kAttnRing + kAttnGraph, zero between launches
+    std::atomic<uint32_t> ring{0}, graph{0};
 };
 
 PagedDevice g_paged[kPagedMaxDevices];
@@ -34,7 +41,19 @@ void init_paged(int dev, PagedDevice& st)
         st.status = FP8MQA_ERR_CUDA;
         return;
     }
-    if (major != 10 || minor != 3) st.status = FP8MQA_ERR_ARCH;
+    if (major != 10 || minor != 3) {
+        st.status = FP8MQA_ERR_ARCH;
+        return;
+    }
+    void* buf = nullptr;
+    const size_t bytes = size_t(kAttnRing + kAttnGraph) * sizeof(AttnCounters);
+    if (cudaMalloc(&buf, bytes) != cudaSuccess || cudaMemset(buf, 0, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        cudaFree(buf);
+        st.status = FP8MQA_ERR_CUDA;
+        return;
+    }
+    st.counters = static_cast<AttnCounters*>(buf);
 }
 
 PagedDevice* paged_device(int* err)
@@ -93,16 +112,66 @@ PagedView view_of(const fp8mqa_cache& c)
     return v;
 }
 
+// The counters of the launch being made, or null with *err set.
+AttnCounters* attention_counters(PagedDevice& st, cudaStream_t s, int* err)
+{
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) {
+        cudaGetLastError();
+        *err = FP8MQA_ERR_CUDA;
+        return nullptr;
+    }
+    if (cap == cudaStreamCaptureStatusNone)
+        return st.counters + st.ring.fetch_add(1, std::memory_order_relaxed) % kAttnRing;
+    const uint32_t i = st.graph.fetch_add(1, std::memory_order_relaxed);
+    if (i >= kAttnGraph) {
+        st.graph.store(kAttnGraph, std::memory_order_relaxed);
+        *err = FP8MQA_ERR_CAPACITY;
+        return nullptr;
+    }
+    return st.counters + kAttnRing + i;
+}
+
+// CTAs of a full wave of the attention kernel: three to an SM at 8 heads, two at 16.
+int64_t attention_wave(int sm_count, int nt)
+{
+    return std::min<int64_t>(kAttnMaxCtas, int64_t(sm_count) * (nt == 1 ? 3 : 2));
+}
+
 int launched() { return cudaGetLastError() == cudaSuccess ? FP8MQA_OK : FP8MQA_ERR_LAUNCH; }
 
-template <class Q, class C>
-void attention_dim(const PagedAttentionParams& p, int32_t dim, cudaStream_t s)
+// CTAs of an attention launch: a full wave, or fewer where there are fewer tiles than that.  A
+// CTA takes 8 heads (three to an SM), or 16 where a group has more than 8 (two to an SM).
+template <int kType, int kDim, int kNT>
+void attention_launch(const PagedAttentionParams& p, int sm_count, cudaStream_t s)
 {
-    const dim3 grid{unsigned(p.q_heads), unsigned(p.B)};
-    if (dim == 64)
-        paged_attention_kernel<Q, C, 64><<<grid, 128, 0, s>>>(p);
+    using S = AttnShape<kType, kDim, kNT>;
+    const int64_t group = p.q_heads / p.k.heads;
+    const int64_t longest =
+        p.n_indices >= 0 ? p.n_indices : int64_t(p.table.cols) * p.k.page_size;
+    const int64_t tiles = p.B * p.k.heads * ((group + S::kHeads - 1) / S::kHeads) *
+                          std::max<int64_t>(1, (longest + S::kTile - 1) / S::kTile);
+    const int64_t wave = attention_wave(sm_count, kNT);
+    const unsigned grid = unsigned(std::min(tiles, wave));
+    paged_attention_kernel<kType, kDim, kNT><<<grid, kAttnThreads, 0, s>>>(p);
+}
+
+template <int kType, int kDim>
+void attention_heads(const PagedAttentionParams& p, int sm_count, cudaStream_t s)
+{
+    if (p.q_heads / p.k.heads <= 8)
+        attention_launch<kType, kDim, 1>(p, sm_count, s);
     else
-        paged_attention_kernel<Q, C, 128><<<grid, 128, 0, s>>>(p);
+        attention_launch<kType, kDim, 2>(p, sm_count, s);
+}
+
+template <int kType>
+void attention_dim(const PagedAttentionParams& p, int32_t dim, int sm_count, cudaStream_t s)
+{
+    if (dim == 64)
+        attention_heads<kType, 64>(p, sm_count, s);
+    else
+        attention_heads<kType, 128>(p, sm_count, s);
 }
 
 }  // namespace
@@ -240,9 +309,15 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
 
 uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t dim)
 {
+    using namespace fp8mqa;
     int err = FP8MQA_OK;
-    if (q_heads < 1 || dim < 1 || !fp8mqa::paged_device(&err)) return 0;
-    return 256;
+    if (q_heads < 1 || dim < 1) return 0;
+    const PagedDevice* st = paged_device(&err);
+    if (!st) return 0;
+    // two partial results a CTA: heads x dim sums, and each head's m and l
+    const uint64_t most = std::max(attention_wave(st->sm_count, 1) * 8,
+                                   attention_wave(st->sm_count, 2) * kAttnMaxHeads);
+    return 2 * most * uint64_t(dim + 2) * sizeof(float);
 }
 
 int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_heads,
@@ -272,7 +347,8 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
         !on(table, 4) || !on(indices, 4) || !on(lse, 4) || !on(workspace, 256))
         return FP8MQA_ERR_MISALIGNED;
     int err = FP8MQA_OK;
-    if (!paged_device(&err)) return err;
+    PagedDevice* st = paged_device(&err);
+    if (!st) return err;
     if (workspace_bytes < fp8_mqa_attention_paged_workspace_bytes(q_heads, k->dim))
         return FP8MQA_ERR_INVALID_ARG;
     PagedAttentionParams p;
@@ -292,18 +368,17 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     p.sm_scale = sm_scale;
     p.out = out;
     p.lse = lse;
+    p.q_bf16 = q_type == FP8MQA_BF16;
+    p.partial = static_cast<float*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (q_type == FP8MQA_BF16) {
-        if (k->type == FP8MQA_E4M3)
-            attention_dim<__nv_bfloat16, __nv_fp8_e4m3>(p, k->dim, s);
-        else
-            attention_dim<__nv_bfloat16, __nv_bfloat16>(p, k->dim, s);
-    } else {
-        if (k->type == FP8MQA_E4M3)
-            attention_dim<__half, __nv_fp8_e4m3>(p, k->dim, s);
-        else
-            attention_dim<__half, __half>(p, k->dim, s);
-    }
+    p.counters = attention_counters(*st, s, &err);
+    if (!p.counters) return err;
+    if (k->type == FP8MQA_E4M3)
+        attention_dim<FP8MQA_E4M3>(p, k->dim, st->sm_count, s);
+    else if (k->type == FP8MQA_BF16)
+        attention_dim<FP8MQA_BF16>(p, k->dim, st->sm_count, s);
+    else
+        attention_dim<FP8MQA_F16>(p, k->dim, st->sm_count, s);
     return launched();
 }
 
