@@ -31,6 +31,22 @@ struct PagedDevice {
 
 PagedDevice g_paged[kPagedMaxDevices];
 
+// CTAs of a full wave of the attention kernel.
+int64_t attention_wave(int sm_count)
+{
+    return std::min<int64_t>(kAttnMaxCtas, int64_t(sm_count) * kAttnCtasPerSm);
+}
+
+template <int kType, int kDim>
+bool attention_smem()
+{
+    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    return cudaFuncSetAttribute(paged_attention_kernel<kType, kDim, 1>, attr,
+                                AttnShape<kType, kDim, 1>::kSmem) == cudaSuccess &&
+           cudaFuncSetAttribute(paged_attention_kernel<kType, kDim, 2>, attr,
+                                AttnShape<kType, kDim, 2>::kSmem) == cudaSuccess;
+}
+
 void init_paged(int dev, PagedDevice& st)
 {
     int major = 0, minor = 0;
@@ -43,6 +59,13 @@ void init_paged(int dev, PagedDevice& st)
     }
     if (major != 10 || minor != 3) {
         st.status = FP8MQA_ERR_ARCH;
+        return;
+    }
+    if (!attention_smem<FP8MQA_E4M3, 64>() || !attention_smem<FP8MQA_E4M3, 128>() ||
+        !attention_smem<FP8MQA_BF16, 64>() || !attention_smem<FP8MQA_BF16, 128>() ||
+        !attention_smem<FP8MQA_F16, 64>() || !attention_smem<FP8MQA_F16, 128>()) {
+        cudaGetLastError();
+        st.status = FP8MQA_ERR_LAUNCH;
         return;
     }
     void* buf = nullptr;
@@ -132,16 +155,10 @@ AttnCounters* attention_counters(PagedDevice& st, cudaStream_t s, int* err)
     return st.counters + kAttnRing + i;
 }
 
-// CTAs of a full wave of the attention kernel: three to an SM at 8 heads, two at 16.
-int64_t attention_wave(int sm_count, int nt)
-{
-    return std::min<int64_t>(kAttnMaxCtas, int64_t(sm_count) * (nt == 1 ? 3 : 2));
-}
-
 int launched() { return cudaGetLastError() == cudaSuccess ? FP8MQA_OK : FP8MQA_ERR_LAUNCH; }
 
 // CTAs of an attention launch: a full wave, or fewer where there are fewer tiles than that.  A
-// CTA takes 8 heads (three to an SM), or 16 where a group has more than 8 (two to an SM).
+// CTA takes 8 heads, or 16 where a group has more than 8.
 template <int kType, int kDim, int kNT>
 void attention_launch(const PagedAttentionParams& p, int sm_count, cudaStream_t s)
 {
@@ -151,9 +168,8 @@ void attention_launch(const PagedAttentionParams& p, int sm_count, cudaStream_t 
         p.n_indices >= 0 ? p.n_indices : int64_t(p.table.cols) * p.k.page_size;
     const int64_t tiles = p.B * p.k.heads * ((group + S::kHeads - 1) / S::kHeads) *
                           std::max<int64_t>(1, (longest + S::kTile - 1) / S::kTile);
-    const int64_t wave = attention_wave(sm_count, kNT);
-    const unsigned grid = unsigned(std::min(tiles, wave));
-    paged_attention_kernel<kType, kDim, kNT><<<grid, kAttnThreads, 0, s>>>(p);
+    const unsigned grid = unsigned(std::min(tiles, attention_wave(sm_count)));
+    paged_attention_kernel<kType, kDim, kNT><<<grid, kAttnThreads, S::kSmem, s>>>(p);
 }
 
 template <int kType, int kDim>
@@ -315,9 +331,8 @@ uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t dim)
     const PagedDevice* st = paged_device(&err);
     if (!st) return 0;
     // two partial results a CTA: heads x dim sums, and each head's m and l
-    const uint64_t most = std::max(attention_wave(st->sm_count, 1) * 8,
-                                   attention_wave(st->sm_count, 2) * kAttnMaxHeads);
-    return 2 * most * uint64_t(dim + 2) * sizeof(float);
+    return 2 * uint64_t(attention_wave(st->sm_count)) * kAttnMaxHeads * uint64_t(dim + 2) *
+           sizeof(float);
 }
 
 int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_heads,

@@ -3,15 +3,19 @@
 //   x_n = sm_scale * q . k_n,   out = sum_n softmax(x)_n v_n,   lse = log sum_n exp(x_n)
 //
 // Bound: every cached row is read once and used by the few query heads of its group, 4 flops a
-// value and head, so the bytes of the cache decide.  The kernel therefore keeps the cache's bytes
-// in flight and out of shared memory: a warp takes kStep positions at a time, and its lanes load
-// the rows straight into the registers that the matrix instructions read them from.
+// value and head, so the bytes of the cache decide.  What counts is bytes in flight: each warp
+// copies its positions' rows asynchronously into a ring of its own in shared memory, kAttnStages
+// steps of kStep positions, and reads matrix fragments from it.  (Loads straight into the fragments'
+// registers left the kernel waiting for memory: 6.4 of 10 warp-cycles, 3.1 TB/s.)
 //
 //   S^T [positions x heads] = K Q^T   A = K rows as they lie, B = Q^T.  The contraction runs over
 //       dim in any order that K and Q share, so lane (g, t) takes 16-byte pieces of row g.
 //   O^T [dim x heads] += V^T P^T      A = V^T, B = P^T.  The rows of O^T may come in any order, so
 //       lane (g, t) takes the g-th piece of four rows and interleaves them by byte permutes; P^T is
 //       S^T's accumulator transposed 8 x 8 by 8 x 8.
+//
+// The pieces of a row are permuted in the ring so that both ways of reading are free of bank
+// conflicts.
 //
 // (g = lane / 4, t = lane % 4: the lane's row and column in an m16n8k16 fragment.)  Eight heads
 // fill a fragment, so a group's heads are taken 8 or 16 at a time.
@@ -30,10 +34,13 @@
 #include <math_constants.h>
 
 #include "paged_common.cuh"
+#include "sm103_ptx.cuh"
 
 namespace fp8mqa {
 
 constexpr int kAttnThreads = 128, kAttnWarps = kAttnThreads / 32;
+constexpr int kAttnStages = 2;     // steps in a warp's ring
+constexpr int kAttnCtasPerSm = 3;
 constexpr int kAttnMaxCtas = 512;  // of one launch
 constexpr int kAttnFan = 16;       // partial results joined at a time
 constexpr int kAttnMaxHeads = 16;  // heads a CTA takes at a time
@@ -72,9 +79,17 @@ struct AttnShape {
     static constexpr int kTile = kStep * kAttnWarps;
     static constexpr int kBlocks = kStep / 16;         // of 16 positions
     static constexpr int kRowBytes = kDim * (kE4m3 ? 1 : 2);
-    static constexpr int kKRows = kStep / 8, kKWords = kRowBytes / 16;  // per lane
-    static constexpr int kVRows = kStep / 4, kVWords = kRowBytes / 32;
+    static constexpr int kPieces = kRowBytes / 16;
+    static constexpr int kKRows = kStep / 8;           // rows of S^T a lane has
+    static constexpr int kVWords = kRowBytes / 32;     // words of a V row a lane has
     static constexpr int kMT = kDim / 16;              // 16-blocks of dim
+    // a ring stage: K rows, V rows, their scales, and which rows are there
+    static constexpr int kRows = kStep * kRowBytes;
+    static constexpr int kScales = 2 * kRows, kThere = kScales + (kE4m3 ? 2 * kStep * 4 : 0);
+    static constexpr int kStage = (kThere + 16 + 127) / 128 * 128;
+    static constexpr int kRing = kAttnStages * kStage;
+    static constexpr int kSmem = kAttnWarps * kRing;
+    static_assert(kHeads * kDim * 4 <= kRing, "the warps' results take the rings' place");
 };
 
 __device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t two)
@@ -126,19 +141,37 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi)
     return r;
 }
 
-// Streaming loads of a cache row's piece: read once, not kept in L1.
-template <int kWords>
-__device__ __forceinline__ void load_piece(uint32_t* w, const uint8_t* p)
+// Asynchronous copies into shared memory; what is not there is filled with zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
 {
-    static_assert(kWords == 2 || kWords == 4, "8 or 16 bytes");
-    if constexpr (kWords == 4)
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "l"(p));
-    else
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-                     : "=r"(w[0]), "=r"(w[1])
-                     : "l"(p));
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// Where piece c of row r lies in a stage.  A fragment read of K takes four pieces of two rows in
+// a phase, one of V two pieces of every second of eight rows.
+template <int kPieces>
+__device__ __forceinline__ int k_place(int r, int c)
+{
+    return r * kPieces + (kPieces >= 8 ? c ^ ((r & 1) << 2) : c);
+}
+template <int kPieces>
+__device__ __forceinline__ int v_place(int r, int c)
+{
+    return r * kPieces + (kPieces >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
 }
 
 // Where the rows' tiles lie: row b's tiles, `chunks` units of tiles(b) each, start at
@@ -187,11 +220,11 @@ __device__ __forceinline__ void attn_join(const float* o, const float* ml, int n
 }
 
 template <int kType, int kDim, int kNT>
-__global__ void __launch_bounds__(kAttnThreads, kNT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     paged_attention_kernel(const __grid_constant__ PagedAttentionParams p)
 {
     using S = AttnShape<kType, kDim, kNT>;
-    __shared__ __align__(16) float s_o[kAttnWarps][S::kHeads][kDim];
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_ml[kAttnWarps][S::kHeads][2];
     __shared__ int64_t s_scan[kAttnThreads];
     __shared__ int64_t s_first[2];  // the first row of this CTA, and the tiles before it
@@ -201,6 +234,8 @@ __global__ void __launch_bounds__(kAttnThreads, kNT == 1 ? 3 : 2)
     const int group = p.q_heads / p.k.heads;
     const int parts = (group + S::kHeads - 1) / S::kHeads;  // head chunks of a group
     const int chunks = p.k.heads * parts;
+    uint8_t* const ring = smem + warp * S::kRing;
+    const uint32_t ring_at = ptx::smem_addr(ring);
     const AttnRows<S> rows{p, int64_t(p.table.cols) * p.k.page_size};
 
     // ---- this CTA's share of the tiles
@@ -332,75 +367,79 @@ __global__ void __launch_bounds__(kAttnThreads, kNT == 1 ? 3 : 2)
         }
         int32_t v_exp = 1;  // value scales are taken relative to 2^(v_exp - 127)
 
-        // ---- a step's rows: lane i knows position i of the step; -1: not there
+        // ---- a step's rows: lane i finds position i of a step, a step ahead of its copies
         const uint8_t* const k_base = p.k.data + kvh * p.k.head_stride;
         const uint8_t* const v_base = p.v.data + kvh * p.v.head_stride;
         const int32_t step_end = min(count, hi * S::kTile);
-        int64_t k_at = -1, v_at = -1;
-        float k_by = 0.0f, v_by = 0.0f;
-        auto find = [&](int32_t i) {  // i: this lane's place in the row's list
-            int32_t n = i;
-            k_at = v_at = -1;
-            k_by = v_by = S::kE4m3 ? 0.0f : 1.0f;
+        const int mine = lane % S::kStep;
+        int32_t page = -1, row = 0;
+        auto find = [&](int32_t i) {  // i: the step's first place in the row's list
+            page = -1;
+            i += mine;
             if (i < step_end) {
+                int32_t n = i;
                 if (p.n_indices >= 0) n = __ldg(p.indices + b * p.indices_stride + i);
-                int32_t page, row;
-                if (n >= 0 && n < len && locate(p.k, p.table, b, n, &page, &row)) {
-                    k_at = page * p.k.page_stride + row * p.k.row_stride;
-                    v_at = page * p.v.page_stride + row * p.v.row_stride;
-                    if (S::kE4m3) {
-                        k_by = __ldg(p.k.scale + page * p.k.scale_page_stride +
-                                     row * p.k.scale_row_stride + kvh * p.k.scale_head_stride);
-                        v_by = __ldg(p.v.scale + page * p.v.scale_page_stride +
-                                     row * p.v.scale_row_stride + kvh * p.v.scale_head_stride);
-                    }
-                }
+                if (!(n >= 0 && n < len && locate(p.k, p.table, b, n, &page, &row))) page = -1;
             }
         };
-        uint32_t kw[S::kKRows][S::kKWords], vw[S::kVRows][S::kVWords];
-        auto load_k = [&] {
+        auto copy = [&](int stage) {  // the rows that find() found
+            const bool there = page >= 0;
+            const int64_t k_at = there ? page * p.k.page_stride + row * p.k.row_stride : -1;
+            const int64_t v_at = there ? page * p.v.page_stride + row * p.v.row_stride : -1;
+            const uint32_t to = ring_at + stage * S::kStage;
+            constexpr int kPer = 32 / S::kPieces;  // rows in one instruction
+            const int c = lane % S::kPieces;
 #pragma unroll
-            for (int r = 0; r < S::kKRows; ++r) {
-                const int64_t off = __shfl_sync(~0u, k_at, r * 8 + g);
-#pragma unroll
-                for (int j = 0; j < S::kKWords / 4; ++j) {
-                    if (off >= 0) {
-                        load_piece<4>(&kw[r][4 * j], k_base + off + j * 64 + t * 16);
-                    } else {
-                        kw[r][4 * j] = kw[r][4 * j + 1] = kw[r][4 * j + 2] = kw[r][4 * j + 3] = 0u;
-                    }
-                }
+            for (int j = 0; j < S::kStep / kPer; ++j) {
+                const int r = j * kPer + lane / S::kPieces;
+                const int64_t off = __shfl_sync(~0u, k_at, r);
+                copy16(to + 16 * k_place<S::kPieces>(r, c), k_base + (off < 0 ? 0 : off) + 16 * c,
+                       off >= 0);
             }
-        };
-        auto load_v = [&] {
-            constexpr int kPiece = S::kVWords < 4 ? S::kVWords : 4;
 #pragma unroll
-            for (int r = 0; r < S::kVRows; ++r) {
-                const int key = r / 4 * 16 + r / 2 % 2 * 8 + 2 * t + r % 2;
-                const int64_t off = __shfl_sync(~0u, v_at, key);
-#pragma unroll
-                for (int j = 0; j < S::kVWords / kPiece; ++j) {
-                    if (off >= 0) {
-                        load_piece<kPiece>(&vw[r][kPiece * j],
-                                           v_base + off + j * 128 + g * (4 * kPiece));
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < kPiece; ++x) vw[r][kPiece * j + x] = 0u;
-                    }
-                }
+            for (int j = 0; j < S::kStep / kPer; ++j) {
+                const int r = j * kPer + lane / S::kPieces;
+                const int64_t off = __shfl_sync(~0u, v_at, r);
+                copy16(to + S::kRows + 16 * v_place<S::kPieces>(r, c),
+                       v_base + (off < 0 ? 0 : off) + 16 * c, off >= 0);
             }
+            if constexpr (S::kE4m3) {
+                const int64_t pg = there ? page : 0, rw = there ? row : 0;
+                copy4(to + S::kScales + 4 * lane,
+                      p.k.scale + pg * p.k.scale_page_stride + rw * p.k.scale_row_stride +
+                          kvh * p.k.scale_head_stride,
+                      there);
+                copy4(to + S::kScales + 4 * (S::kStep + lane),
+                      p.v.scale + pg * p.v.scale_page_stride + rw * p.v.scale_row_stride +
+                          kvh * p.v.scale_head_stride,
+                      there);
+            }
+            const uint32_t here = __ballot_sync(~0u, there);
+            if (lane == 0) *reinterpret_cast<uint32_t*>(ring + stage * S::kStage + S::kThere) = here;
         };
 
-        int32_t i0 = lo * S::kTile + warp * S::kStep;
-        const int mine = lane % S::kStep;
-        if (i0 < step_end) {
-            find(i0 + mine);
-            load_k();
+        int32_t i0 = lo * S::kTile + warp * S::kStep;  // the step being computed
+        int32_t ahead = i0;                            // the step that find() found
+        find(ahead);
+#pragma unroll
+        for (int j = 0; j < kAttnStages - 1; ++j) {
+            if (ahead < step_end) {
+                copy(j);
+                find(ahead += S::kTile);
+            }
+            copy_commit();
         }
-        for (; i0 < step_end; i0 += S::kTile) {
-            load_v();
-            const float ks = k_by, vs = v_by;
-            const bool there = k_at >= 0;
+        for (int stage = 0; i0 < step_end; i0 += S::kTile, stage = (stage + 1) % kAttnStages) {
+            if (ahead < step_end) {
+                copy((stage + kAttnStages - 1) % kAttnStages);
+                find(ahead += S::kTile);
+            }
+            copy_commit();
+            copy_wait<kAttnStages - 1>();
+            __syncwarp();
+            const uint8_t* const at_k = ring + stage * S::kStage;
+            const uint8_t* const at_v = at_k + S::kRows;
+            const uint32_t here = *reinterpret_cast<const uint32_t*>(at_k + S::kThere);
 
             // ---- scores
             float x[kNT][S::kBlocks][4];
@@ -413,39 +452,44 @@ __global__ void __launch_bounds__(kAttnThreads, kNT == 1 ? 3 : 2)
 #pragma unroll
             for (int mb = 0; mb < S::kBlocks; ++mb)
 #pragma unroll
-                for (int s = 0; s < S::kMT; ++s) {
-                    uint32_t a0, a1, a2, a3;
-                    if constexpr (S::kE4m3) {
-                        const uint32_t w0 = kw[2 * mb][s], w1 = kw[2 * mb + 1][s];
-                        a0 = f16_of_e4m3(w0);
-                        a1 = f16_of_e4m3(w1);
-                        a2 = f16_of_e4m3(w0 >> 16);
-                        a3 = f16_of_e4m3(w1 >> 16);
-                    } else {
-                        a0 = kw[2 * mb][2 * s];
-                        a1 = kw[2 * mb + 1][2 * s];
-                        a2 = kw[2 * mb][2 * s + 1];
-                        a3 = kw[2 * mb + 1][2 * s + 1];
-                    }
+                for (int j = 0; j < S::kPieces / 4; ++j) {
+                    const int r = 16 * mb + g;
+                    const uint4 x0 = *reinterpret_cast<const uint4*>(
+                        at_k + 16 * k_place<S::kPieces>(r, 4 * j + t));
+                    const uint4 x1 = *reinterpret_cast<const uint4*>(
+                        at_k + 16 * k_place<S::kPieces>(r + 8, 4 * j + t));
+                    const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w};
+                    const uint32_t w1[4] = {x1.x, x1.y, x1.z, x1.w};
+                    constexpr int kSteps = S::kE4m3 ? 4 : 2;  // 16 columns of dim each
 #pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt)
-                        mma16816<S::kBf16>(x[nt][mb], a0, a1, a2, a3, qf[nt][s][0], qf[nt][s][1]);
+                    for (int y = 0; y < kSteps; ++y) {
+                        const int s = j * kSteps + y;
+                        uint32_t a0, a1, a2, a3;
+                        if constexpr (S::kE4m3) {
+                            a0 = f16_of_e4m3(w0[y]);
+                            a1 = f16_of_e4m3(w1[y]);
+                            a2 = f16_of_e4m3(w0[y] >> 16);
+                            a3 = f16_of_e4m3(w1[y] >> 16);
+                        } else {
+                            a0 = w0[2 * y];
+                            a1 = w1[2 * y];
+                            a2 = w0[2 * y + 1];
+                            a3 = w1[2 * y + 1];
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < kNT; ++nt)
+                            mma16816<S::kBf16>(x[nt][mb], a0, a1, a2, a3, qf[nt][s][0], qf[nt][s][1]);
+                    }
                 }
-
-            // ---- the next step's keys
-            if (i0 + S::kTile < step_end) {
-                find(i0 + S::kTile + mine);
-                load_k();
-            }
 
             // ---- softmax: this lane has positions 8r + g, heads 2t and 2t + 1
             float row_vs[S::kKRows];
-            const uint32_t here = __ballot_sync(~0u, there);
+            const float* const scales = reinterpret_cast<const float*>(at_k + S::kScales);
 #pragma unroll
             for (int r = 0; r < S::kKRows; ++r) {
-                const float row_ks = S::kE4m3 ? __shfl_sync(~0u, ks, r * 8 + g) : 1.0f;
+                const float row_ks = S::kE4m3 ? scales[r * 8 + g] : 1.0f;
+                row_vs[r] = S::kE4m3 ? scales[S::kStep + r * 8 + g] : 1.0f;
                 const bool ok = here >> (r * 8 + g) & 1u;
-                row_vs[r] = S::kE4m3 ? __shfl_sync(~0u, vs, r * 8 + g) : 1.0f;
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -457,7 +501,8 @@ __global__ void __launch_bounds__(kAttnThreads, kNT == 1 ? 3 : 2)
             float c_v = 1.0f, v_inv = 1.0f;
             bool moved = false;
             if constexpr (S::kE4m3) {
-                const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(vs) & 0x7FFFFFFFu);
+                const uint32_t top =
+                    __reduce_max_sync(~0u, __float_as_uint(scales[S::kStep + lane]) & 0x7FFFFFFFu);
                 const int32_t e = min(max(int32_t(top >> 23), v_exp), 253);
                 if (e > v_exp) {
                     c_v = exp2_fast(float(v_exp - e));
@@ -509,7 +554,27 @@ __global__ void __launch_bounds__(kAttnThreads, kNT == 1 ? 3 : 2)
                     pf[nt][0] = transpose8(pack16<S::kBf16>(x[nt][mb][0], x[nt][mb][1]));
                     pf[nt][1] = transpose8(pack16<S::kBf16>(x[nt][mb][2], x[nt][mb][3]));
                 }
-                const uint32_t(*w)[S::kVWords] = &vw[4 * mb];
+                uint32_t w[4][S::kVWords];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int key = 16 * mb + r / 2 * 8 + 2 * t + r % 2;
+                    if constexpr (S::kVWords == 2) {
+                        const uint2 y = *reinterpret_cast<const uint2*>(
+                            at_v + 16 * v_place<S::kPieces>(key, g / 2) + g % 2 * 8);
+                        w[r][0] = y.x;
+                        w[r][1] = y.y;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < S::kVWords / 4; ++j) {
+                            const uint4 y = *reinterpret_cast<const uint4*>(
+                                at_v + 16 * v_place<S::kPieces>(key, 8 * j + g));
+                            w[r][4 * j] = y.x;
+                            w[r][4 * j + 1] = y.y;
+                            w[r][4 * j + 2] = y.z;
+                            w[r][4 * j + 3] = y.w;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < S::kMT; ++i) {
                     uint32_t a0, a1, a2, a3;
@@ -532,11 +597,12 @@ __global__ void __launch_bounds__(kAttnThreads, kNT == 1 ? 3 : 2)
                         mma16816<S::kBf16>(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
                 }
             }
+            __syncwarp();  // the stage may be filled again
         }
 
         // ---- the warps' results, joined in shared memory
         const float v_back = S::kE4m3 ? __uint_as_float(uint32_t(v_exp) << 23) : 1.0f;
-        __syncthreads();  // the last segment's reads of s_o are done
+        float* const s_o = reinterpret_cast<float*>(ring);  // [heads][dim], where the ring was
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -554,8 +620,8 @@ __global__ void __launch_bounds__(kAttnThreads, kNT == 1 ? 3 : 2)
                 for (int i = 0; i < S::kMT; ++i) {
                     const int d = S::kE4m3 ? g * (kDim / 8) + 2 * i
                                            : i / 4 * 64 + g * 8 + 2 * i % 8;
-                    s_o[warp][h][d] = o[nt][i][j] * v_back;
-                    s_o[warp][h][d + 1] = o[nt][i][2 + j] * v_back;
+                    s_o[h * kDim + d] = o[nt][i][j] * v_back;
+                    s_o[h * kDim + d + 1] = o[nt][i][2 + j] * v_back;
                 }
             }
         __syncthreads();
@@ -587,7 +653,7 @@ __global__ void __launch_bounds__(kAttnThreads, kNT == 1 ? 3 : 2)
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
                 const float f = exp2_fast(s_ml[w][h][0] - ref);
-                const float4 y = reinterpret_cast<const float4*>(&s_o[w][0][0])[i];
+                const float4 y = reinterpret_cast<const float4*>(smem + w * S::kRing)[i];
                 sum = fmaf(f, s_ml[w][h][1], sum);
                 v.x = fmaf(f, y.x, v.x);
                 v.y = fmaf(f, y.y, v.y);
@@ -651,6 +717,7 @@ __global__ void __launch_bounds__(kAttnThreads, kNT == 1 ? 3 : 2)
             }
         }
         at = unit_start + hi;
+        __syncthreads();  // the results are read: the rings may be filled again
     }
 }
 
