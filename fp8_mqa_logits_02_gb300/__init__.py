@@ -62,7 +62,7 @@ SIGNATURES = {
     "fp8_mqa_cache_read": (ctypes.c_int, [_P, _P, _I64, _I32, _P, _I64, _I64, _I32, _P, _P, _P]),
     "fp8_mqa_logits_paged": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _I64, _I32, _P,
                                             _P, _I64, _I64, _I32, _P]),
-    "fp8_mqa_attention_paged_workspace_bytes": (ctypes.c_uint64, [_I32, _I32]),
+    "fp8_mqa_attention_paged_workspace_bytes": (ctypes.c_uint64, [_I32, _I32, _I32]),
     "fp8_mqa_attention_paged": (ctypes.c_int, [_P, _I32, _I64, _I32, _I64, _I64, _P, _P, _P, _I64,
                                                _I32, _P, _P, _I64, _I32, ctypes.c_float, _P, _P,
                                                _P, _U64, _P]),

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cstdint>
 #include <mutex>
+#include <numeric>
 
 #include "../../include/fp8_mqa_logits.h"
 #include "cache_kernels.cuh"
@@ -16,17 +17,11 @@ namespace fp8mqa {
 namespace {
 
 constexpr int kPagedMaxDevices = 64;
-// Attention counters: a ring for direct launches, and one of its own for every launch captured
-// into a CUDA graph (a graph's kernel keeps it for every replay).
-constexpr uint32_t kAttnRing = 256, kAttnGraph = 1024;
-
 
 struct PagedDevice {
     std::once_flag once;
     int status = FP8MQA_OK;
     int sm_count = 0;
-    AttnCounters* counters = nullptr;  // kAttnRing + kAttnGraph, zero between launches
-    std::atomic<uint32_t> ring{0}, graph{0};
 };
 
 PagedDevice g_paged[kPagedMaxDevices];
@@ -68,15 +63,6 @@ void init_paged(int dev, PagedDevice& st)
         st.status = FP8MQA_ERR_LAUNCH;
         return;
     }
-    void* buf = nullptr;
-    const size_t bytes = size_t(kAttnRing + kAttnGraph) * sizeof(AttnCounters);
-    if (cudaMalloc(&buf, bytes) != cudaSuccess || cudaMemset(buf, 0, bytes) != cudaSuccess) {
-        cudaGetLastError();
-        cudaFree(buf);
-        st.status = FP8MQA_ERR_CUDA;
-        return;
-    }
-    st.counters = static_cast<AttnCounters*>(buf);
 }
 
 PagedDevice* paged_device(int* err)
@@ -135,45 +121,66 @@ PagedView view_of(const fp8mqa_cache& c)
     return v;
 }
 
-// The counters of the launch being made, or null with *err set.
-AttnCounters* attention_counters(PagedDevice& st, cudaStream_t s, int* err)
+// The units that a cache's rows are counted in; false if 32 bits do not hold them.
+bool row_units(const PagedView& v, RowUnits* u)
 {
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) {
-        cudaGetLastError();
-        *err = FP8MQA_ERR_CUDA;
-        return nullptr;
-    }
-    if (cap == cudaStreamCaptureStatusNone)
-        return st.counters + st.ring.fetch_add(1, std::memory_order_relaxed) % kAttnRing;
-    const uint32_t i = st.graph.fetch_add(1, std::memory_order_relaxed);
-    if (i >= kAttnGraph) {
-        st.graph.store(kAttnGraph, std::memory_order_relaxed);
-        *err = FP8MQA_ERR_CAPACITY;
-        return nullptr;
-    }
-    return st.counters + kAttnRing + i;
+    // strides of dimensions of one do not count; negative ones are not taken
+    const int64_t page = v.pages > 1 ? v.page_stride : 0, row = v.page_size > 1 ? v.row_stride : 0;
+    const int64_t unit = std::max<int64_t>(16, std::gcd(page, row));
+    if (page < 0 || row < 0 || unit > INT32_MAX ||
+        (v.pages * page + v.page_size * row) / unit >= int64_t(kNoRow))
+        return false;
+    u->page = uint32_t(page / unit);
+    u->row = uint32_t(row / unit);
+    u->unit = uint32_t(unit);
+    return true;
 }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? FP8MQA_OK : FP8MQA_ERR_LAUNCH; }
 
-// CTAs of an attention launch: a full wave, or fewer where there are fewer tiles than that.  A
-// CTA takes 8 heads, or 16 where a group has more than 8.
+// Key heads that a CTA's warps take: side by side (up to four) where a CTA gets kAttnHeadTiles
+// tiles or more that way, else one, with four steps of its positions (fewer partial results).
+// Measured: 90 tiles a CTA (64 rows of up to 20001, 8 heads) 230 us side by side, 244 one by one;
+// 19 (16 rows of up to 16385, 4 heads, 16 bits) 62.6 and 60.5; 9 (64 rows of 2048 selected) 53 and 48.
+constexpr int64_t kAttnHeadTiles = 32;
+
+// A CTA takes 8 query heads of each key head, or 16 where a group has more than 8; the grid is a
+// full wave, or fewer where there are fewer tiles, and a multiple of the chunks of heads.
 template <int kType, int kDim, int kNT>
-void attention_launch(const PagedAttentionParams& p, int sm_count, cudaStream_t s)
+void attention_launch(PagedAttentionParams& p, int sm_count, cudaStream_t s)
 {
     using S = AttnShape<kType, kDim, kNT>;
-    const int64_t group = p.q_heads / p.k.heads;
+    const int64_t group = p.q_heads / p.k.heads, parts = (group + S::kHeads - 1) / S::kHeads;
+    const int64_t wave = attention_wave(sm_count);
     const int64_t longest =
-        p.n_indices >= 0 ? p.n_indices : int64_t(p.table.cols) * p.k.page_size;
-    const int64_t tiles = p.B * p.k.heads * ((group + S::kHeads - 1) / S::kHeads) *
-                          std::max<int64_t>(1, (longest + S::kTile - 1) / S::kTile);
-    const unsigned grid = unsigned(std::min(tiles, attention_wave(sm_count)));
-    paged_attention_kernel<kType, kDim, kNT><<<grid, kAttnThreads, S::kSmem, s>>>(p);
+        std::max<int64_t>(1, p.n_indices >= 0 ? p.n_indices : int64_t(p.table.cols) * p.k.page_size);
+    p.hw = p.k.heads % 4 == 0 ? 4 : p.k.heads % 2 == 0 ? 2 : 1;
+    int64_t tile, chunks, tiles;
+    for (;; p.hw = 1) {
+        tile = S::kStep * (kAttnWarps / p.hw);
+        chunks = p.k.heads / p.hw * parts;
+        tiles = p.B * ((longest + tile - 1) / tile);
+        if (p.hw == 1 || tiles * chunks >= kAttnHeadTiles * wave) break;
+    }
+    const int64_t per_chunk = std::min(tiles, std::max<int64_t>(1, wave / chunks));
+    paged_attention_kernel<kType, kDim, kNT>
+        <<<unsigned(per_chunk * chunks), kAttnThreads, S::kSmem, s>>>(p);
+    if (per_chunk == 1) return;  // nothing is split
+    // the join is set up while the first kernel runs
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(per_chunk - 1), unsigned(chunks * p.hw * kNT));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, paged_attention_join_kernel<kDim>, p, S::kHeads, int(per_chunk));
 }
 
 template <int kType, int kDim>
-void attention_heads(const PagedAttentionParams& p, int sm_count, cudaStream_t s)
+void attention_heads(PagedAttentionParams& p, int sm_count, cudaStream_t s)
 {
     if (p.q_heads / p.k.heads <= 8)
         attention_launch<kType, kDim, 1>(p, sm_count, s);
@@ -182,7 +189,7 @@ void attention_heads(const PagedAttentionParams& p, int sm_count, cudaStream_t s
 }
 
 template <int kType>
-void attention_dim(const PagedAttentionParams& p, int32_t dim, int sm_count, cudaStream_t s)
+void attention_dim(PagedAttentionParams& p, int32_t dim, int sm_count, cudaStream_t s)
 {
     if (dim == 64)
         attention_heads<kType, 64>(p, sm_count, s);
@@ -323,16 +330,19 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
     return launched();
 }
 
-uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t dim)
+uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t dim)
 {
     using namespace fp8mqa;
     int err = FP8MQA_OK;
-    if (q_heads < 1 || dim < 1) return 0;
+    if (q_heads < 1 || kv_heads < 1 || dim < 1) return 0;
     const PagedDevice* st = paged_device(&err);
     if (!st) return 0;
-    // two partial results a CTA: heads x dim sums, and each head's m and l
-    return 2 * uint64_t(attention_wave(st->sm_count)) * kAttnMaxHeads * uint64_t(dim + 2) *
-           sizeof(float);
+    // two partial results a CTA (heads x dim sums, and each head's m and l); a launch with more
+    // chunks of heads than a wave has CTAs splits no row
+    const uint64_t heads = uint64_t(kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1) *
+                           (q_heads / kv_heads <= 8 ? 8 : kAttnMaxHeads);
+    return kAttnMaxCtas * sizeof(AttnSplit) +
+           2 * uint64_t(attention_wave(st->sm_count)) * heads * uint64_t(dim + 2) * sizeof(float);
 }
 
 int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_heads,
@@ -364,7 +374,7 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     int err = FP8MQA_OK;
     PagedDevice* st = paged_device(&err);
     if (!st) return err;
-    if (workspace_bytes < fp8_mqa_attention_paged_workspace_bytes(q_heads, k->dim))
+    if (workspace_bytes < fp8_mqa_attention_paged_workspace_bytes(q_heads, k->heads, k->dim))
         return FP8MQA_ERR_INVALID_ARG;
     PagedAttentionParams p;
     p.q = q;
@@ -373,6 +383,9 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     p.k = view_of(*k);
     p.v = view_of(*v);
     p.k.pages = p.v.pages = p.k.pages < p.v.pages ? p.k.pages : p.v.pages;
+    if (!row_units(p.k, &p.k_units) || !row_units(p.v, &p.v_units))
+        return FP8MQA_ERR_UNSUPPORTED_SHAPE;
+    p.same_rows = p.k_units.page == p.v_units.page && p.k_units.row == p.v_units.row;
     p.table = {table, table_stride, table_cols};
     p.lens = lens;
     p.indices = indices;
@@ -384,10 +397,9 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     p.out = out;
     p.lse = lse;
     p.q_bf16 = q_type == FP8MQA_BF16;
-    p.partial = static_cast<float*>(workspace);
+    p.splits = static_cast<AttnSplit*>(workspace);
+    p.partial = reinterpret_cast<float*>(p.splits + kAttnMaxCtas);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    p.counters = attention_counters(*st, s, &err);
-    if (!p.counters) return err;
     if (k->type == FP8MQA_E4M3)
         attention_dim<FP8MQA_E4M3>(p, k->dim, st->sm_count, s);
     else if (k->type == FP8MQA_BF16)

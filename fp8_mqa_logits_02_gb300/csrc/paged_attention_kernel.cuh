@@ -25,10 +25,14 @@
 // unrounded); their value scales are taken relative to a running power of two, so the largest
 // keep their 11 bits whatever the scales' size.
 //
-// Split and join: the rows' tiles (four warps' steps) are laid end to end, and every CTA takes an
-// equal share of them.  A unit (row and head chunk) that lies in one CTA is finished there; the
-// others' partial (m, l, O) go to the workspace, and the last CTA of each group of kFan to arrive
-// joins the group, then the last group's CTA the groups, always in the same order.
+// A CTA's four warps take hw heads (1, 2 or 4) of the same positions, 4 / hw steps of positions
+// each, and keep in step: the heads of a position lie side by side in memory, and reading them
+// together is what DRAM wants.
+//
+// Split and join: for each chunk of heads the rows' tiles (the CTA's steps) are laid end to end,
+// and its CTAs take equal shares of them; the CTAs of one share number follow one another in the
+// grid.  A row that lies in one CTA is finished there; the others' partial (m, l, O) go to the
+// workspace, and a second kernel joins them, always in the same order.
 #pragma once
 
 #include <math_constants.h>
@@ -42,18 +46,22 @@ constexpr int kAttnThreads = 128, kAttnWarps = kAttnThreads / 32;
 constexpr int kAttnStages = 2;     // steps in a warp's ring
 constexpr int kAttnCtasPerSm = 3;
 constexpr int kAttnMaxCtas = 512;  // of one launch
-constexpr int kAttnFan = 16;       // partial results joined at a time
-constexpr int kAttnMaxHeads = 16;  // heads a CTA takes at a time
-// One launch's arrival counters (zero between launches): a group's and a unit's, by the first
-// member's partial slot (two a CTA).
-struct AttnCounters {
-    int32_t group[2 * kAttnMaxCtas], unit[2 * kAttnMaxCtas];
+constexpr int kAttnMaxHeads = 16;  // query heads of a key head that a CTA takes
+
+// What CTA `me` of a chunk (me > 0) says of the row that its share begins within: the row's parts
+// are those of CTAs first .. first + parts - 1.  parts = 0: its share begins with a row.
+struct AttnSplit {
+    int64_t row;
+    int32_t first, parts, first_slot, pad[3];
 };
 
 struct PagedAttentionParams {
     const void* q;
     int64_t q_row_stride, q_head_stride;  // elements
     PagedView k, v;
+    RowUnits k_units, v_units;
+    int32_t same_rows;  // k_units and v_units are alike
+    int32_t hw;         // key heads that a CTA's warps take: 1, 2 or 4
     PageTable table;
     const int32_t* lens;
     const int32_t* indices;
@@ -65,8 +73,8 @@ struct PagedAttentionParams {
     float sm_scale;
     void* out;
     float* lse;
-    float* partial;  // [2 * CTAs][heads][dim], then m and l [2 * CTAs][heads][2]
-    AttnCounters* counters;
+    float* partial;  // [2 * CTAs][heads of a CTA][dim], then m and l [2 * CTAs][heads of a CTA][2]
+    AttnSplit* splits;  // [CTAs of a chunk]
 };
 
 // kType: FP8MQA_E4M3, FP8MQA_BF16 or FP8MQA_F16 of the cache.
@@ -76,7 +84,6 @@ struct AttnShape {
     static constexpr int kDim = kDim_, kNT = kNT_;
     static constexpr int kHeads = 8 * kNT;             // heads of a unit
     static constexpr int kStep = kE4m3 ? 32 : 16;      // positions of a warp's step
-    static constexpr int kTile = kStep * kAttnWarps;
     static constexpr int kBlocks = kStep / 16;         // of 16 positions
     static constexpr int kRowBytes = kDim * (kE4m3 ? 1 : 2);
     static constexpr int kPieces = kRowBytes / 16;
@@ -174,12 +181,11 @@ __device__ __forceinline__ int v_place(int r, int c)
     return r * kPieces + (kPieces >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
 }
 
-// Where the rows' tiles lie: row b's tiles, `chunks` units of tiles(b) each, start at
-// chunks * (tiles of the rows before it).
-template <class S>
+// The rows' positions and tiles.
 struct AttnRows {
     const PagedAttentionParams& p;
     int64_t cap;
+    int32_t tile;  // positions
     __device__ int32_t count(int64_t b) const
     {
         if (p.n_indices >= 0) return p.n_indices;
@@ -187,36 +193,24 @@ struct AttnRows {
         return int32_t(n < 0 ? 0 : n < cap ? n : cap);
     }
     // a row with nothing still has one tile, which writes its empty result
-    __device__ int32_t tiles(int64_t b) const { return max(1, (count(b) + S::kTile - 1) / S::kTile); }
+    __device__ int32_t tiles(int64_t b) const { return max(1, (count(b) + tile - 1) / tile); }
 };
 
-// Combines n partial results (slots slot(0) .. slot(n - 1)) of a unit's heads; each thread gets
-// float4 number i of [heads][dim / 4] with its head's m and l.
-template <class S, class Slot, class Use>
-__device__ __forceinline__ void attn_join(const float* o, const float* ml, int n, Slot slot, Use use)
+// Writes float4 number i of a head's result, given the running maximum and sum.
+template <int kDim>
+__device__ __forceinline__ void attn_store(const PagedAttentionParams& p, int64_t head, int i,
+                                           float top, float sum, float4 v)
 {
-    for (int i = threadIdx.x; i < S::kHeads * S::kDim / 4; i += kAttnThreads) {
-        const int h = i / (S::kDim / 4);
-        float top = -CUDART_INF_F;
-        for (int k = 0; k < n; ++k) top = fmaxf(top, __ldcg(ml + (slot(k) * S::kHeads + h) * 2));
-        float l = 0.0f;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float ref = top == -CUDART_INF_F ? 0.0f : top;
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const int64_t at = slot(k);
-            const float2 a = __ldcg(reinterpret_cast<const float2*>(ml) + at * S::kHeads + h);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(o) +
-                                    at * (S::kHeads * S::kDim / 4) + i);
-            const float f = exp2_fast(a.x - ref);
-            l = fmaf(f, a.y, l);
-            sum.x = fmaf(f, x.x, sum.x);
-            sum.y = fmaf(f, x.y, sum.y);
-            sum.z = fmaf(f, x.z, sum.z);
-            sum.w = fmaf(f, x.w, sum.w);
-        }
-        use(i, h, top, l, sum);
-    }
+    if (4 * i >= kDim) return;
+    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+    uint2 two;
+    if (p.q_bf16)
+        two = make_uint2(pack16<true>(v.x * inv, v.y * inv), pack16<true>(v.z * inv, v.w * inv));
+    else
+        two = make_uint2(pack16<false>(v.x * inv, v.y * inv), pack16<false>(v.z * inv, v.w * inv));
+    static_cast<uint2*>(p.out)[head * (kDim / 4) + i] = two;
+    if (p.lse && i == 0)
+        p.lse[head] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int kType, int kDim, int kNT>
@@ -226,151 +220,107 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     using S = AttnShape<kType, kDim, kNT>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_ml[kAttnWarps][S::kHeads][2];
-    __shared__ int64_t s_scan[kAttnThreads];
+    __shared__ int64_t s_scan[kAttnWarps];
     __shared__ int64_t s_first[2];  // the first row of this CTA, and the tiles before it
-    __shared__ int32_t s_last;
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int group = p.q_heads / p.k.heads;
     const int parts = (group + S::kHeads - 1) / S::kHeads;  // head chunks of a group
-    const int chunks = p.k.heads * parts;
+    const int hw = p.hw, chunks = p.k.heads / hw * parts;
+    const int chunk = blockIdx.x % chunks;
+    const int me = blockIdx.x / chunks;                      // of the chunk's CTAs
+    const int kvh = chunk / parts * hw + warp % hw;          // this warp's key head
+    const int part0 = chunk % parts * S::kHeads;             // its first query head of the group
+    const int n_heads = min(S::kHeads, group - part0);
+    const int all_heads = hw * S::kHeads;                    // of the CTA, with the empty ones
+    const int tile = S::kStep * (kAttnWarps / hw);           // positions
     uint8_t* const ring = smem + warp * S::kRing;
     const uint32_t ring_at = ptx::smem_addr(ring);
-    const AttnRows<S> rows{p, int64_t(p.table.cols) * p.k.page_size};
+    const AttnRows rows{p, int64_t(p.table.cols) * p.k.page_size, tile};
 
-    // ---- this CTA's share of the tiles
-    int64_t total;  // tiles of all rows, for one chunk
+    asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this kernel's end
+
+    // ---- this CTA's share of the tiles (each thread counts those of some consecutive rows)
+    const int64_t per = (p.B + kAttnThreads - 1) / kAttnThreads;
+    int64_t total, before = 0, mine_sum = 0;  // tiles of all rows, of those before mine, of mine
     if (p.n_indices >= 0) {
         total = p.B * rows.tiles(0);
     } else {
-        const int64_t per = (p.B + kAttnThreads - 1) / kAttnThreads;
-        const int64_t b0 = min(per * tid, p.B), b1 = min(b0 + per, p.B);
-        int64_t sum = 0;
-        for (int64_t b = b0; b < b1; ++b) sum += rows.tiles(b);
-        s_scan[tid] = sum;
-        __syncthreads();
-        for (int o = 1; o < kAttnThreads; o *= 2) {
-            const int64_t x = tid >= o ? s_scan[tid - o] : 0;
-            __syncthreads();
-            s_scan[tid] += x;
-            __syncthreads();
+        const int64_t b1 = min(per * (tid + 1), p.B);
+        for (int64_t b = per * tid; b < b1; ++b) mine_sum += rows.tiles(b);
+        int64_t scan = mine_sum;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t x = __shfl_up_sync(~0u, scan, o);
+            if (lane >= o) scan += x;
         }
-        total = s_scan[kAttnThreads - 1];
+        if (lane == 31) s_scan[warp] = scan;
+        __syncthreads();
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            if (w == warp) before = total + scan - mine_sum;
+            total += s_scan[w];
+        }
     }
-    const int64_t all = total * chunks;
-    const int64_t ctas = min(int64_t(gridDim.x), all);
-    if (blockIdx.x >= ctas) return;
-    const int64_t first = blockIdx.x * all / ctas, end = (blockIdx.x + 1) * all / ctas;
+    const int64_t ctas = min(int64_t(gridDim.x / chunks), total);
+    if (me >= ctas) {
+        if (chunk == 0 && tid == 0) p.splits[me].parts = 0;
+        return;
+    }
+    const int64_t first = me * total / ctas, end = (me + 1) * total / ctas;
     if (p.n_indices >= 0) {
         if (tid == 0) {
             const int64_t n = rows.tiles(0);
-            s_first[0] = first / (n * chunks);
-            s_first[1] = s_first[0] * n * chunks;
+            s_first[0] = first / n;
+            s_first[1] = first / n * n;
         }
-    } else {
-        const int64_t per = (p.B + kAttnThreads - 1) / kAttnThreads;
-        int64_t before = (tid ? s_scan[tid - 1] : 0) * chunks;
-        if (before <= first && first < s_scan[tid] * chunks) {
-            int64_t b = per * tid;
-            for (;; ++b) {
-                const int64_t n = int64_t(rows.tiles(b)) * chunks;
-                if (first < before + n) break;
-                before += n;
-            }
-            s_first[0] = b;
-            s_first[1] = before;
+    } else if (before <= first && first < before + mine_sum) {
+        int64_t b = per * tid, at = before;
+        for (;; ++b) {
+            const int64_t n = rows.tiles(b);
+            if (first < at + n) break;
+            at += n;
         }
+        s_first[0] = b;
+        s_first[1] = at;
     }
     __syncthreads();
     int64_t b = s_first[0], row_start = s_first[1];
 
     float* const part_o = p.partial;
-    float* const part_ml = p.partial + int64_t(2) * gridDim.x * S::kHeads * kDim;
+    float* const part_ml = p.partial + int64_t(2) * gridDim.x * all_heads * kDim;
 
-    for (int64_t at = first; at < end;) {
-        // ---- one segment: tiles [lo, hi) of unit (b, chunk)
+    for (int64_t at = first; at < end; ++b) {
+        // ---- one segment: tiles [lo, hi) of row b
         const int32_t count = rows.count(b), n_tiles = rows.tiles(b);
-        if (at >= row_start + int64_t(n_tiles) * chunks) {
-            row_start += int64_t(n_tiles) * chunks;
-            ++b;
-            continue;
-        }
-        const int chunk = int((at - row_start) / n_tiles);
-        const int64_t unit_start = row_start + int64_t(chunk) * n_tiles;
-        const int32_t lo = int32_t(at - unit_start);
-        const int32_t hi = int32_t(min(int64_t(n_tiles), end - unit_start));
-        const int kvh = chunk / parts, h0 = kvh * group + (chunk % parts) * S::kHeads;
-        const int n_heads = min(S::kHeads, (kvh + 1) * group - h0);
+        const int32_t lo = int32_t(at - row_start);
+        const int32_t hi = int32_t(min(int64_t(n_tiles), end - row_start));
+        const int h0 = kvh * group + part0;
         const int32_t len = int32_t(min(int64_t(max(__ldg(p.lens + b), 0)), rows.cap));
 
-        // ---- Q as B fragments, and each head's factor of the scores (in powers of two)
+        // ---- Q: the words of this lane's columns, two values each
         uint32_t qf[kNT][S::kMT][2];
-        float factor[kNT][2], m[kNT][2], l[kNT][2], o[kNT][S::kMT][4];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             const int h = nt * 8 + g;
             const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.q_row_stride +
                                 int64_t(h0 + h) * p.q_head_stride;
-            // the words of this lane's columns, two values each
-            uint32_t raw[S::kMT][2];
 #pragma unroll
             for (int s = 0; s < S::kMT; ++s)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int d = S::kE4m3 ? s / 4 * 64 + t * 16 + s % 4 * 4 + 2 * j
                                            : (2 * s + j) / 4 * 32 + t * 8 + (2 * s + j) % 4 * 2;
-                    raw[s][j] = h < n_heads
-                                    ? __ldg(reinterpret_cast<const uint32_t*>(q + d))
-                                    : 0u;
+                    qf[nt][s][j] = h < n_heads ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
                 }
-            float by = 1.0f;
-            if (S::kE4m3 && p.q_bf16) {
-                // bfloat16 -> f16: exact but for the range, so each head is brought to a largest
-                // magnitude of 2^12 .. 2^13 by a power of two (what then falls below f16's range
-                // is under 2^-36 of the largest)
-                float top = 0.0f;
-#pragma unroll
-                for (int s = 0; s < S::kMT; ++s)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        top = fmaxf(top, fabsf(__uint_as_float(raw[s][j] << 16)));
-                        top = fmaxf(top, fabsf(__uint_as_float(raw[s][j] & 0xFFFF0000u)));
-                    }
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                const int e = min(max(int(__float_as_uint(top) >> 23), 20), 240) - 139;
-                const float down = __uint_as_float(uint32_t(127 - e) << 23);
-                by = __uint_as_float(uint32_t(127 + e) << 23);
-#pragma unroll
-                for (int s = 0; s < S::kMT; ++s)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        raw[s][j] = pack16<false>(__uint_as_float(raw[s][j] << 16) * down,
-                                                  __uint_as_float(raw[s][j] & 0xFFFF0000u) * down);
-            }
-#pragma unroll
-            for (int s = 0; s < S::kMT; ++s)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) qf[nt][s][j] = raw[s][j];
-            const float c = p.sm_scale * 1.4426950408889634f * by;
-            factor[nt][0] = __shfl_sync(~0u, c, 8 * t);
-            factor[nt][1] = __shfl_sync(~0u, c, 8 * t + 4);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                m[nt][j] = -CUDART_INF_F;
-                l[nt][j] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < S::kMT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
         }
         int32_t v_exp = 1;  // value scales are taken relative to 2^(v_exp - 127)
 
         // ---- a step's rows: lane i finds position i of a step, a step ahead of its copies
         const uint8_t* const k_base = p.k.data + kvh * p.k.head_stride;
         const uint8_t* const v_base = p.v.data + kvh * p.v.head_stride;
-        const int32_t step_end = min(count, hi * S::kTile);
+        const int32_t step_end = min(count, hi * tile);
         const int mine = lane % S::kStep;
         int32_t page = -1, row = 0;
         auto find = [&](int32_t i) {  // i: the step's first place in the row's list
@@ -384,24 +334,21 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         };
         auto copy = [&](int stage) {  // the rows that find() found
             const bool there = page >= 0;
-            const int64_t k_at = there ? page * p.k.page_stride + row * p.k.row_stride : -1;
-            const int64_t v_at = there ? page * p.v.page_stride + row * p.v.row_stride : -1;
+            const uint32_t k_at = there ? page * p.k_units.page + row * p.k_units.row : kNoRow;
+            const uint32_t v_at = there ? page * p.v_units.page + row * p.v_units.row : kNoRow;
             const uint32_t to = ring_at + stage * S::kStage;
             constexpr int kPer = 32 / S::kPieces;  // rows in one instruction
             const int c = lane % S::kPieces;
 #pragma unroll
             for (int j = 0; j < S::kStep / kPer; ++j) {
                 const int r = j * kPer + lane / S::kPieces;
-                const int64_t off = __shfl_sync(~0u, k_at, r);
-                copy16(to + 16 * k_place<S::kPieces>(r, c), k_base + (off < 0 ? 0 : off) + 16 * c,
-                       off >= 0);
-            }
-#pragma unroll
-            for (int j = 0; j < S::kStep / kPer; ++j) {
-                const int r = j * kPer + lane / S::kPieces;
-                const int64_t off = __shfl_sync(~0u, v_at, r);
+                const uint32_t at = __shfl_sync(~0u, k_at, r);
+                const uint32_t at2 = p.same_rows ? at : __shfl_sync(~0u, v_at, r);
+                const bool ok = at != kNoRow;
+                copy16(to + 16 * k_place<S::kPieces>(r, c),
+                       k_base + uint64_t(ok ? at : 0) * p.k_units.unit + 16 * c, ok);
                 copy16(to + S::kRows + 16 * v_place<S::kPieces>(r, c),
-                       v_base + (off < 0 ? 0 : off) + 16 * c, off >= 0);
+                       v_base + uint64_t(ok ? at2 : 0) * p.v_units.unit + 16 * c, ok);
             }
             if constexpr (S::kE4m3) {
                 const int64_t pg = there ? page : 0, rw = there ? row : 0;
@@ -418,21 +365,69 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             if (lane == 0) *reinterpret_cast<uint32_t*>(ring + stage * S::kStage + S::kThere) = here;
         };
 
-        int32_t i0 = lo * S::kTile + warp * S::kStep;  // the step being computed
-        int32_t ahead = i0;                            // the step that find() found
+        int32_t i0 = lo * tile + warp / hw * S::kStep;  // the step being computed
+        int32_t ahead = i0;                             // the step that find() found
         find(ahead);
 #pragma unroll
         for (int j = 0; j < kAttnStages - 1; ++j) {
             if (ahead < step_end) {
                 copy(j);
-                find(ahead += S::kTile);
+                find(ahead += tile);
             }
             copy_commit();
         }
-        for (int stage = 0; i0 < step_end; i0 += S::kTile, stage = (stage + 1) % kAttnStages) {
+
+        // ---- Q as B fragments, and each head's factor of the scores (in powers of two)
+        float factor[kNT][2], m[kNT][2], l[kNT][2], o[kNT][S::kMT][4];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+            float by = 1.0f;
+            if (S::kE4m3 && p.q_bf16) {
+                // bfloat16 -> f16: exact but for the range, so each head is brought to a largest
+                // magnitude of 2^12 .. 2^13 by a power of two (what then falls below f16's range
+                // is under 2^-36 of the largest)
+                float top = 0.0f;
+#pragma unroll
+                for (int s = 0; s < S::kMT; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        top = fmaxf(top, fabsf(__uint_as_float(qf[nt][s][j] << 16)));
+                        top = fmaxf(top, fabsf(__uint_as_float(qf[nt][s][j] & 0xFFFF0000u)));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                const int e = min(max(int(__float_as_uint(top) >> 23), 20), 240) - 139;
+                const float down = __uint_as_float(uint32_t(127 - e) << 23);
+                by = __uint_as_float(uint32_t(127 + e) << 23);
+#pragma unroll
+                for (int s = 0; s < S::kMT; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        qf[nt][s][j] =
+                            pack16<false>(__uint_as_float(qf[nt][s][j] << 16) * down,
+                                          __uint_as_float(qf[nt][s][j] & 0xFFFF0000u) * down);
+            }
+            const float c = p.sm_scale * 1.4426950408889634f * by;
+            factor[nt][0] = __shfl_sync(~0u, c, 8 * t);
+            factor[nt][1] = __shfl_sync(~0u, c, 8 * t + 4);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                m[nt][j] = -CUDART_INF_F;
+                l[nt][j] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < S::kMT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
+        }
+
+        for (int stage = 0, t_left = hi - lo; t_left > 0;
+             --t_left, i0 += tile, stage = (stage + 1) % kAttnStages) {
+            if (hw > 1) __syncthreads();  // the heads' copies go out together
+            if (i0 >= step_end) continue;
             if (ahead < step_end) {
                 copy((stage + kAttnStages - 1) % kAttnStages);
-                find(ahead += S::kTile);
+                find(ahead += tile);
             }
             copy_commit();
             copy_wait<kAttnStages - 1>();
@@ -625,35 +620,25 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                 }
             }
         __syncthreads();
-        auto finish = [&](int i, int h, float top, float sum, float4 v) {
+        auto finish = [&](int i, int hh, float top, float sum, float4 v) {
+            const int h = hh % S::kHeads;
             if (h >= n_heads) return;
-            const int64_t head = b * p.q_heads + h0 + h;
-            const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-            const int64_t at4 = head * (kDim / 4) + i % (kDim / 4);
-            uint2 two;
-            if (p.q_bf16)
-                two = make_uint2(pack16<true>(v.x * inv, v.y * inv), pack16<true>(v.z * inv, v.w * inv));
-            else
-                two = make_uint2(pack16<false>(v.x * inv, v.y * inv), pack16<false>(v.z * inv, v.w * inv));
-            static_cast<uint2*>(p.out)[at4] = two;
-            if (p.lse && i % (kDim / 4) == 0)
-                p.lse[head] = sum == 0.0f ? -CUDART_INF_F
-                                          : (top + log2f(sum)) * 0.6931471805599453f;
+            const int64_t head =
+                b * p.q_heads + (chunk / parts * hw + hh / S::kHeads) * group + part0 + h;
+            attn_store<kDim>(p, head, i % (kDim / 4), top, sum, v);
         };
         const bool whole = lo == 0 && hi == n_tiles;
         const int64_t slot = 2 * int64_t(blockIdx.x) + (at == first ? 0 : 1);
-        for (int i = tid; i < S::kHeads * kDim / 4; i += kAttnThreads) {
-            const int h = i / (kDim / 4);
+        for (int i = tid; i < all_heads * (kDim / 4); i += kAttnThreads) {
+            const int hh = i / (kDim / 4), h = hh % S::kHeads;
             float top = -CUDART_INF_F;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, s_ml[w][h][0]);
+            for (int w = hh / S::kHeads; w < kAttnWarps; w += hw) top = fmaxf(top, s_ml[w][h][0]);
             const float ref = top == -CUDART_INF_F ? 0.0f : top;
             float sum = 0.0f;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
+            for (int w = hh / S::kHeads; w < kAttnWarps; w += hw) {
                 const float f = exp2_fast(s_ml[w][h][0] - ref);
-                const float4 y = reinterpret_cast<const float4*>(smem + w * S::kRing)[i];
+                const float4 y = reinterpret_cast<const float4*>(smem + w * S::kRing)[i % (S::kHeads * (kDim / 4))];
                 sum = fmaf(f, s_ml[w][h][1], sum);
                 v.x = fmaf(f, y.x, v.x);
                 v.y = fmaf(f, y.y, v.y);
@@ -661,63 +646,127 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                 v.w = fmaf(f, y.w, v.w);
             }
             if (whole) {
-                finish(i, h, top, sum, v);
+                finish(i, hh, top, sum, v);
             } else {
-                reinterpret_cast<float4*>(part_o)[slot * (S::kHeads * kDim / 4) + i] = v;
+                reinterpret_cast<float4*>(part_o)[slot * (all_heads * (kDim / 4)) + i] = v;
                 if (i % (kDim / 4) == 0)
-                    reinterpret_cast<float2*>(part_ml)[slot * S::kHeads + h] = make_float2(top, sum);
+                    reinterpret_cast<float2*>(part_ml)[slot * all_heads + hh] = make_float2(top, sum);
             }
         }
 
-        // ---- the CTAs' results, joined by whoever arrives last
-        if (!whole) {
-            // the unit's CTAs are p0 .. p1; the first one's part is its last segment
-            const int64_t p0 = ((unit_start + 1) * ctas - 1) / all;
-            const int64_t p1 = ((unit_start + n_tiles) * ctas - 1) / all;
-            const int n = int(p1 - p0) + 1, me = int(blockIdx.x - p0);
-            const int64_t slot0 = 2 * p0 + (p0 * all / ctas == unit_start ? 0 : 1);
-            auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (p0 + k); };
-            auto arrive = [&](int32_t* counter, int expected) {  // true in the last CTA to arrive
-                __threadfence();
-                __syncthreads();
-                if (tid == 0) {
-                    const bool last = atomicAdd(counter, 1) == expected - 1;
-                    if (last) *counter = 0;
-                    s_last = last;
+        // ---- what the second kernel has to know of this row
+        if (at == first && chunk == 0 && tid == 0 && me > 0) {
+            AttnSplit split;
+            split.row = b;
+            split.first = int32_t(((row_start + 1) * ctas - 1) / total);
+            split.parts = lo == 0 ? 0 : int32_t(((row_start + n_tiles) * ctas - 1) / total) - split.first + 1;
+            split.first_slot = split.first * total / ctas == row_start ? 0 : 1;
+            p.splits[me] = split;
+        }
+        at = row_start += hi;
+        __syncthreads();  // the results are read: the rings may be filled again
+    }
+}
+
+// Joins the rows that several CTAs took.  Block (e, k) stands for 8 query heads (k) of share e + 1:
+// the row that the share begins within has `parts` shares, so parts - 1 such blocks, which divide the
+// 8 heads among them; a head's partial results are divided among the block's warps.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+
+template <int kDim>
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_attention_join_kernel(const __grid_constant__ PagedAttentionParams p, int heads, int ctas)
+{
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+    __shared__ __align__(16) float s_o[kJoinWarps][kDim];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int group = p.q_heads / p.k.heads, parts = (group + heads - 1) / heads;
+    const int chunks = p.k.heads / p.hw * parts, all_heads = p.hw * heads;
+    const int chunk = blockIdx.y * 8 / all_heads, first_head = blockIdx.y * 8 % all_heads;
+    const int me = blockIdx.x + 1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const AttnSplit split = p.splits[me];
+    if (split.parts == 0) return;
+    const int n = split.parts, helpers = min(n - 1, 8), helper = me - split.first - 1;
+    if (helper >= helpers) return;
+    const int mine = 8 / helpers + (helper < 8 % helpers);  // heads, helper + j * helpers
+    // a power of two of heads at a time, the warps shared out among them
+    const int at_once = mine >= 8 ? 8 : mine >= 4 ? 4 : mine >= 2 ? 2 : 1, share = kJoinWarps / at_once;
+    const float* const part_ml = p.partial + int64_t(2) * ctas * chunks * all_heads * kDim;
+    for (int j0 = 0; j0 < mine; j0 += at_once) {
+        const int j = j0 + warp / share, r = warp % share;
+        const int hh = first_head + helper + j * helpers;
+        float m = -CUDART_INF_F, l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (j < mine) {
+            constexpr int kBatch = 8;
+            for (int k0 = r; k0 < n; k0 += share * kBatch) {
+                float2 ml[kBatch];
+                float4 x[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int k = k0 + i * share;
+                    ml[i] = make_float2(-CUDART_INF_F, 0.0f);
+                    x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (k < n) {
+                        const int64_t slot = 2 * (int64_t(split.first + k) * chunks + chunk) +
+                                             (k == 0 ? split.first_slot : 0);
+                        ml[i] = __ldcg(reinterpret_cast<const float2*>(part_ml) + slot * all_heads + hh);
+                        if (4 * lane < kDim)
+                            x[i] = __ldcg(reinterpret_cast<const float4*>(
+                                              p.partial + (slot * all_heads + hh) * kDim) + lane);
+                    }
                 }
-                __syncthreads();
-                const bool last = s_last;
-                if (last) __threadfence();
-                return last;
-            };
-            const int groups = (n + kAttnFan - 1) / kAttnFan;
-            const int k0 = me / kAttnFan * kAttnFan, members = min(kAttnFan, n - k0);
-            if (arrive(&p.counters->group[slot_of(k0)], members)) {
-                if (groups == 1) {
-                    attn_join<S>(part_o, part_ml, n, slot_of, finish);
-                } else {
-                    // the group's sum takes its first member's place
-                    const int64_t to = slot_of(k0);
-                    float2 ml[S::kHeads * kDim / 4 / kAttnThreads];
-                    int c = 0;
-                    attn_join<S>(part_o, part_ml, members, [&](int k) { return slot_of(k0 + k); },
-                                 [&](int i, int, float top, float sum, float4 v) {
-                                     reinterpret_cast<float4*>(part_o)[to * (S::kHeads * kDim / 4) + i] = v;
-                                     ml[c++] = make_float2(top, sum);
-                                 });
-                    __syncthreads();  // every thread has read the first member's m and l
-                    c = 0;
-                    for (int i = tid; i < S::kHeads * kDim / 4; i += kAttnThreads, ++c)
-                        if (i % (kDim / 4) == 0)
-                            reinterpret_cast<float2*>(part_ml)[to * S::kHeads + i / (kDim / 4)] = ml[c];
-                    if (arrive(&p.counters->unit[slot0], groups))
-                        attn_join<S>(part_o, part_ml, groups,
-                                     [&](int k) { return slot_of(k * kAttnFan); }, finish);
+                float top = m;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+                const float ref = top == -CUDART_INF_F ? 0.0f : top, c = exp2_fast(m - ref);
+                l *= c;
+                o.x *= c;
+                o.y *= c;
+                o.z *= c;
+                o.w *= c;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const float f = exp2_fast(ml[i].x - ref);
+                    l = fmaf(f, ml[i].y, l);
+                    o.x = fmaf(f, x[i].x, o.x);
+                    o.y = fmaf(f, x[i].y, o.y);
+                    o.z = fmaf(f, x[i].z, o.z);
+                    o.w = fmaf(f, x[i].w, o.w);
                 }
+                m = top;
             }
         }
-        at = unit_start + hi;
-        __syncthreads();  // the results are read: the rings may be filled again
+        __syncthreads();
+        if (lane == 0) {
+            s_m[warp] = m;
+            s_l[warp] = l;
+        }
+        if (4 * lane < kDim) reinterpret_cast<float4*>(s_o[warp])[lane] = o;
+        __syncthreads();
+        const int h = hh % heads, part0 = chunk % parts * heads;
+        if (j < mine && r == 0 && h < min(heads, group - part0)) {
+            float top = -CUDART_INF_F;
+            for (int w = warp; w < warp + share; ++w) top = fmaxf(top, s_m[w]);
+            const float ref = top == -CUDART_INF_F ? 0.0f : top;
+            l = 0.0f;
+            o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int w = warp; w < warp + share; ++w) {
+                const float f = exp2_fast(s_m[w] - ref);
+                l = fmaf(f, s_l[w], l);
+                if (4 * lane < kDim) {
+                    const float4 x = reinterpret_cast<const float4*>(s_o[w])[lane];
+                    o.x = fmaf(f, x.x, o.x);
+                    o.y = fmaf(f, x.y, o.y);
+                    o.z = fmaf(f, x.z, o.z);
+                    o.w = fmaf(f, x.w, o.w);
+                }
+            }
+            const int64_t head =
+                split.row * p.q_heads + (chunk / parts * p.hw + hh / heads) * group + part0 + h;
+            attn_store<kDim>(p, head, lane, top, l, o);
+        }
     }
 }
 

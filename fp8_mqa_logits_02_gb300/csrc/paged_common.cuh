@@ -28,6 +28,14 @@ struct PageTable {
     int32_t cols;
 };
 
+// A row's place in a cache as a 32-bit number of units of `unit` bytes (a common divisor of the
+// page and row strides), so that lanes can hand it to one another in one shuffle.
+struct RowUnits {
+    uint32_t page, row;  // units a page and a row
+    uint32_t unit;       // bytes
+};
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+
 // The page and row of position n of sequence b; false if it is not there.
 __device__ __forceinline__ bool locate(const PagedView& c, const PageTable& t, int64_t b, int32_t n,
                                        int32_t* page, int32_t* row)

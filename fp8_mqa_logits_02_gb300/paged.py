@@ -226,7 +226,7 @@ def attention_paged(q: torch.Tensor, k_data: torch.Tensor, v_data: torch.Tensor,
         at, by, n = indices.data_ptr(), indices.stride(0), indices.shape[1]
     out = _empty((B, heads, dim), q.dtype, dev, stream)
     lse = _empty((B, heads), torch.float32, dev, stream) if return_lse else None
-    need = _on(dev, _entry("fp8_mqa_attention_paged_workspace_bytes"), heads, dim)
+    need = _on(dev, _entry("fp8_mqa_attention_paged_workspace_bytes"), heads, shape[2], dim)
     space = _empty((need,), torch.uint8, dev, stream)
     _call("fp8_mqa_attention_paged", dev, stream, q.data_ptr(), _TYPE[q.dtype], B, heads,
           q.stride(0), q.stride(1), k, v, table.data_ptr(), table.stride(0), table.shape[1],

@@ -278,7 +278,9 @@ FP8MQA_API int fp8_mqa_topk_ex(const float* logits, int64_t M, int64_t N, int64_
  * are never read.  Table entries past a sequence's length are not read either.
  *
  * Limits: dim is 64 or 128; data 16-byte aligned with strides of a multiple of 16 bytes;
- * pages * page_size < 2^31.  Byte offsets are 64-bit throughout.
+ * pages * page_size < 2^31; strides are not negative.  Byte offsets are 64-bit throughout;
+ * fp8_mqa_attention_paged counts a cache's rows in units of the greatest common divisor of its
+ * page and row strides, of which a cache may span up to 2^32 - 2 (64 GB even at 16 bytes).
  * ------------------------------------------------------------------------------------------ */
 
 /* Element types. */
@@ -399,9 +401,11 @@ FP8MQA_API int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B,
                                        int32_t n_indices, float sm_scale, void* out, float* lse,
                                        void* workspace, uint64_t workspace_bytes, void* stream);
 
-/* fp8_mqa_attention_paged_workspace_bytes -- the workspace of a call with q_heads query heads of
- * width dim, on the current device (0 when there is none of compute capability 10.3). */
-FP8MQA_API uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t dim);
+/* fp8_mqa_attention_paged_workspace_bytes -- the workspace of a call with q_heads query
+ * and kv_heads key heads of width dim, on the current device (0 when there is none of compute
+ * capability 10.3).  It does not depend on the rows or their lengths. */
+FP8MQA_API uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t kv_heads,
+                                                            int32_t dim);
 
 /* fp8_mqa_logits_strerror -- a static, human-readable name for a status code. */
 FP8MQA_API const char* fp8_mqa_logits_strerror(int status);
