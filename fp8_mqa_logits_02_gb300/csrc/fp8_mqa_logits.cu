@@ -15,6 +15,7 @@
 
 #include "../../include/fp8_mqa_logits.h"
 #include "logits_kernel.cuh"
+#include "paged_host.h"
 #include "topk_kernel.cuh"
 
 namespace fp8mqa {
@@ -470,6 +471,9 @@ int launch_noalloc(const uint8_t* q, const uint8_t* k, const float* kv, const fl
 }
 
 }  // namespace
+
+uint64_t wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
+
 }  // namespace fp8mqa
 
 extern "C" {
@@ -571,6 +575,7 @@ int fp8_mqa_logits_check_error(void* stream)
         !fp8mqa::take_status(reinterpret_cast<int32_t*>(na.scratch + fp8mqa::kNoAllocStatusOffset),
                              &flags))
         return FP8MQA_ERR_CUDA;
+    if (!fp8mqa::paged_take_status(dev, &flags)) return FP8MQA_ERR_CUDA;
     if (flags & fp8mqa::kStatusBounds) return FP8MQA_ERR_BOUNDS;
     if (flags & fp8mqa::kStatusTimeout) return FP8MQA_ERR_TIMEOUT;
     return FP8MQA_OK;

@@ -11,6 +11,7 @@
 #include "../../include/fp8_mqa_logits.h"
 #include "cache_kernels.cuh"
 #include "paged_attention_kernel.cuh"
+#include "paged_host.h"
 #include "paged_logits_kernel.cuh"
 
 namespace fp8mqa {
@@ -20,11 +21,19 @@ constexpr int kPagedMaxDevices = 64;
 
 struct PagedDevice {
     std::once_flag once;
-    int status = FP8MQA_OK;
+    int init_status = FP8MQA_OK;
     int sm_count = 0;
+    int32_t* status = nullptr;  // status word of the paged logits
+    std::atomic<bool> ready{false};
 };
 
 PagedDevice g_paged[kPagedMaxDevices];
+template <int kTok>
+bool logits_smem()
+{
+    return cudaFuncSetAttribute(paged_logits_kernel<kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                int(PagedShape<kTok>::kSmem)) == cudaSuccess;
+}
 
 // CTAs of a full wave of the attention kernel.
 int64_t attention_wave(int sm_count)
@@ -49,20 +58,30 @@ void init_paged(int dev, PagedDevice& st)
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&st.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         cudaGetLastError();
-        st.status = FP8MQA_ERR_CUDA;
+        st.init_status = FP8MQA_ERR_CUDA;
         return;
     }
     if (major != 10 || minor != 3) {
-        st.status = FP8MQA_ERR_ARCH;
+        st.init_status = FP8MQA_ERR_ARCH;
         return;
     }
     if (!attention_smem<FP8MQA_E4M3, 64>() || !attention_smem<FP8MQA_E4M3, 128>() ||
         !attention_smem<FP8MQA_BF16, 64>() || !attention_smem<FP8MQA_BF16, 128>() ||
-        !attention_smem<FP8MQA_F16, 64>() || !attention_smem<FP8MQA_F16, 128>()) {
+        !attention_smem<FP8MQA_F16, 64>() || !attention_smem<FP8MQA_F16, 128>() ||
+        !logits_smem<1>() || !logits_smem<2>() || !logits_smem<4>()) {
         cudaGetLastError();
-        st.status = FP8MQA_ERR_LAUNCH;
+        st.init_status = FP8MQA_ERR_LAUNCH;
         return;
     }
+    void* buf = nullptr;
+    if (cudaMalloc(&buf, 256) != cudaSuccess || cudaMemset(buf, 0, 256) != cudaSuccess) {
+        cudaGetLastError();
+        cudaFree(buf);
+        st.init_status = FP8MQA_ERR_CUDA;
+        return;
+    }
+    st.status = static_cast<int32_t*>(buf);
+    st.ready.store(true, std::memory_order_release);
 }
 
 PagedDevice* paged_device(int* err)
@@ -75,8 +94,8 @@ PagedDevice* paged_device(int* err)
     }
     PagedDevice& st = g_paged[dev];
     std::call_once(st.once, [dev, &st] { init_paged(dev, st); });
-    *err = st.status;
-    return st.status == FP8MQA_OK ? &st : nullptr;
+    *err = st.init_status;
+    return st.init_status == FP8MQA_OK ? &st : nullptr;
 }
 
 bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -197,7 +216,30 @@ void attention_dim(PagedAttentionParams& p, int32_t dim, int sm_count, cudaStrea
         attention_heads<kType, 128>(p, sm_count, s);
 }
 
+// One launch of the paged logits, kTok tokens a CTA: a full wave, or a CTA for each tile and span.
+template <int kTok>
+void logits_launch(const PagedLogitsParams& p, int sm_count, cudaStream_t s)
+{
+    using S = PagedShape<kTok>;
+    const int64_t work = p.B * ((p.N + kPagedTile - 1) / kPagedTile);
+    const int64_t grid = std::min<int64_t>(work, int64_t(sm_count) * S::kCtasPerSm);
+    paged_logits_kernel<kTok>
+        <<<dim3(unsigned(grid), unsigned((p.T + kTok - 1) / kTok)), kPagedThreads, S::kSmem, s>>>(p);
+}
+
 }  // namespace
+
+bool paged_take_status(int dev, int32_t* flags)
+{
+    const PagedDevice& st = g_paged[dev];
+    if (!st.ready.load(std::memory_order_acquire)) return true;
+    int32_t word = 0;
+    if (cudaMemcpy(&word, st.status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return false;
+    if (word != 0 && cudaMemset(st.status, 0, sizeof(word)) != cudaSuccess) return false;
+    *flags |= word;
+    return true;
+}
+
 }  // namespace fp8mqa
 
 extern "C" {
@@ -306,13 +348,14 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
     if (rc != FP8MQA_OK) return rc;
     if (keys->type != FP8MQA_E4M3 || keys->heads != 1 || keys->dim != kPagedDim)
         return FP8MQA_ERR_UNSUPPORTED_SHAPE;
-    if (B * T > 65535 || N >= int64_t(1) << 30) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
+    if (B * T >= int64_t(1) << 31 || T > 65535 || N >= int64_t(1) << 30) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
     if (B == 0 || T == 0 || N == 0) return FP8MQA_OK;
     if (!q_fp8 || !w || !lens || !out || (table_cols > 0 && !table)) return FP8MQA_ERR_INVALID_ARG;
     if (!on(q_fp8, 16) || !on(w, 16) || !on(table, 4) || !on(lens, 4) || !on(out, 4))
         return FP8MQA_ERR_MISALIGNED;
     int err = FP8MQA_OK;
-    if (!paged_device(&err)) return err;
+    PagedDevice* st = paged_device(&err);
+    if (!st) return err;
     PagedLogitsParams p;
     p.q = q_fp8;
     p.w = w;
@@ -325,8 +368,17 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
     p.B = B;
     p.T = T;
     p.clean = clean_logits;
-    paged_logits_kernel<<<dim3(unsigned((N + 127) / 128), unsigned(B * T)), 128, 0,
-                          static_cast<cudaStream_t>(stream)>>>(p);
+    p.aligned = on(out, 16) && ld % 4 == 0;
+    p.status = st->status;
+    p.wait_ns = wait_limit_ns();
+    if (!row_units(p.keys, &p.units)) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 1)
+        logits_launch<1>(p, st->sm_count, s);
+    else if (T == 2)
+        logits_launch<2>(p, st->sm_count, s);
+    else
+        logits_launch<4>(p, st->sm_count, s);
     return launched();
 }
 

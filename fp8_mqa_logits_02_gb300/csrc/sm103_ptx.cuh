@@ -243,4 +243,18 @@ __device__ __forceinline__ void regs_inc()
 }
 
 }  // namespace ptx
+
+// Shared-memory matrix descriptor for a K-major operand whose rows are exactly 128 bytes,
+// stored with the 128-byte swizzle (8-row atoms of 1024 bytes, as TMA writes them).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= uint64_t((saddr >> 4) & 0x3FFF);  // start address
+    d |= uint64_t(1) << 16;                // leading byte offset (unused with this swizzle)
+    d |= uint64_t(1024 >> 4) << 32;        // stride byte offset: next 8-row atom
+    d |= uint64_t(1) << 46;                // descriptor version
+    d |= uint64_t(2) << 61;                // 128-byte swizzle
+    return d;
+}
+
 }  // namespace fp8mqa
