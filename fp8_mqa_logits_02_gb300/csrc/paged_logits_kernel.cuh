@@ -137,7 +137,11 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
 
     // ---- tensor memory and barriers
     const uint32_t bar = base + S::kOffBar;  // two: one for each TMEM buffer
-    if (warp == 0) ptx::tmem_alloc(ptx::smem_addr(&s_tmem), S::kTmemCols);
+    if (warp == 0) {
+        // the permit is given up at once: while a CTA holds it, the SM's next CTA waits in its alloc
+        ptx::tmem_alloc(ptx::smem_addr(&s_tmem), S::kTmemCols);
+        ptx::tmem_relinquish();
+    }
     if (tid == 0) {
         ptx::mbar_init(bar, 1);
         ptx::mbar_init(bar + 8, 1);
@@ -373,10 +377,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
         }
         __syncthreads();
     }
-    if (warp == 0) {
-        ptx::tmem_relinquish();
-        ptx::tmem_dealloc(tmem, S::kTmemCols);
-    }
+    if (warp == 0) ptx::tmem_dealloc(tmem, S::kTmemCols);
 }
 
 }  // namespace fp8mqa
