@@ -368,7 +368,6 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
     p.B = B;
     p.T = T;
     p.clean = clean_logits;
-    p.aligned = on(out, 16) && ld % 4 == 0;
     p.status = st->status;
     p.wait_ns = wait_limit_ns();
     if (!row_units(p.keys, &p.units)) return FP8MQA_ERR_UNSUPPORTED_SHAPE;

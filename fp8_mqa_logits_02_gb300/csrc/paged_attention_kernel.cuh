@@ -148,26 +148,6 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi)
     return r;
 }
 
-// Asynchronous copies into shared memory; what is not there is filled with zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
-{
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(there ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-                 "r"(there ? 4 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copy_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
 // Where piece c of row r lies in a stage.  A fragment read of K takes four pieces of two rows in
 // a phase, one of V two pieces of every second of eight rows.
 template <int kPieces>

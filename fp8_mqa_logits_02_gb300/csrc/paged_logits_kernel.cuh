@@ -6,20 +6,21 @@
 // (8192 flops a key and token) go to tcgen05: at the rate at which HBM gives keys that is 415 TFLOP/s
 // for one token, 1.7 PFLOP/s for four, more than the warps' own matrix instructions can be asked for.
 //
-// A CTA's four warps do everything, a tile of 128 keys at a time (thread = key = TMEM lane):
-//   copy      each warp copies its 32 keys' rows into a ring of kStages tiles, as the 128-byte swizzle
-//             of the MMA wants them, wherever their pages lie; two stages or three are in flight;
-//   multiply  one thread issues S[key, (t, h)] = K Q^T for the tile whose copies are done, into one
-//             of two TMEM buffers;
-//   finish    meanwhile the threads take the previous tile's S: relu, times w, the sum over 32 heads
-//             in registers, times the key's scale, a coalesced store.
+// Warps of a CTA, a tile of 128 keys at a time (thread = key = TMEM lane):
+//   copy (4)     each copies its 32 keys' rows into a ring of kStages tiles, as the 128-byte swizzle of
+//                the MMA wants them, wherever their pages lie; the next tile's pages are looked up first;
+//   multiply (1) one thread issues S[key, (t, h)] = K Q^T into one of two TMEM buffers;
+//   finish (8)   S from TMEM, relu, times w, the sum over 32 heads in registers, times the key's scale,
+//                a coalesced store; four warps take the even tiles (and their buffer), four the odd ones;
+//   fill (1)     clean_logits: the -inf spans.
+// (With four warps doing it all in turn the chain of a tile's steps decided: 1.65 us a tile, 47 us for
+// 64 rows x 2 tokens.)
 //
-// Split: the rows' tiles, and for clean_logits their -inf spans, are laid end to end by cost, and
-// every CTA takes an equal share; it writes its -inf spans while its first copies are under way.
-// A CTA's stream of tiles runs on from row to row; Q and w have kSlots slots for that.
+// Split: the rows' tiles and -inf spans are laid end to end by cost, and every CTA takes an equal
+// share.  A CTA's stream of tiles runs on from row to row; Q and w have kSlots slots for that.
 //
-// The waits for the tensor core are bounded (PagedLogitsParams::wait_ns); on expiry the CTA reports
-// it in the status word, waits for its MMAs once more, frees its tensor memory and returns.
+// Every wait is bounded (PagedLogitsParams::wait_ns); on expiry the CTA reports it in the status
+// word, all its warps stop, its MMAs under way get kPagedDrainNs more, and it frees its tensor memory.
 #pragma once
 
 #include <math_constants.h>
@@ -39,44 +40,57 @@ struct PagedLogitsParams {
     float* out;
     int64_t ld, N, B;
     int32_t T, clean;
-    int32_t aligned;  // rows of out start on 16 bytes
     int32_t* status;
     uint64_t wait_ns;
 };
 
 constexpr int kPagedHeads = 32, kPagedDim = 128;
-constexpr int kPagedThreads = 128, kPagedWarps = kPagedThreads / 32, kPagedTile = 128;
+constexpr int kPagedTile = 128;
+constexpr int kPagedCopyWarps = 4, kPagedFinishWarps = 8;
+constexpr int kPagedMmaWarp = kPagedCopyWarps + kPagedFinishWarps;
+constexpr int kPagedCopyThreads = 32 * kPagedCopyWarps;
+constexpr int kPagedThreads = 32 * (kPagedMmaWarp + 2);  // the last one fills
+constexpr int kPagedAhead = 2;    // tiles a copy warp leaves under way when it reports one
 constexpr int kPagedMmaK = 32;     // E4M3 values of a tcgen05.mma
 constexpr int kPagedFill = 1024;  // columns of a -inf span
 constexpr int32_t kPagedTimeout = 1;           // status bit: a bounded wait gave up
 constexpr uint64_t kPagedDrainNs = 1000000000ull;  // bound of the last wait before a CTA gives up
 
+// A tile in the ring.
+struct PagedItem {
+    int64_t b;
+    int32_t tile, row;  // tile -1: the end; row: the CTA's running number of its rows
+    int32_t len, pad;
+    uint32_t there[4];  // which keys are there
+    float scale[kPagedTile];
+};
+
 // kTok: tokens of a CTA (1, 2 or 4).
 template <int kTok>
 struct PagedShape {
-    static constexpr int kStages = kTok == 2 ? 4 : 3;
-    static constexpr int kSlots = 3;  // rows whose Q and w are held: of the tile being finished and two on
-    static constexpr int kCtasPerSm = kTok == 1 ? 3 : 2;
+    static constexpr int kStages = kTok == 4 ? 3 : 4;
+    // What is known of a tile outlives its keys: when the copies of tile j + kItems begin, tile j + 3 is
+    // multiplied, so tile j + 1 is finished, and all finishing warps have seen tile j.
+    static constexpr int kItems = kStages + 3;
+    static constexpr int kSlots = kTok == 4 ? 3 : 4;  // rows whose Q and w are held
+    static constexpr int kCtasPerSm = 2;
     static constexpr uint32_t kN = kTok * kPagedHeads;
     static constexpr uint32_t kTmemCols = 2 * kN;
     static constexpr uint32_t kKBytes = kPagedTile * kPagedDim, kQBytes = kN * kPagedDim;
     static constexpr uint32_t kOffQ = kStages * kKBytes;
     static constexpr uint32_t kOffW = kOffQ + kSlots * kQBytes;
-    static constexpr uint32_t kOffScale = kOffW + kSlots * kN * 4;
-    static constexpr uint32_t kOffItem = kOffScale + kStages * kPagedTile * 4;
-    static constexpr uint32_t kOffBar = kOffItem + kStages * 32;
-    static constexpr uint32_t kSmem = kOffBar + 32 + 1024;  // slack for aligning the base
+    static constexpr uint32_t kOffItem = kOffW + kSlots * kN * 4;
+    static constexpr uint32_t kOffBar = kOffItem + kItems * sizeof(PagedItem);
+    // Barriers: stage full, stage empty, item there, buffer full, buffer empty, slot empty.  Nobody may
+    // fall a whole phase behind a barrier that it waits for, so the finishing warps wait for the items',
+    // not for the stages', which may be filled again before a tile is finished.
+    static constexpr int kFull = 0, kEmpty = kStages, kItem = 2 * kStages;
+    static constexpr int kAccFull = kItem + kItems, kAccEmpty = kAccFull + 2;
+    static constexpr int kSlotEmpty = kAccEmpty + 2, kBars = kSlotEmpty + kSlots;
+    static constexpr uint32_t kSmem = kOffBar + 8 * kBars + 1024;  // slack for aligning the base
     // D f32, A = B = E4M3, both K-major, M = 128 keys
     static constexpr uint32_t kIdesc = (1u << 4) | ((kN >> 3) << 17) | (uint32_t(kPagedTile >> 4) << 24);
 };
-
-// A tile in the ring.
-struct PagedItem {
-    int64_t b;
-    int32_t tile, row;   // row: the CTA's running number of its rows
-    uint32_t there[4];   // which keys are there
-};
-static_assert(sizeof(PagedItem) == 32, "PagedShape::kOffItem");
 
 __device__ __forceinline__ void tmem_ld_32(uint32_t addr, uint32_t (&r)[32])
 {
@@ -99,65 +113,80 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
 {
     using S = PagedShape<kTok>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t s_scan[kPagedWarps], s_first[2];
+    __shared__ int64_t s_scan[kPagedCopyWarps], s_first[2];
     __shared__ uint32_t s_tmem;
+    __shared__ volatile int32_t s_stop;
     uint8_t* const smem =
         smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_addr(smem);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int t0 = blockIdx.y * kTok, n_tok = min(kTok, p.T - t0);
     const int64_t cap = min(p.N, int64_t(p.table.cols) * p.keys.page_size);
+    auto bar = [&](int i) { return base + S::kOffBar + 8 * i; };
+    PagedItem* const items = reinterpret_cast<PagedItem*>(smem + S::kOffItem);
 
     // ---- the rows' costs, in units of about half a kilobyte moved
-    const int64_t c_tile = 34 + n_tok, c_fill = 8 * n_tok;
+    const int32_t c_tile = 34 + n_tok, c_fill = 8 * n_tok;
     auto length = [&](int64_t b) {
         const int64_t n = __ldg(p.lens + b);
         return int32_t(n < 0 ? 0 : n < cap ? n : cap);
     };
     auto tiles = [&](int64_t b) { return (length(b) + kPagedTile - 1) / kPagedTile; };
     auto fills = [&](int32_t n_tiles) {
-        const int64_t left = p.N - int64_t(n_tiles) * kPagedTile;
-        return !p.clean || left <= 0 ? int64_t(0) : (left + kPagedFill - 1) / kPagedFill;
+        const int32_t left = int32_t(p.N) - n_tiles * kPagedTile;
+        return !p.clean || left <= 0 ? 0 : (left + kPagedFill - 1) / kPagedFill;
     };
     auto cost = [&](int64_t b) {
         const int32_t n = tiles(b);
-        return n * c_tile + fills(n) * c_fill;
+        return int64_t(n) * c_tile + int64_t(fills(n)) * c_fill;
     };
-    const int64_t per = (p.B + kPagedThreads - 1) / kPagedThreads;
-    const int64_t b1 = min(per * (tid + 1), p.B);
-    int64_t sum = 0;
-    for (int64_t b = per * tid; b < b1; ++b) sum += cost(b);
-    int64_t scan = sum, total = 0, before = 0;
+    const int64_t per = (p.B + kPagedCopyThreads - 1) / kPagedCopyThreads;
+    int64_t sum = 0, scan = 0;
+    if (tid < kPagedCopyThreads) {
+        const int64_t b1 = min(per * (tid + 1), p.B);
+        for (int64_t b = per * tid; b < b1; ++b) sum += cost(b);
+        scan = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int64_t x = __shfl_up_sync(~0u, scan, o);
-        if (lane >= o) scan += x;
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t x = __shfl_up_sync(~0u, scan, o);
+            if (lane >= o) scan += x;
+        }
+        if (lane == 31) s_scan[warp] = scan;
     }
-    if (lane == 31) s_scan[warp] = scan;
 
     // ---- tensor memory and barriers
-    const uint32_t bar = base + S::kOffBar;  // two: one for each TMEM buffer
-    if (warp == 0) {
+    if (warp == kPagedMmaWarp) {
         // the permit is given up at once: while a CTA holds it, the SM's next CTA waits in its alloc
         ptx::tmem_alloc(ptx::smem_addr(&s_tmem), S::kTmemCols);
         ptx::tmem_relinquish();
-    }
-    if (tid == 0) {
-        ptx::mbar_init(bar, 1);
-        ptx::mbar_init(bar + 8, 1);
-        ptx::mbar_init_fence();
+        if (lane == 0) {
+            for (int i = 0; i < S::kStages; ++i) {
+                ptx::mbar_init(bar(S::kFull + i), kPagedCopyWarps);
+                ptx::mbar_init(bar(S::kEmpty + i), 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                ptx::mbar_init(bar(S::kAccFull + i), 1);
+                ptx::mbar_init(bar(S::kAccEmpty + i), 4);
+            }
+            for (int i = 0; i < S::kItems; ++i) ptx::mbar_init(bar(S::kItem + i), kPagedCopyWarps);
+            for (int i = 0; i < S::kSlots; ++i)
+                ptx::mbar_init(bar(S::kSlotEmpty + i), kPagedFinishWarps);
+            ptx::mbar_init_fence();
+            s_stop = 0;
+        }
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = s_tmem;
+    int64_t total = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < kPagedWarps; ++w) {
+    for (int w = 0; w < kPagedCopyWarps; ++w) {
         if (w == warp) before = total + scan - sum;
         total += s_scan[w];
     }
     const int64_t from = blockIdx.x * total / gridDim.x, to = (blockIdx.x + 1) * total / gridDim.x;
-    if (before <= from && from < before + sum) {
+    if (tid < kPagedCopyThreads && before <= from && from < before + sum) {
         int64_t b = per * tid, at = before;
         for (;; ++b) {
             const int64_t c = cost(b);
@@ -169,180 +198,157 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
     }
     __syncthreads();
 
-    // ---- the stream of this CTA's tiles: those whose cost begins in [from, to)
-    int64_t next_b = s_first[0], next_at = s_first[1];  // the next row, the cost before it
-    if (from >= to) next_at = to;
-    int64_t cur_b = 0;
-    int32_t cur_tile = 0, cur_end = 0, cur_len = 0, cur_row = -1;  // the row being copied
-    auto more = [&] {  // whether there is a tile to copy; moves on to its row
-        while (cur_tile >= cur_end) {
-            if (next_at >= to) return false;
-            cur_b = next_b++;
-            cur_len = length(cur_b);
-            const int32_t n = (cur_len + kPagedTile - 1) / kPagedTile;
-            const int64_t lo = from > next_at ? (from - next_at + c_tile - 1) / c_tile : 0;
-            const int64_t hi = (to - next_at + c_tile - 1) / c_tile;
-            cur_tile = int32_t(min(lo, int64_t(n)));
-            cur_end = int32_t(min(hi, int64_t(n)));
-            next_at += n * c_tile + fills(n) * c_fill;
-            cur_row = -1;  // not numbered yet
-        }
-        return true;
-    };
-    // ---- copies
-    int32_t copied = 0, rows_copied = 0;
-    auto copy = [&] {  // the tile that more() found, and its row's Q and w with the first one
-        const int stage = copied % S::kStages;
-        const int32_t n = cur_tile * kPagedTile + tid;
-        int32_t page = -1, row = 0;
-        const bool there = n < cur_len && locate(p.keys, p.table, cur_b, n, &page, &row);
-        const uint32_t at = there ? page * p.units.page + row * p.units.row : kNoRow;
-        const uint32_t dst = base + stage * S::kKBytes;
-        const int c = lane % 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int r = j * 4 + lane / 8;
-            const uint32_t from_row = __shfl_sync(~0u, at, r);
-            const bool ok = from_row != kNoRow;
-            copy16(dst + (warp * 32 + r) * 128 + 16 * (c ^ (r & 7)),
-                   p.keys.data + uint64_t(ok ? from_row : 0) * p.units.unit + 16 * c, ok);
-        }
-        copy4(base + S::kOffScale + (stage * kPagedTile + tid) * 4,
-              p.keys.scale + (there ? int64_t(page) * p.keys.scale_page_stride +
-                                          int64_t(row) * p.keys.scale_row_stride
-                                    : 0),
-              there);
-        const uint32_t here = __ballot_sync(~0u, there);
-        if (cur_row < 0) {  // the row's first tile
-            cur_row = rows_copied++;
-            const int slot = cur_row % S::kSlots;
-            const int64_t first = (cur_b * p.T + t0) * kPagedHeads;
-            for (int i = tid; i < n_tok * kPagedHeads * 8; i += kPagedThreads)
-                copy16(base + S::kOffQ + slot * S::kQBytes + i / 8 * 128 + 16 * (i % 8 ^ (i / 8 & 7)),
-                       p.q + (first + i / 8) * kPagedDim + 16 * (i % 8), true);
-            for (int i = tid; i < n_tok * kPagedHeads / 4; i += kPagedThreads)
-                copy16(base + S::kOffW + slot * S::kN * 4 + 16 * i, p.w + first + 4 * i, true);
-        }
-        PagedItem* const item = reinterpret_cast<PagedItem*>(smem + S::kOffItem) + stage;
-        if (lane == 0) item->there[warp] = here;
-        if (tid == 0) {
-            item->b = cur_b;
-            item->tile = cur_tile;
-            item->row = cur_row;
-        }
-        copy_commit();
-        ++copied;
-        ++cur_tile;
-    };
-    // Waits until tile i is multiplied, for `limit` ns at most.
-    auto wait = [&](int32_t i, uint64_t limit) {
-        const uint32_t at = bar + 8 * (i & 1), parity = uint32_t(i >> 1) & 1u;
-        if (ptx::mbar_try_wait(at, parity)) return true;
+    // Waits for a phase of a barrier; false when the CTA gives up.
+    auto wait = [&](int i, uint32_t parity) {
+        if (ptx::mbar_try_wait(bar(i), parity)) return true;
         const uint64_t start = ptx::globaltimer_ns();
-        while (!ptx::mbar_try_wait_sleep(at, parity, 20000))
-            if (ptx::globaltimer_ns() - start > limit) return false;
+        while (!ptx::mbar_try_wait_sleep(bar(i), parity, 20000)) {
+            if (s_stop) return false;
+            if (ptx::globaltimer_ns() - start > p.wait_ns) {
+                s_stop = 1;
+                atomicOr(p.status, kPagedTimeout);
+                return false;
+            }
+        }
         return true;
     };
-
-    // ---- the first copies, and the -inf spans while they are under way
-    int32_t row_done = 0;  // the number of the row whose tile was finished last (or comes first)
-    auto allowed = [&] {   // whether the next tile's row has a slot
-        return cur_row >= 0 || rows_copied - row_done < S::kSlots;
+    // The same for all lanes of a warp: they go on or give up together.
+    auto wait_warp = [&](int i, uint32_t parity) { return __all_sync(~0u, wait(i, parity)) != 0; };
+    // Items i of a share that begin in [from, to), of n items of cost c each from `at` on.
+    auto share = [&](int64_t at, int32_t c, int32_t n, int32_t* lo, int32_t* hi) {
+        *lo = from > at ? int32_t(min(int64_t(n), (from - at + c - 1) / c)) : 0;
+        *hi = to > at ? int32_t(min(int64_t(n), (to - at + c - 1) / c)) : 0;
     };
-    while (copied < S::kStages - 1 && more() && allowed()) copy();
-    if (p.clean) {
-        int64_t at = s_first[1];
-        for (int64_t b = s_first[0]; at < to; ++b) {
-            const int32_t n = tiles(b);
-            const int64_t n_fill = fills(n), begin = at + n * c_tile;
-            at = begin + n_fill * c_fill;
-            const int64_t lo = from > begin ? (from - begin + c_fill - 1) / c_fill : 0;
-            const int64_t hi = min(n_fill, (to - begin + c_fill - 1) / c_fill);
-            for (int64_t f = lo; f < hi; ++f) {
-                const int64_t c0 = int64_t(n) * kPagedTile + f * kPagedFill;
-                const int64_t c1 = min(p.N, c0 + kPagedFill);
-                for (int t = 0; t < n_tok; ++t) {
-                    float* const out = p.out + (b * p.T + t0 + t) * p.ld;
-                    if (p.aligned) {
-                        const int64_t c4 = c0 + (c1 - c0) / 4 * 4;
-                        for (int64_t c = c0 + 4 * tid; c < c4; c += 4 * kPagedThreads)
-                            __stcs(reinterpret_cast<float4*>(out + c),
-                                   make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F,
-                                               -CUDART_INF_F));
-                        if (c4 + tid < c1) __stcs(out + c4 + tid, -CUDART_INF_F);
-                    } else {
-                        for (int64_t c = c0 + tid; c < c1; c += kPagedThreads)
-                            __stcs(out + c, -CUDART_INF_F);
-                    }
-                }
-            }
-        }
-    }
 
-    // ---- tile i multiplied while tile i - 1 is finished
-    bool late = false;
-    int32_t issued = 0;
-    int64_t prev_b = 0;
-    int32_t prev_tile = 0, prev_row = 0, prev_len = 0;
-    uint32_t prev_there = 0;
-    float prev_scale = 0.0f;
-    for (int32_t i = 0;; ++i) {
-        const bool any = i < copied;  // the same in all threads
-        if (any) {
-            const int behind = copied - 1 - i;  // copies after this tile's
-            if (behind <= 0)
-                copy_wait<0>();
-            else if (behind == 1)
-                copy_wait<1>();
-            else
-                copy_wait<2>();
-            ptx::fence_proxy_async_smem();
-        }
-        ptx::tc_fence_before();  // tile i - 2 is read from the buffer that tile i takes
-        if (__syncthreads_or(late) || (!any && i == 0)) break;
-        PagedItem item;
-        uint32_t there = 0;
-        float scale = 0.0f;
-        int32_t len = 0;
-        if (any) {
-            const int stage = i % S::kStages;
-            const PagedItem* const at = reinterpret_cast<const PagedItem*>(smem + S::kOffItem) + stage;
-            item.b = at->b;
-            item.tile = at->tile;
-            item.row = at->row;
-            there = at->there[warp];
-            scale = reinterpret_cast<const float*>(smem + S::kOffScale)[stage * kPagedTile + tid];
-            len = __ldg(p.lens + item.b);
-            if (tid == 0) {
-                ptx::tc_fence_after();
-                const uint64_t a = sw128_desc(base + stage * S::kKBytes);
-                const uint64_t q = sw128_desc(base + S::kOffQ + item.row % S::kSlots * S::kQBytes);
-#pragma unroll
-                for (int k = 0; k < kPagedDim / kPagedMmaK; ++k)
-                    ptx::mma_f8f6f4(tmem + (i & 1) * S::kN, a + 2ull * k, q + 2ull * k, S::kIdesc,
-                                    k > 0 ? 1u : 0u);
-                ptx::mma_commit(bar + 8 * (i & 1));
+    if (from >= to) {
+        // nothing to do
+    } else if (warp < kPagedCopyWarps) {
+        // ------------------------------------------------------------ copy
+        int64_t b = s_first[0], at = s_first[1];  // the next row, the cost before it
+        int64_t cur_b = 0;
+        int32_t tile = 0, tile_end = 0, len = 0, row = -1;
+        bool first = false;
+        int32_t page = -1, page_row = 0;
+        // Moves on to the next tile and looks up its pages; tile = -1: there is none.
+        auto next = [&] {
+            ++tile;
+            first = false;
+            while (tile >= tile_end) {
+                if (at >= to) {
+                    tile = -1;
+                    return;
+                }
+                cur_b = b++;
+                len = length(cur_b);
+                const int32_t n = (len + kPagedTile - 1) / kPagedTile;
+                share(at, c_tile, n, &tile, &tile_end);
+                at += int64_t(n) * c_tile + int64_t(fills(n)) * c_fill;
+                first = true;
             }
+            if (first) ++row;
+            const int32_t n = tile * kPagedTile + tid;
+            if (!(n < len && locate(p.keys, p.table, cur_b, n, &page, &page_row))) page = -1;
+        };
+        int32_t reported = 0;
+        auto report = [&](int32_t end) {  // this warp's parts of the tiles before `end` are there
+            ptx::fence_proxy_async_smem();
             __syncwarp();
-            ++issued;
-        }
-        if (i > 0) {
-            late = __any_sync(~0u, !wait(i - 1, p.wait_ns));
-            row_done = prev_row;
-        }
-        // every MMA before tile i is done, so the stage of tile i - 1 is free
-        while (!late && copied < i + S::kStages && more() && allowed()) copy();
-        if (i > 0 && !late) {
-            ptx::tc_fence_after();
-            const float* const w =
-                reinterpret_cast<const float*>(smem + S::kOffW) + prev_row % S::kSlots * S::kN;
-            const int64_t n = int64_t(prev_tile) * kPagedTile + tid;
+            for (; reported < end; ++reported)
+                if (lane == 0) {
+                    ptx::mbar_arrive(bar(S::kFull + reported % S::kStages));
+                    ptx::mbar_arrive(bar(S::kItem + reported % S::kItems));
+                }
+        };
+        tile = tile_end = 0;
+        next();
+        int32_t j = 0;
+        bool ok = true;
+        for (;; ++j) {
+            const int stage = j % S::kStages;
+            if (j >= S::kStages &&
+                !(ok = wait_warp(S::kEmpty + stage, uint32_t(j / S::kStages - 1) & 1u)))
+                break;
+            PagedItem& item = items[j % S::kItems];
+            if (tid == 0) {
+                item.b = cur_b;
+                item.tile = tile;
+                item.row = row;
+                item.len = len;
+            }
+            if (tile < 0) break;
+            if (first) {  // the row's Q and w
+                const int slot = row % S::kSlots;
+                if (row >= S::kSlots) {
+                    const uint32_t parity = uint32_t(row / S::kSlots - 1) & 1u;
+                    if (!__all_sync(~0u, ptx::mbar_try_wait(bar(S::kSlotEmpty + slot), parity))) {
+                        // rows of a tile or two: the slot may wait for tiles not reported yet
+                        copy_wait<0>();
+                        report(j);
+                    }
+                    if (!(ok = wait_warp(S::kSlotEmpty + slot, parity))) break;
+                }
+                const int64_t q0 = (cur_b * p.T + t0) * kPagedHeads;
+                for (int i = tid; i < n_tok * kPagedHeads * 8; i += kPagedCopyThreads)
+                    copy16(base + S::kOffQ + slot * S::kQBytes + i / 8 * 128 + 16 * (i % 8 ^ (i / 8 & 7)),
+                           p.q + (q0 + i / 8) * kPagedDim + 16 * (i % 8), true);
+                for (int i = tid; i < n_tok * kPagedHeads / 4; i += kPagedCopyThreads)
+                    copy16(base + S::kOffW + slot * S::kN * 4 + 16 * i, p.w + q0 + 4 * i, true);
+            }
+            const bool there = page >= 0;
+            const uint32_t place = there ? page * p.units.page + page_row * p.units.row : kNoRow;
+            const uint32_t dst = base + stage * S::kKBytes + warp * 32 * 128;
+            const int c = lane % 8;
 #pragma unroll
-            for (int t = 0; t < kTok; ++t) {
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + lane / 8;
+                const uint32_t src = __shfl_sync(~0u, place, r);
+                const bool have = src != kNoRow;
+                copy16(dst + r * 128 + 16 * (c ^ (r & 7)),
+                       p.keys.data + uint64_t(have ? src : 0) * p.units.unit + 16 * c, have);
+            }
+            copy4(ptx::smem_addr(&item.scale[tid]),
+                  p.keys.scale + (there ? int64_t(page) * p.keys.scale_page_stride +
+                                              int64_t(page_row) * p.keys.scale_row_stride
+                                        : 0),
+                  there);
+            const uint32_t here = __ballot_sync(~0u, there);
+            if (lane == 0) item.there[warp] = here;
+            copy_commit();
+            next();
+            copy_wait<kPagedAhead>();
+            report(j - kPagedAhead + 1);
+        }
+        copy_wait<0>();
+        if (ok) report(j + 1);  // the last tiles, and the end
+    } else if (warp < kPagedMmaWarp) {
+        // ------------------------------------------------------------ finish
+        const int quarter = warp % 4, parity = warp / 4 % 2;  // TMEM lanes, and tiles
+        int32_t row = 0;
+        for (int32_t j = 0;; ++j) {
+            if (!wait_warp(S::kItem + j % S::kItems, uint32_t(j / S::kItems) & 1u)) break;
+            const PagedItem& item = items[j % S::kItems];
+            const int32_t tile = item.tile;
+            if (tile < 0) break;
+            if (item.row != row) {  // the row before is finished with
+                if (lane == 0) ptx::mbar_arrive(bar(S::kSlotEmpty + row % S::kSlots));
+                row = item.row;
+            }
+            if ((j & 1) != parity) continue;
+            const int64_t b = item.b;
+            const int32_t n = tile * kPagedTile + quarter * 32 + lane, len = item.len;
+            const float scale = item.scale[quarter * 32 + lane];
+            const bool there = item.there[quarter] >> lane & 1u;
+            const int64_t len_full = __ldg(p.lens + b);
+            const float* const w =
+                reinterpret_cast<const float*>(smem + S::kOffW) + row % S::kSlots * S::kN;
+            float* out = p.out + (b * p.T + t0) * p.ld + n;
+            if (!wait_warp(S::kAccFull + (j & 1), uint32_t(j >> 1) & 1u)) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int t = 0; t < kTok; ++t, out += p.ld) {
                 if (t >= n_tok) break;
                 uint32_t x[kPagedHeads];
-                tmem_ld_32(tmem + (uint32_t(warp * 32) << 16) + ((i - 1) & 1) * S::kN + t * kPagedHeads,
-                           x);
+                tmem_ld_32(tmem + (uint32_t(quarter * 32) << 16) + (j & 1) * S::kN + t * kPagedHeads, x);
                 float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int h = 0; h < kPagedHeads; h += 4) {
@@ -352,32 +358,76 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
                     y[2] = fmaf(fmaxf(__uint_as_float(x[h + 2]), 0.0f), wh.z, y[2]);
                     y[3] = fmaf(fmaxf(__uint_as_float(x[h + 3]), 0.0f), wh.w, y[3]);
                 }
-                const float sum = ((y[0] + y[1]) + (y[2] + y[3])) * prev_scale;
-                const bool seen = n < min(int64_t(prev_len) - (p.T - 1 - (t0 + t)), cap);
+                const bool seen = n < len && n < len_full - (p.T - 1 - (t0 + t));
                 if (n < p.N && (seen || p.clean))
-                    __stcs(p.out + (prev_b * p.T + t0 + t) * p.ld + n,
-                           seen && (prev_there >> lane & 1u) ? sum : -CUDART_INF_F);
+                    __stcs(out, seen && there ? ((y[0] + y[1]) + (y[2] + y[3])) * scale
+                                              : -CUDART_INF_F);
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(S::kAccEmpty + (j & 1)));
+        }
+    } else if (warp == kPagedMmaWarp) {
+        // ------------------------------------------------------------ multiply
+        if (lane == 0) {
+            int32_t j = 0;
+            for (;; ++j) {
+                const int stage = j % S::kStages;
+                if (!wait(S::kFull + stage, uint32_t(j / S::kStages) & 1u)) break;
+                const PagedItem& item = items[j % S::kItems];
+                if (item.tile < 0) break;
+                if (j >= 2 && !wait(S::kAccEmpty + (j & 1), uint32_t((j >> 1) - 1) & 1u)) break;
+                ptx::tc_fence_after();
+                const uint64_t a = sw128_desc(base + stage * S::kKBytes);
+                const uint64_t q = sw128_desc(base + S::kOffQ + item.row % S::kSlots * S::kQBytes);
+#pragma unroll
+                for (int k = 0; k < kPagedDim / kPagedMmaK; ++k)
+                    ptx::mma_f8f6f4(tmem + (j & 1) * S::kN, a + 2ull * k, q + 2ull * k, S::kIdesc,
+                                    k > 0 ? 1u : 0u);
+                ptx::mma_commit(bar(S::kEmpty + stage));
+                ptx::mma_commit(bar(S::kAccFull + (j & 1)));
+            }
+            // all MMAs are done before their tensor memory is freed
+            if (j > 0) {
+                const int i = S::kAccFull + ((j - 1) & 1);
+                const uint32_t parity = uint32_t((j - 1) >> 1) & 1u;
+                const uint64_t start = ptx::globaltimer_ns();
+                while (!ptx::mbar_try_wait_sleep(bar(i), parity, 20000) &&
+                       ptx::globaltimer_ns() - start <= kPagedDrainNs) {
+                }
             }
         }
-        if (!any) break;
-        prev_b = item.b;
-        prev_tile = item.tile;
-        prev_row = item.row;
-        prev_there = there;
-        prev_scale = scale;
-        prev_len = len;
-    }
-
-    // ---- the end; after a wait that gave up, the MMAs under way get kPagedDrainNs more
-    copy_wait<0>();
-    if (__syncthreads_or(late)) {
-        if (tid == 0) {
-            atomicOr(p.status, kPagedTimeout);
-            if (issued > 0) wait(issued - 1, kPagedDrainNs);
+        __syncwarp();
+    } else if (p.clean) {
+        // ------------------------------------------------------------ fill
+        int64_t at = s_first[1];
+        for (int64_t b = s_first[0]; at < to; ++b) {
+            const int32_t n = tiles(b), n_fill = fills(n);
+            int32_t lo, hi;
+            at += int64_t(n) * c_tile;
+            share(at, c_fill, n_fill, &lo, &hi);
+            at += int64_t(n_fill) * c_fill;
+            if (lo >= hi) continue;
+            const int64_t c0 = int64_t(n) * kPagedTile + int64_t(lo) * kPagedFill;
+            const int64_t c1 = min(p.N, int64_t(n) * kPagedTile + int64_t(hi) * kPagedFill);
+            for (int t = 0; t < n_tok; ++t) {
+                float* const out = p.out + (b * p.T + t0 + t) * p.ld;
+                // 16-byte stores between the first and the last 16-byte boundary
+                const int64_t a0 = min(c1, c0 + int64_t((16u - uint32_t(reinterpret_cast<uintptr_t>(out + c0) & 15u)) % 16u / 4u));
+                const int64_t a1 = a0 + (c1 - a0) / 4 * 4;
+                if (c0 + lane < a0) __stcs(out + c0 + lane, -CUDART_INF_F);
+#pragma unroll 4
+                for (int64_t c = a0 + 4 * lane; c < a1; c += 128)
+                    __stcs(reinterpret_cast<float4*>(out + c),
+                           make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F));
+                if (a1 + lane < c1) __stcs(out + a1 + lane, -CUDART_INF_F);
+            }
         }
-        __syncthreads();
     }
-    if (warp == 0) ptx::tmem_dealloc(tmem, S::kTmemCols);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kPagedMmaWarp) ptx::tmem_dealloc(tmem, S::kTmemCols);
 }
 
 }  // namespace fp8mqa
