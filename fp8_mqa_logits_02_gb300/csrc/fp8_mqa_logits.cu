@@ -472,6 +472,16 @@ int launch_noalloc(const uint8_t* q, const uint8_t* k, const float* kv, const fl
 
 }  // namespace
 
+bool encode_rows128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t pitch, uint32_t box)
+{
+    std::call_once(g_encode_once, load_encode);
+    if (!g_encode) return false;
+    const cuuint64_t dims[2] = {128, rows}, strides[1] = {pitch};
+    const cuuint32_t boxes[2] = {128, box};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, boxes,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 uint64_t wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
 
 }  // namespace fp8mqa

@@ -31,8 +31,11 @@ PagedDevice g_paged[kPagedMaxDevices];
 template <int kTok>
 bool logits_smem()
 {
-    return cudaFuncSetAttribute(paged_logits_kernel<kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                int(PagedShape<kTok>::kSmem)) == cudaSuccess;
+    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    return cudaFuncSetAttribute(paged_logits_kernel<kTok, true>, attr,
+                                int(PagedShape<kTok, true>::kSmem)) == cudaSuccess &&
+           cudaFuncSetAttribute(paged_logits_kernel<kTok, false>, attr,
+                                int(PagedShape<kTok, false>::kSmem)) == cudaSuccess;
 }
 
 // CTAs of a full wave of the attention kernel.
@@ -216,15 +219,41 @@ void attention_dim(PagedAttentionParams& p, int32_t dim, int sm_count, cudaStrea
         attention_heads<kType, 128>(p, sm_count, s);
 }
 
+// Whether TMA can fetch the keys: a page's rows evenly apart, pages a whole number of rows apart, and
+// pieces of 8 rows or more, so that a piece keeps to the swizzle's atoms of 8 rows; their scales side
+// by side on 16 bytes.
+bool paged_maps(PagedLogitsParams& p, uint32_t tokens, CUtensorMap* map_k, CUtensorMap* map_q)
+{
+    const PagedView& k = p.keys;
+    const int64_t pitch = k.row_stride, step = k.pages > 1 ? k.page_stride : 0;
+    if (k.pages < 1 || k.page_size % 8 != 0 || pitch < kPagedDim || step % pitch != 0) return false;
+    if (k.scale_row_stride != 1 || (k.pages > 1 && k.scale_page_stride % 4 != 0) || !on(k.scale, 16))
+        return false;
+    const int64_t rows = (k.pages - 1) * (step / pitch) + k.page_size;
+    const int64_t q_rows = p.B * p.T * kPagedHeads;
+    if (rows >= int64_t(1) << 31 || q_rows >= int64_t(1) << 31) return false;
+    p.box = std::min(kPagedTile, k.page_size & -k.page_size);
+    p.box_shift = __builtin_ctz(unsigned(p.box));
+    p.page_rows = uint32_t(step / pitch);
+    return encode_rows128(map_k, k.data, uint64_t(rows), uint64_t(pitch), uint32_t(p.box)) &&
+           encode_rows128(map_q, p.q, uint64_t(q_rows), kPagedDim, tokens * kPagedHeads);
+}
+
 // One launch of the paged logits, kTok tokens a CTA: a full wave, or a CTA for each tile and span.
 template <int kTok>
-void logits_launch(const PagedLogitsParams& p, int sm_count, cudaStream_t s)
+void logits_launch(PagedLogitsParams& p, int sm_count, cudaStream_t s)
 {
-    using S = PagedShape<kTok>;
+    using S = PagedShape<kTok, true>;
     const int64_t work = p.B * ((p.N + kPagedTile - 1) / kPagedTile);
-    const int64_t grid = std::min<int64_t>(work, int64_t(sm_count) * S::kCtasPerSm);
-    paged_logits_kernel<kTok>
-        <<<dim3(unsigned(grid), unsigned((p.T + kTok - 1) / kTok)), kPagedThreads, S::kSmem, s>>>(p);
+    const int64_t wave = int64_t(sm_count) * S::kCtasPerSm;
+    const dim3 grid(unsigned(std::min(work, wave)), unsigned((p.T + kTok - 1) / kTok));
+    CUtensorMap map_k = {}, map_q = {};
+    if (paged_maps(p, kTok, &map_k, &map_q))
+        paged_logits_kernel<kTok, true>
+            <<<grid, S::kThreads, S::kSmem, s>>>(p, map_k, map_q);
+    else
+        paged_logits_kernel<kTok, false>
+            <<<grid, PagedShape<kTok, false>::kThreads, PagedShape<kTok, false>::kSmem, s>>>(p, map_k, map_q);
 }
 
 }  // namespace
@@ -314,7 +343,7 @@ int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t 
     if (!paged_device(&err)) return err;
     CacheReadParams p;
     p.cache = view_of(*cache);
-    p.table = {table, table_stride, table_cols};
+    p.table = {table, table_stride, table_cols, FastDiv(uint32_t(cache->page_size))};
     p.starts = starts;
     p.B = B;
     p.total = total;
@@ -360,7 +389,7 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
     p.q = q_fp8;
     p.w = w;
     p.keys = view_of(*keys);
-    p.table = {table, table_stride, table_cols};
+    p.table = {table, table_stride, table_cols, FastDiv(uint32_t(keys->page_size))};
     p.lens = lens;
     p.out = out;
     p.ld = ld;
@@ -437,7 +466,7 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     if (!row_units(p.k, &p.k_units) || !row_units(p.v, &p.v_units))
         return FP8MQA_ERR_UNSUPPORTED_SHAPE;
     p.same_rows = p.k_units.page == p.v_units.page && p.k_units.row == p.v_units.row;
-    p.table = {table, table_stride, table_cols};
+    p.table = {table, table_stride, table_cols, FastDiv(uint32_t(k->page_size))};
     p.lens = lens;
     p.indices = indices;
     p.indices_stride = indices_stride;

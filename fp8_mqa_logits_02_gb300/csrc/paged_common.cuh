@@ -22,10 +22,30 @@ struct PagedView {
     int32_t pages, page_size, heads;
 };
 
+// Division of 0 <= n < 2^31 by a number known before the launch: with 2^bits >= d and
+// mul = ceil(2^(31 + bits) / d) (under 2^32), mul * d - 2^(31 + bits) < d <= 2^bits, so
+// n * mul >> (31 + bits) is exact.
+struct FastDiv {
+    uint32_t mul, shift;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t d)
+    {
+        uint32_t bits = 0;
+        while ((uint64_t(1) << bits) < d) ++bits;
+        shift = 31 + bits;
+        mul = uint32_t(((uint64_t(1) << shift) + d - 1) / d);
+    }
+    __device__ __forceinline__ int32_t of(int32_t n) const
+    {
+        return int32_t(uint64_t(uint32_t(n)) * mul >> shift);
+    }
+};
+
 struct PageTable {
     const int32_t* ids;
     int64_t stride;
     int32_t cols;
+    FastDiv by_page;  // by the cache's page size
 };
 
 // A row's place in a cache as a 32-bit number of units of `unit` bytes (a common divisor of the
@@ -40,7 +60,7 @@ constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 __device__ __forceinline__ bool locate(const PagedView& c, const PageTable& t, int64_t b, int32_t n,
                                        int32_t* page, int32_t* row)
 {
-    const int32_t col = int32_t(uint32_t(n) / uint32_t(c.page_size));
+    const int32_t col = t.by_page.of(n);
     if (n < 0 || col >= t.cols) return false;
     *page = __ldg(t.ids + b * t.stride + col);
     *row = n - col * c.page_size;

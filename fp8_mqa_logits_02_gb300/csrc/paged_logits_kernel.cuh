@@ -7,8 +7,10 @@
 // for one token, 1.7 PFLOP/s for four, more than the warps' own matrix instructions can be asked for.
 //
 // Warps of a CTA, a tile of 128 keys at a time (thread = key = TMEM lane):
-//   copy (4)     each copies its 32 keys' rows into a ring of kStages tiles, as the 128-byte swizzle of
-//                the MMA wants them, wherever their pages lie; the next tile's pages are looked up first;
+//   copy         fills a ring of kStages tiles, as the 128-byte swizzle of the MMA wants them, wherever
+//                their pages lie.  kTma: one warp, a lane for each page's piece of the tile (boxes of
+//                a power of two of rows that divides the page); else four warps by 16-byte
+//                asynchronous copies, their keys' pages looked up a tile ahead;
 //   multiply (1) one thread issues S[key, (t, h)] = K Q^T into one of two TMEM buffers;
 //   finish (8)   S from TMEM, relu, times w, the sum over 32 heads in registers, times the key's scale,
 //                a coalesced store; four warps take the even tiles (and their buffer), four the odd ones;
@@ -23,6 +25,7 @@
 // word, all its warps stop, its MMAs under way get kPagedDrainNs more, and it frees its tensor memory.
 #pragma once
 
+#include <cuda.h>
 #include <math_constants.h>
 
 #include "paged_common.cuh"
@@ -42,14 +45,13 @@ struct PagedLogitsParams {
     int32_t T, clean;
     int32_t* status;
     uint64_t wait_ns;
+    int32_t box, box_shift;  // kTma: rows of a piece, 2^box_shift
+    uint32_t page_rows;      // kTma: rows of the tensor map from page to page
 };
 
 constexpr int kPagedHeads = 32, kPagedDim = 128;
 constexpr int kPagedTile = 128;
-constexpr int kPagedCopyWarps = 4, kPagedFinishWarps = 8;
-constexpr int kPagedMmaWarp = kPagedCopyWarps + kPagedFinishWarps;
-constexpr int kPagedCopyThreads = 32 * kPagedCopyWarps;
-constexpr int kPagedThreads = 32 * (kPagedMmaWarp + 2);  // the last one fills
+constexpr int kPagedFinishWarps = 8, kPagedScanThreads = 128;
 constexpr int kPagedAhead = 2;    // tiles a copy warp leaves under way when it reports one
 constexpr int kPagedMmaK = 32;     // E4M3 values of a tcgen05.mma
 constexpr int kPagedFill = 1024;  // columns of a -inf span
@@ -57,17 +59,20 @@ constexpr int32_t kPagedTimeout = 1;           // status bit: a bounded wait gav
 constexpr uint64_t kPagedDrainNs = 1000000000ull;  // bound of the last wait before a CTA gives up
 
 // A tile in the ring.
-struct PagedItem {
+struct alignas(16) PagedItem {
+    float scale[kPagedTile];
     int64_t b;
     int32_t tile, row;  // tile -1: the end; row: the CTA's running number of its rows
     int32_t len, pad;
-    uint32_t there[4];  // which keys are there
-    float scale[kPagedTile];
+    uint32_t there[4];  // which keys are there; kTma: which pieces, in the first
 };
 
 // kTok: tokens of a CTA (1, 2 or 4).
-template <int kTok>
+template <int kTok, bool kTma>
 struct PagedShape {
+    static constexpr int kCopyWarps = kTma ? 1 : 4;
+    static constexpr int kMmaWarp = kCopyWarps + kPagedFinishWarps, kFillWarp = kMmaWarp + 1;
+    static constexpr int kThreads = 32 * (kFillWarp + 1);
     static constexpr int kStages = kTok == 4 ? 3 : 4;
     // What is known of a tile outlives its keys: when the copies of tile j + kItems begin, tile j + 3 is
     // multiplied, so tile j + 1 is finished, and all finishing warps have seen tile j.
@@ -107,13 +112,28 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t addr, uint32_t (&r)[32])
         : "memory");
 }
 
-template <int kTok>
-__global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
-    paged_logits_kernel(const __grid_constant__ PagedLogitsParams p)
+// Two floats' fused multiply-add in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
-    using S = PagedShape<kTok>;
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+template <int kTok, bool kTma>
+__global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<kTok, kTma>::kCtasPerSm)
+    paged_logits_kernel(const __grid_constant__ PagedLogitsParams p,
+                        const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_q)
+{
+    using S = PagedShape<kTok, kTma>;
+    constexpr int kScanWarps = kPagedScanThreads / 32;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t s_scan[kPagedCopyWarps], s_first[2];
+    __shared__ int64_t s_scan[kPagedScanThreads / 32], s_first[2];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int32_t s_stop;
     uint8_t* const smem =
@@ -140,9 +160,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
         const int32_t n = tiles(b);
         return int64_t(n) * c_tile + int64_t(fills(n)) * c_fill;
     };
-    const int64_t per = (p.B + kPagedCopyThreads - 1) / kPagedCopyThreads;
+    const int64_t per = (p.B + kPagedScanThreads - 1) / kPagedScanThreads;
     int64_t sum = 0, scan = 0;
-    if (tid < kPagedCopyThreads) {
+    if (tid < kPagedScanThreads) {
         const int64_t b1 = min(per * (tid + 1), p.B);
         for (int64_t b = per * tid; b < b1; ++b) sum += cost(b);
         scan = sum;
@@ -155,20 +175,20 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
     }
 
     // ---- tensor memory and barriers
-    if (warp == kPagedMmaWarp) {
+    if (warp == S::kMmaWarp) {
         // the permit is given up at once: while a CTA holds it, the SM's next CTA waits in its alloc
         ptx::tmem_alloc(ptx::smem_addr(&s_tmem), S::kTmemCols);
         ptx::tmem_relinquish();
         if (lane == 0) {
             for (int i = 0; i < S::kStages; ++i) {
-                ptx::mbar_init(bar(S::kFull + i), kPagedCopyWarps);
+                ptx::mbar_init(bar(S::kFull + i), S::kCopyWarps);
                 ptx::mbar_init(bar(S::kEmpty + i), 1);
             }
             for (int i = 0; i < 2; ++i) {
                 ptx::mbar_init(bar(S::kAccFull + i), 1);
                 ptx::mbar_init(bar(S::kAccEmpty + i), 4);
             }
-            for (int i = 0; i < S::kItems; ++i) ptx::mbar_init(bar(S::kItem + i), kPagedCopyWarps);
+            for (int i = 0; i < S::kItems; ++i) ptx::mbar_init(bar(S::kItem + i), S::kCopyWarps);
             for (int i = 0; i < S::kSlots; ++i)
                 ptx::mbar_init(bar(S::kSlotEmpty + i), kPagedFinishWarps);
             ptx::mbar_init_fence();
@@ -181,12 +201,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
     const uint32_t tmem = s_tmem;
     int64_t total = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < kPagedCopyWarps; ++w) {
+    for (int w = 0; w < kScanWarps; ++w) {
         if (w == warp) before = total + scan - sum;
         total += s_scan[w];
     }
     const int64_t from = blockIdx.x * total / gridDim.x, to = (blockIdx.x + 1) * total / gridDim.x;
-    if (tid < kPagedCopyThreads && before <= from && from < before + sum) {
+    if (tid < kPagedScanThreads && before <= from && from < before + sum) {
         int64_t b = per * tid, at = before;
         for (;; ++b) {
             const int64_t c = cost(b);
@@ -212,6 +232,13 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
         }
         return true;
     };
+    // Waits for what is under way, whether or not the CTA gives up, for kPagedDrainNs at most.
+    auto drain = [&](uint32_t at, uint32_t parity) {
+        const uint64_t start = ptx::globaltimer_ns();
+        while (!ptx::mbar_try_wait_sleep(at, parity, 20000) &&
+               ptx::globaltimer_ns() - start <= kPagedDrainNs) {
+        }
+    };
     // The same for all lanes of a warp: they go on or give up together.
     auto wait_warp = [&](int i, uint32_t parity) { return __all_sync(~0u, wait(i, parity)) != 0; };
     // Items i of a share that begin in [from, to), of n items of cost c each from `at` on.
@@ -222,7 +249,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
 
     if (from >= to) {
         // nothing to do
-    } else if (warp < kPagedCopyWarps) {
+    } else if (warp < S::kCopyWarps) {
         // ------------------------------------------------------------ copy
         int64_t b = s_first[0], at = s_first[1];  // the next row, the cost before it
         int64_t cur_b = 0;
@@ -246,8 +273,11 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
                 first = true;
             }
             if (first) ++row;
-            const int32_t n = tile * kPagedTile + tid;
-            if (!(n < len && locate(p.keys, p.table, cur_b, n, &page, &page_row))) page = -1;
+            // kTma: a lane's piece, else its key
+            const int32_t n = tile * kPagedTile + (kTma ? lane << p.box_shift : tid);
+            if (!((!kTma || lane < kPagedTile >> p.box_shift) && n < len &&
+                  locate(p.keys, p.table, cur_b, n, &page, &page_row)))
+                page = -1;
         };
         int32_t reported = 0;
         auto report = [&](int32_t end) {  // this warp's parts of the tiles before `end` are there
@@ -269,7 +299,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
                 !(ok = wait_warp(S::kEmpty + stage, uint32_t(j / S::kStages - 1) & 1u)))
                 break;
             PagedItem& item = items[j % S::kItems];
-            if (tid == 0) {
+            if (warp == 0 && lane == 0) {
                 item.b = cur_b;
                 item.tile = tile;
                 item.row = row;
@@ -280,7 +310,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
                 const int slot = row % S::kSlots;
                 if (row >= S::kSlots) {
                     const uint32_t parity = uint32_t(row / S::kSlots - 1) & 1u;
-                    if (!__all_sync(~0u, ptx::mbar_try_wait(bar(S::kSlotEmpty + slot), parity))) {
+                    if (!kTma && !__all_sync(~0u, ptx::mbar_try_wait(bar(S::kSlotEmpty + slot), parity))) {
                         // rows of a tile or two: the slot may wait for tiles not reported yet
                         copy_wait<0>();
                         report(j);
@@ -288,11 +318,38 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
                     if (!(ok = wait_warp(S::kSlotEmpty + slot, parity))) break;
                 }
                 const int64_t q0 = (cur_b * p.T + t0) * kPagedHeads;
-                for (int i = tid; i < n_tok * kPagedHeads * 8; i += kPagedCopyThreads)
+                for (int i = tid; !kTma && i < n_tok * kPagedHeads * 8; i += 32 * S::kCopyWarps)
                     copy16(base + S::kOffQ + slot * S::kQBytes + i / 8 * 128 + 16 * (i % 8 ^ (i / 8 & 7)),
                            p.q + (q0 + i / 8) * kPagedDim + 16 * (i % 8), true);
-                for (int i = tid; i < n_tok * kPagedHeads / 4; i += kPagedCopyThreads)
+                for (int i = tid; !kTma && i < n_tok * kPagedHeads / 4; i += 32 * S::kCopyWarps)
                     copy16(base + S::kOffW + slot * S::kN * 4 + 16 * i, p.w + q0 + 4 * i, true);
+            }
+            if constexpr (kTma) {
+                const bool have = page >= 0;
+                const uint32_t pieces = __ballot_sync(~0u, have);
+                const int slot = row % S::kSlots;
+                const uint32_t full = bar(S::kFull + stage), seen = bar(S::kItem + j % S::kItems);
+                const uint32_t n_rows = uint32_t(__popc(pieces)) << p.box_shift;
+                if (lane == 0) {
+                    item.there[0] = pieces;
+                    ptx::mbar_arrive_expect_tx(full, n_rows * kPagedDim + (first ? S::kQBytes : 0u));
+                    ptx::mbar_arrive_expect_tx(seen, n_rows * 4 + (first ? n_tok * kPagedHeads * 4 : 0u));
+                }
+                __syncwarp();
+                if (have) {
+                    ptx::tma_load_2d(base + stage * S::kKBytes + (lane << p.box_shift) * kPagedDim, &map_k,
+                                     full, 0, int32_t(uint32_t(page) * p.page_rows + page_row));
+                    ptx::bulk_load(ptx::smem_addr(&item.scale[lane << p.box_shift]),
+                                   p.keys.scale + page * p.keys.scale_page_stride + page_row,
+                                   4u << p.box_shift, seen);
+                }
+                if (first && lane == 31) {
+                    const int64_t q0 = (cur_b * p.T + t0) * kPagedHeads;
+                    ptx::tma_load_2d(base + S::kOffQ + slot * S::kQBytes, &map_q, full, 0, int32_t(q0));
+                    ptx::bulk_load(base + S::kOffW + slot * S::kN * 4, p.w + q0, n_tok * kPagedHeads * 4, seen);
+                }
+                next();
+                continue;
             }
             const bool there = page >= 0;
             const uint32_t place = there ? page * p.units.page + page_row * p.units.row : kNoRow;
@@ -318,11 +375,24 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
             copy_wait<kPagedAhead>();
             report(j - kPagedAhead + 1);
         }
-        copy_wait<0>();
-        if (ok) report(j + 1);  // the last tiles, and the end
-    } else if (warp < kPagedMmaWarp) {
+        if constexpr (kTma) {
+            if (ok && lane == 0) {  // the end
+                ptx::mbar_arrive(bar(S::kFull + j % S::kStages));
+                ptx::mbar_arrive(bar(S::kItem + j % S::kItems));
+            }
+            // the copies under way land before this CTA's memory goes, whoever gave up
+            for (int32_t i = max(0, j - S::kStages + (ok ? 1 : 0)); i < j; ++i) {
+                drain(bar(S::kFull + i % S::kStages), uint32_t(i / S::kStages) & 1u);
+                drain(bar(S::kItem + i % S::kItems), uint32_t(i / S::kItems) & 1u);
+            }
+        } else {
+            copy_wait<0>();
+            if (ok) report(j + 1);  // the last tiles, and the end
+        }
+    } else if (warp < S::kMmaWarp) {
         // ------------------------------------------------------------ finish
-        const int quarter = warp % 4, parity = warp / 4 % 2;  // TMEM lanes, and tiles
+        // a warp reads the TMEM lanes of its number modulo 4
+        const int quarter = warp % 4, parity = (warp - S::kCopyWarps) / 4;
         int32_t row = 0;
         for (int32_t j = 0;; ++j) {
             if (!wait_warp(S::kItem + j % S::kItems, uint32_t(j / S::kItems) & 1u)) break;
@@ -337,7 +407,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
             const int64_t b = item.b;
             const int32_t n = tile * kPagedTile + quarter * 32 + lane, len = item.len;
             const float scale = item.scale[quarter * 32 + lane];
-            const bool there = item.there[quarter] >> lane & 1u;
+            const bool there = kTma ? item.there[0] >> ((quarter * 32 + lane) >> p.box_shift) & 1u
+                                    : item.there[quarter] >> lane & 1u;
             const int64_t len_full = __ldg(p.lens + b);
             const float* const w =
                 reinterpret_cast<const float*>(smem + S::kOffW) + row % S::kSlots * S::kN;
@@ -349,25 +420,27 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
                 if (t >= n_tok) break;
                 uint32_t x[kPagedHeads];
                 tmem_ld_32(tmem + (uint32_t(quarter * 32) << 16) + (j & 1) * S::kN + t * kPagedHeads, x);
-                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                float2 y0 = make_float2(0.0f, 0.0f), y1 = y0;
 #pragma unroll
                 for (int h = 0; h < kPagedHeads; h += 4) {
                     const float4 wh = *reinterpret_cast<const float4*>(w + t * kPagedHeads + h);
-                    y[0] = fmaf(fmaxf(__uint_as_float(x[h]), 0.0f), wh.x, y[0]);
-                    y[1] = fmaf(fmaxf(__uint_as_float(x[h + 1]), 0.0f), wh.y, y[1]);
-                    y[2] = fmaf(fmaxf(__uint_as_float(x[h + 2]), 0.0f), wh.z, y[2]);
-                    y[3] = fmaf(fmaxf(__uint_as_float(x[h + 3]), 0.0f), wh.w, y[3]);
+                    y0 = fma2(make_float2(fmaxf(__uint_as_float(x[h]), 0.0f),
+                                          fmaxf(__uint_as_float(x[h + 1]), 0.0f)),
+                              make_float2(wh.x, wh.y), y0);
+                    y1 = fma2(make_float2(fmaxf(__uint_as_float(x[h + 2]), 0.0f),
+                                          fmaxf(__uint_as_float(x[h + 3]), 0.0f)),
+                              make_float2(wh.z, wh.w), y1);
                 }
                 const bool seen = n < len && n < len_full - (p.T - 1 - (t0 + t));
                 if (n < p.N && (seen || p.clean))
-                    __stcs(out, seen && there ? ((y[0] + y[1]) + (y[2] + y[3])) * scale
+                    __stcs(out, seen && there ? ((y0.x + y0.y) + (y1.x + y1.y)) * scale
                                               : -CUDART_INF_F);
             }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(S::kAccEmpty + (j & 1)));
         }
-    } else if (warp == kPagedMmaWarp) {
+    } else if (warp == S::kMmaWarp) {
         // ------------------------------------------------------------ multiply
         if (lane == 0) {
             int32_t j = 0;
@@ -388,14 +461,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
                 ptx::mma_commit(bar(S::kAccFull + (j & 1)));
             }
             // all MMAs are done before their tensor memory is freed
-            if (j > 0) {
-                const int i = S::kAccFull + ((j - 1) & 1);
-                const uint32_t parity = uint32_t((j - 1) >> 1) & 1u;
-                const uint64_t start = ptx::globaltimer_ns();
-                while (!ptx::mbar_try_wait_sleep(bar(i), parity, 20000) &&
-                       ptx::globaltimer_ns() - start <= kPagedDrainNs) {
-                }
-            }
+            if (j > 0) drain(bar(S::kAccFull + ((j - 1) & 1)), uint32_t((j - 1) >> 1) & 1u);
         }
         __syncwarp();
     } else if (p.clean) {
@@ -427,7 +493,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<kTok>::kCtasPerSm)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == kPagedMmaWarp) ptx::tmem_dealloc(tmem, S::kTmemCols);
+    if (warp == S::kMmaWarp) ptx::tmem_dealloc(tmem, S::kTmemCols);
 }
 
 }  // namespace fp8mqa
