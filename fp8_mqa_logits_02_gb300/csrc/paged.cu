@@ -160,6 +160,45 @@ bool row_units(const PagedView& v, RowUnits* u)
 
 int launched() { return cudaGetLastError() == cudaSuccess ? FP8MQA_OK : FP8MQA_ERR_LAUNCH; }
 
+// Rows of x that start on 16 bytes are read 16 bytes at a time, others value by value.
+template <class X, int kDim, int kTensors>
+void write_tensors(const CacheWriteParams& p, cudaStream_t s)
+{
+    const int64_t rows = p.T * p.heads, per = kCacheThreads / (kDim / 16);
+    const unsigned blocks = unsigned((rows + per - 1) / per);
+    bool vec = true;
+    for (int i = 0; i < kTensors; ++i)
+        vec = vec && on(p.x[i], 16) && p.row_stride[i] * int64_t(sizeof(X)) % 16 == 0 &&
+              p.head_stride[i] * int64_t(sizeof(X)) % 16 == 0;
+    if (vec)
+        cache_write_kernel<X, kDim, true, kTensors><<<blocks, kCacheThreads, 0, s>>>(p);
+    else
+        cache_write_kernel<X, kDim, false, kTensors><<<blocks, kCacheThreads, 0, s>>>(p);
+}
+
+template <class X>
+void write_rows(const CacheWriteParams& p, int32_t dim, int tensors, cudaStream_t s)
+{
+    if (dim == 64)
+        tensors == 1 ? write_tensors<X, 64, 1>(p, s) : write_tensors<X, 64, 2>(p, s);
+    else
+        tensors == 1 ? write_tensors<X, 128, 1>(p, s) : write_tensors<X, 128, 2>(p, s);
+}
+
+// A block packs about kReadPieces pieces a thread.
+template <class Out>
+void read_rows(CacheReadParams& p, int32_t dim, cudaStream_t s)
+{
+    const int64_t row_pieces = int64_t(p.cache.heads) * dim * int64_t(sizeof(Out)) / 16;
+    p.block_rows = int32_t(std::max<int64_t>(
+        1, std::min<int64_t>(kReadRows, kReadPieces * kCacheThreads / row_pieces)));
+    const unsigned blocks = unsigned((p.total + p.block_rows - 1) / p.block_rows);
+    if (dim == 64)
+        cache_read_kernel<Out, 64><<<blocks, kCacheThreads, 0, s>>>(p);
+    else
+        cache_read_kernel<Out, 128><<<blocks, kCacheThreads, 0, s>>>(p);
+}
+
 // Key heads that a CTA's warps take: side by side (up to four) where a CTA gets kAttnHeadTiles
 // tiles or more that way, else one, with four steps of its positions (fewer partial results).
 // Measured: 90 tiles a CTA (64 rows of up to 20001, 8 heads) 230 us side by side, 244 one by one;
@@ -300,8 +339,8 @@ int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const v
     p.slots = slots;
     p.T = T;
     p.heads = cache->heads;
-    p.dim = cache->dim;
-    p.tensors = x2 ? 2 : 1;
+    p.by_heads = FastDiv(uint32_t(p.heads));
+    p.by_page = FastDiv(uint32_t(cache->page_size));
     p.x[0] = x;
     p.x[1] = x2;
     p.row_stride[0] = x_row_stride;
@@ -310,14 +349,13 @@ int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const v
     p.head_stride[1] = x2_head_stride;
     p.cache[0] = view_of(*cache);
     p.cache[1] = view_of(cache2 ? *cache2 : *cache);
-    const int64_t blocks = (T * p.heads * p.tensors + 7) / 8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (x_type == FP8MQA_BF16)
-        cache_write_kernel<__nv_bfloat16><<<unsigned(blocks), 256, 0, s>>>(p);
+        write_rows<__nv_bfloat16>(p, cache->dim, x2 ? 2 : 1, s);
     else if (x_type == FP8MQA_F16)
-        cache_write_kernel<__half><<<unsigned(blocks), 256, 0, s>>>(p);
+        write_rows<__half>(p, cache->dim, x2 ? 2 : 1, s);
     else
-        cache_write_kernel<float><<<unsigned(blocks), 256, 0, s>>>(p);
+        write_rows<float>(p, cache->dim, x2 ? 2 : 1, s);
     return launched();
 }
 
@@ -347,19 +385,18 @@ int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t 
     p.starts = starts;
     p.B = B;
     p.total = total;
-    p.dim = cache->dim;
+    p.by_heads = FastDiv(uint32_t(cache->heads));
     p.out = out;
     p.out_scale = out_scale;
-    const unsigned blocks = unsigned((total * cache->heads + 7) / 8);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (out_type == FP8MQA_E4M3)
-        cache_read_kernel<uint8_t><<<blocks, 256, 0, s>>>(p);
+        read_rows<uint8_t>(p, cache->dim, s);
     else if (out_type == FP8MQA_BF16)
-        cache_read_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(p);
+        read_rows<__nv_bfloat16>(p, cache->dim, s);
     else if (out_type == FP8MQA_F16)
-        cache_read_kernel<__half><<<blocks, 256, 0, s>>>(p);
+        read_rows<__half>(p, cache->dim, s);
     else
-        cache_read_kernel<float><<<blocks, 256, 0, s>>>(p);
+        read_rows<float>(p, cache->dim, s);
     return launched();
 }
 

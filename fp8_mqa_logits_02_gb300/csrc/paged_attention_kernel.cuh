@@ -99,13 +99,6 @@ struct AttnShape {
     static_assert(kHeads * kDim * 4 <= kRing, "the warps' results take the rings' place");
 };
 
-__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t two)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(two)));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 {
     uint32_t r;

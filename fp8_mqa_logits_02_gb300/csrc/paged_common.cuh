@@ -67,11 +67,12 @@ __device__ __forceinline__ bool locate(const PagedView& c, const PageTable& t, i
     return uint32_t(*page) < uint32_t(c.pages);
 }
 
-__device__ __forceinline__ float e4m3_to_float(uint8_t v)
+// Two E4M3 values (the low 16 bits) as two f16 values: exact.
+__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t two)
 {
-    __nv_fp8_e4m3 x;
-    x.__x = v;
-    return float(x);
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(two)));
+    return r;
 }
 
 template <class T>
@@ -80,8 +81,6 @@ template <>
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 template <>
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_float(__nv_fp8_e4m3 x) { return float(x); }
 
 template <class T>
 __device__ __forceinline__ T from_float(float x);

@@ -23,50 +23,56 @@ _TYPE = {_E4M3: 0, torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
 _pack_cache = struct.Struct("@PPqiiiiqqqqqq").pack  # struct fp8mqa_cache
 
 
-def _cuda(t, name, device=None):
+# A call's checks cost about as much as its launch, so each looks at a tensor's attributes once and
+# states what is wrong only after it knows that something is.
+def _cuda(t, name):
+    """The device of a CUDA tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if device is not None and t.device != device:
+    return t.device
+
+
+def _on_device(t, name, device):
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        _cuda(t, name)
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t
 
 
-def _ints(t, name, device, shape):
-    """An int32 tensor of ``shape`` (None: any size) whose last dimension is contiguous."""
-    _cuda(t, name, device)
+def _ints(t, name, device, *shape):
+    """Checks an int32 tensor of ``shape`` (None: any size) whose last dimension is contiguous."""
+    _on_device(t, name, device)
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32, got {t.dtype}")
     got = t.shape
-    if len(got) != len(shape) or any(n is not None and n != m for n, m in zip(shape, got)):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(got)}")
+    if len(got) != len(shape) or (shape[0] is not None and got[0] != shape[0]):
+        want = ["any" if n is None else n for n in shape]
+        raise ValueError(f"{name} must be {want}, got {list(got)}")
     if got[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t
 
 
-def _cache(data, scale, name, device, types=(_E4M3,)):
-    """(the packed fp8mqa_cache, the data's shape)."""
-    _cuda(data, f"{name} data", device)
-    if data.dtype not in types:
-        raise TypeError(f"{name} data must have dtype in {types}, got {data.dtype}")
-    shape = data.shape
+def _cache(data, scale, name, device, other=None):
+    """(the packed fp8mqa_cache, the data's shape); e4m3, or the type ``other``."""
+    _on_device(data, f"{name} data", device)
+    dtype, shape, stride = data.dtype, data.shape, data.stride()
     if len(shape) != 4:
         raise ValueError(f"{name} data must be [pages, page_size, heads, dim], got {list(shape)}")
-    stride = data.stride()
     if stride[3] != 1:
         raise ValueError(f"{name} data must be contiguous in its last dimension")
-    if data.dtype == _E4M3:
-        _cuda(scale, f"{name} scale", device)
+    if dtype == _E4M3:
+        _on_device(scale, f"{name} scale", device)
         if scale.dtype != torch.float32 or scale.shape != shape[:3]:
             raise ValueError(f"{name} scale must be float32 {list(shape[:3])}")
-        at, by = scale.data_ptr(), scale.stride()
+        at, (a, b, c) = scale.data_ptr(), scale.stride()
     else:
+        if other is None or dtype != other:
+            raise TypeError(f"{name} data must be {_E4M3}{'' if other is None else f' or {other}'}, got {dtype}")
         if scale is not None:
             raise ValueError(f"{name} scale goes with float8_e4m3fn data only")
-        at, by = 0, (0, 0, 0)
-    return _pack_cache(data.data_ptr(), at, *shape, _TYPE[data.dtype], *stride[:3], *by), shape
+        at = a = b = c = 0
+    return _pack_cache(data.data_ptr(), at, *shape, _TYPE[dtype], stride[0], stride[1], stride[2], a, b, c), shape
 
 
 def _call(name, device, stream, *args):
@@ -85,11 +91,11 @@ def _empty(shape, dtype, device, stream):
 
 def _rows(x, name, device, shape, dtype=None):
     """x [tokens, heads, dim] for cache_write: its address and strides."""
-    _cuda(x, name, device)
+    _on_device(x, name, device)
     if x.dtype not in _TYPE or x.dtype == _E4M3 or (dtype is not None and x.dtype != dtype):
         raise TypeError(f"{name} must be bfloat16, float16 or float32"
                         f"{'' if dtype is None else ' as k is'}, got {x.dtype}")
-    if len(x.shape) != 3 or tuple(x.shape) != shape:
+    if x.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(x.shape)}")
     stride = x.stride()
     if stride[2] != 1:
@@ -107,9 +113,9 @@ def cache_write(slots: torch.Tensor, k: torch.Tensor, k_data: torch.Tensor, k_sc
     may be strided.  Each row gets the scale max|x| / 448 (at least 1e-30 / 448) and the e4m3
     values nearest to x / scale; a row with a NaN or an infinity reads back as NaN.
     """
-    dev = _cuda(k_data, "k data").device
+    dev = _cuda(k_data, "k data")
     cache, shape = _cache(k_data, k_scale, "k", dev)
-    _ints(slots, "slots", dev, (None,))
+    _ints(slots, "slots", dev, None)
     rows = (slots.shape[0], shape[2], shape[3])
     x = _rows(k, "k", dev, rows)
     if (v is None) != (v_data is None) or (v is None) != (v_scale is None):
@@ -136,10 +142,11 @@ def cache_read(data: torch.Tensor, scale: torch.Tensor, table: torch.Tensor, sta
     after ``squeeze(1)``; otherwise rows of ``dtype``, values times scale.  Rows whose page is not
     there are zero.
     """
-    dev = _cuda(data, "data").device
+    dev = _cuda(data, "data")
     cache, shape = _cache(data, scale, "cache", dev)
-    _ints(table, "table", dev, (None, None))
-    _ints(starts, "starts", dev, (table.shape[0] + 1,))
+    _ints(table, "table", dev, None, None)
+    rows, cols = table.shape
+    _ints(starts, "starts", dev, rows + 1)
     if dtype not in _TYPE:
         raise TypeError(f"dtype must be one of {list(_TYPE)}, got {dtype}")
     total = int(total)
@@ -147,8 +154,8 @@ def cache_read(data: torch.Tensor, scale: torch.Tensor, table: torch.Tensor, sta
         raise ValueError("total must not be negative")
     out = _empty((total, shape[2], shape[3]), dtype, dev, stream)
     scales = _empty((total, shape[2]), torch.float32, dev, stream) if dtype == _E4M3 else None
-    _call("fp8_mqa_cache_read", dev, stream, cache, table.data_ptr(), table.stride(0),
-          table.shape[1], starts.data_ptr(), table.shape[0], total, _TYPE[dtype], out.data_ptr(),
+    _call("fp8_mqa_cache_read", dev, stream, cache, table.data_ptr(), table.stride(0), cols,
+          starts.data_ptr(), rows, total, _TYPE[dtype], out.data_ptr(),
           None if scales is None else scales.data_ptr())
     return out if scales is None else (out, scales)
 
@@ -165,29 +172,38 @@ def logits_paged(q: torch.Tensor, data: torch.Tensor, scale: torch.Tensor, w: to
     n < lens[b] - (T - 1 - t).  Returns float32 [B * T, max_len] (default: all that the table can
     hold), -inf outside (left as they are with ``clean_logits=False``); ``out`` may have strided rows.
     """
-    dev = _cuda(q, "q").device
-    if q.dtype != _E4M3 or len(q.shape) != 4 or q.shape[2:] != (HEADS, DIM) or not q.is_contiguous():
+    dev = _cuda(q, "q")
+    got = q.shape
+    if q.dtype != _E4M3 or len(got) != 4 or got[2] != HEADS or got[3] != DIM or not q.is_contiguous():
         raise ValueError(f"q must be contiguous float8_e4m3fn [B, T, {HEADS}, {DIM}]")
-    B, T = q.shape[:2]
-    _cuda(w, "w", dev)
+    B, T = got[0], got[1]
+    _on_device(w, "w", dev)
     if w.dtype != torch.float32 or w.shape != (B, T, HEADS) or not w.is_contiguous():
         raise ValueError(f"w must be contiguous float32 [{B}, {T}, {HEADS}]")
     cache, shape = _cache(data, scale, "key", dev)
     if shape[2] != 1 or shape[3] != DIM:
         raise ValueError(f"key data must be [pages, page_size, 1, {DIM}]")
-    _ints(table, "table", dev, (B, None))
-    _ints(lens, "lens", dev, (B,))
-    N = table.shape[1] * shape[1] if max_len is None else int(max_len)
+    _ints(table, "table", dev, B, None)
+    _ints(lens, "lens", dev, B)
+    cols = table.shape[1]
+    N = cols * shape[1] if max_len is None else int(max_len)
+    if N < 0:
+        raise ValueError("max_len must not be negative")
     if out is None:
-        out = _empty((B * T, N), torch.float32, dev, stream)
+        out, ld = _empty((B * T, N), torch.float32, dev, stream), N
     else:
-        _cuda(out, "out", dev)
+        _on_device(out, "out", dev)
         if out.dtype != torch.float32 or out.shape != (B * T, N) or (N > 1 and out.stride(1) != 1):
             raise ValueError(f"out must be float32 [{B * T}, {N}] with contiguous rows")
+        ld = out.stride(0) if B * T > 1 else N
     _call("fp8_mqa_logits_paged", dev, stream, q.data_ptr(), w.data_ptr(), B, T, HEADS, DIM, cache,
-          table.data_ptr(), table.stride(0), table.shape[1], lens.data_ptr(), out.data_ptr(),
-          max(out.stride(0), N), N, 1 if clean_logits else 0)
+          table.data_ptr(), table.stride(0), cols, lens.data_ptr(), out.data_ptr(), ld, N,
+          1 if clean_logits else 0)
     return out
+
+
+# Workspace bytes by (device, query heads, key heads, width): they depend on nothing else.
+_workspace = {}
 
 
 def attention_paged(q: torch.Tensor, k_data: torch.Tensor, v_data: torch.Tensor,
@@ -204,31 +220,36 @@ def attention_paged(q: torch.Tensor, k_data: torch.Tensor, v_data: torch.Tensor,
     ignored.  Returns out [B, q_heads, dim] in q's type, and with ``return_lse`` the float32
     [B, q_heads] log of the softmax's sum.  A row with nothing to attend to gives 0 and -inf.
     """
-    dev = _cuda(q, "q").device
-    if q.dtype != torch.bfloat16 and q.dtype != torch.float16:
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    if len(q.shape) != 3 or q.stride(2) != 1:
+    dev, dtype = _cuda(q, "q"), q.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float16:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    if q.dim() != 3 or q.stride(2) != 1:
         raise ValueError("q must be [B, q_heads, dim], contiguous in its last dimension")
     B, heads, dim = q.shape
-    types = (_E4M3, q.dtype)
-    k, shape = _cache(k_data, k_scale, "k", dev, types)
-    v, shape2 = _cache(v_data, v_scale, "v", dev, types)
+    k, shape = _cache(k_data, k_scale, "k", dev, dtype)
+    v, shape2 = _cache(v_data, v_scale, "v", dev, dtype)
     if shape != shape2 or k_data.dtype != v_data.dtype:
         raise ValueError("k data and v data must have one shape and type")
-    if shape[3] != dim or heads == 0 or heads % shape[2]:
+    kv_heads = shape[2]
+    if shape[3] != dim or heads == 0 or kv_heads == 0 or heads % kv_heads:
         raise ValueError(f"q {list(q.shape)} does not go with a cache of {list(shape)}")
-    _ints(table, "table", dev, (B, None))
-    _ints(lens, "lens", dev, (B,))
+    _ints(table, "table", dev, B, None)
+    _ints(lens, "lens", dev, B)
     if indices is None:
         at, by, n = None, 0, -1
     else:
-        _ints(indices, "indices", dev, (B, None))
+        _ints(indices, "indices", dev, B, None)
         at, by, n = indices.data_ptr(), indices.stride(0), indices.shape[1]
-    out = _empty((B, heads, dim), q.dtype, dev, stream)
+    key = (dev.index, heads, kv_heads, dim)
+    need = _workspace.get(key)
+    if need is None:
+        need = _on(dev, _entry("fp8_mqa_attention_paged_workspace_bytes"), heads, kv_heads, dim)
+        if need:
+            _workspace[key] = need
+    out = _empty((B, heads, dim), dtype, dev, stream)
     lse = _empty((B, heads), torch.float32, dev, stream) if return_lse else None
-    need = _on(dev, _entry("fp8_mqa_attention_paged_workspace_bytes"), heads, shape[2], dim)
     space = _empty((need,), torch.uint8, dev, stream)
-    _call("fp8_mqa_attention_paged", dev, stream, q.data_ptr(), _TYPE[q.dtype], B, heads,
+    _call("fp8_mqa_attention_paged", dev, stream, q.data_ptr(), _TYPE[dtype], B, heads,
           q.stride(0), q.stride(1), k, v, table.data_ptr(), table.stride(0), table.shape[1],
           lens.data_ptr(), at, by, n, dim ** -0.5 if sm_scale is None else float(sm_scale),
           out.data_ptr(), None if lse is None else lse.data_ptr(), space.data_ptr(), need)

@@ -310,7 +310,8 @@ typedef struct fp8mqa_cache {
  * or an infinity reads back as NaN, so that it does not pass for data.
  *
  *   slots    DEVICE int32 [T]: page * page_size + row.  A slot outside [0, pages * page_size)
- *            is skipped (padding).  Two tokens with one slot: one of them is written whole.
+ *            is skipped (padding).  Tokens of one call must not share a slot: what such a row
+ *            holds afterwards is unspecified.
  *   x        DEVICE [T, heads, dim] of x_type (BF16, F16 or F32), element (t, h, d) at
  *            t*x_row_stride + h*x_head_stride + d; aligned to its type.
  *   cache    where x goes.

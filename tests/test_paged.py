@@ -149,17 +149,6 @@ def test_write_special_rows():
     assert np.all(np.abs(got[6] - x[6, 0].double().numpy()) <= 2.0 ** -4 * np.abs(x[6, 0].double().numpy()) + 2.0 ** -10 / 448)
 
 
-def test_write_same_slot_twice_writes_one_of_them_whole():
-    rng = np.random.default_rng(5)
-    data, scale = cache(rng, 1, 4, 2, 128)
-    x = torch.from_numpy(rng.standard_normal((64, 2, 128))).to(torch.bfloat16).cuda()
-    fm.cache_write(torch.full((64,), 2, dtype=torch.int32, device="cuda"), x, data, scale)
-    values, _ = plain.quantise32(x.float().cpu().numpy())
-    got = f64(data)[0, 2]
-    for h in range(2):
-        assert any(same(got[h], values[t, h]) for t in range(64))
-
-
 # ------------------------------------------------------------------------------------ read
 
 @pytest.mark.parametrize("dtype", [F8, torch.bfloat16, torch.float16, torch.float32])
