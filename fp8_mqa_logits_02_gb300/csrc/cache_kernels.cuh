@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid
     const int c = threadIdx.x % kLanes;
     const bool row = at < uint32_t(p.T * p.heads);
     const int32_t t = row ? p.by_heads.of(int32_t(at)) : 0, h = row ? int32_t(at) - t * p.heads : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t slot = row ? __ldg(p.slots + t) : -1;
     float v[kTensors][16];
 #pragma unroll
@@ -102,7 +103,11 @@ struct CacheReadParams {
     void* out;
     float* out_scale;
 };
-constexpr int kReadRows = 128, kReadPieces = 8;  // pieces of 16 bytes of output that a thread has under way
+constexpr int kReadRows = 128;
+
+// Pieces of 16 bytes of output that a thread has under way.
+template <class Out>
+constexpr int kReadPieces = sizeof(Out) == 1 ? 4 : 8;
 
 // The sequence of output row r: the last b with starts[b] <= r (B where r is past the end).
 __device__ __forceinline__ int64_t sequence_of(const int32_t* starts, int64_t B, int64_t r)
@@ -125,6 +130,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
     const PagedView& c = p.cache;
     const int64_t r0 = int64_t(blockIdx.x) * p.block_rows;
     const int rows = int(min(int64_t(p.block_rows), p.total - r0));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x < rows) {
         const int64_t r = r0 + threadIdx.x, b = sequence_of(p.starts, p.B, r);
         int32_t page = 0, row = 0;
@@ -137,11 +143,12 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
     constexpr int kPer = 16 / sizeof(Out), kLanes = kDim / kPer;
     const int n = rows * c.heads * kLanes;
     uint4* const out = reinterpret_cast<uint4*>(static_cast<Out*>(p.out) + r0 * c.heads * kDim);
-    for (int i0 = threadIdx.x; i0 < n; i0 += kReadPieces * kCacheThreads) {
-        uint32_t x[kReadPieces][kPer / 4];
-        float by[kReadPieces];
+    constexpr int kPieces = kReadPieces<Out>;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kPieces * kCacheThreads) {
+        uint32_t x[kPieces][kPer / 4];
+        float by[kPieces];
 #pragma unroll
-        for (int j = 0; j < kReadPieces; ++j) {
+        for (int j = 0; j < kPieces; ++j) {
             const int i = i0 + j * kCacheThreads, at = i / kLanes;
 #pragma unroll
             for (int k = 0; k < kPer / 4; ++k) x[j][k] = 0u;
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
             }
         }
 #pragma unroll
-        for (int j = 0; j < kReadPieces; ++j) {
+        for (int j = 0; j < kPieces; ++j) {
             const int i = i0 + j * kCacheThreads;
             if (i >= n) break;
             if constexpr (kPer == 16) {

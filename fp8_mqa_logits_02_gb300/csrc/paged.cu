@@ -44,14 +44,39 @@ int64_t attention_wave(int sm_count)
     return std::min<int64_t>(kAttnMaxCtas, int64_t(sm_count) * kAttnCtasPerSm);
 }
 
-template <int kType, int kDim>
+template <int kType, int kDim, int kNT, int kHq>
 bool attention_smem()
 {
-    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    return cudaFuncSetAttribute(paged_attention_kernel<kType, kDim, 1>, attr,
-                                AttnShape<kType, kDim, 1>::kSmem) == cudaSuccess &&
-           cudaFuncSetAttribute(paged_attention_kernel<kType, kDim, 2>, attr,
-                                AttnShape<kType, kDim, 2>::kSmem) == cudaSuccess;
+    return cudaFuncSetAttribute(paged_attention_kernel<kType, kDim, kNT, kHq>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                AttnShape<kType, kDim, kNT, kHq>::kSmem) == cudaSuccess;
+}
+
+template <int kType>
+bool attention_smem()
+{
+    return attention_smem<kType, 64, 1, 1>() && attention_smem<kType, 64, 2, 1>() &&
+           attention_smem<kType, 64, 2, 2>() && attention_smem<kType, 64, 2, 4>() &&
+           attention_smem<kType, 128, 1, 1>() && attention_smem<kType, 128, 2, 1>() &&
+           attention_smem<kType, 128, 2, 2>() && attention_smem<kType, 128, 2, 4>();
+}
+
+// Launches a kernel that begins with griddepcontrol.wait: it is set up while the one before it ends.
+template <class... Params, class... Args>
+void launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                  const Args&... args)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 void init_paged(int dev, PagedDevice& st)
@@ -68,9 +93,8 @@ void init_paged(int dev, PagedDevice& st)
         st.init_status = FP8MQA_ERR_ARCH;
         return;
     }
-    if (!attention_smem<FP8MQA_E4M3, 64>() || !attention_smem<FP8MQA_E4M3, 128>() ||
-        !attention_smem<FP8MQA_BF16, 64>() || !attention_smem<FP8MQA_BF16, 128>() ||
-        !attention_smem<FP8MQA_F16, 64>() || !attention_smem<FP8MQA_F16, 128>() ||
+    if (!attention_smem<FP8MQA_E4M3>() || !attention_smem<FP8MQA_BF16>() ||
+        !attention_smem<FP8MQA_F16>() ||
         !logits_smem<1>() || !logits_smem<2>() || !logits_smem<4>()) {
         cudaGetLastError();
         st.init_status = FP8MQA_ERR_LAUNCH;
@@ -171,9 +195,9 @@ void write_tensors(const CacheWriteParams& p, cudaStream_t s)
         vec = vec && on(p.x[i], 16) && p.row_stride[i] * int64_t(sizeof(X)) % 16 == 0 &&
               p.head_stride[i] * int64_t(sizeof(X)) % 16 == 0;
     if (vec)
-        cache_write_kernel<X, kDim, true, kTensors><<<blocks, kCacheThreads, 0, s>>>(p);
+        launch_after(cache_write_kernel<X, kDim, true, kTensors>, dim3(blocks), kCacheThreads, 0, s, p);
     else
-        cache_write_kernel<X, kDim, false, kTensors><<<blocks, kCacheThreads, 0, s>>>(p);
+        launch_after(cache_write_kernel<X, kDim, false, kTensors>, dim3(blocks), kCacheThreads, 0, s, p);
 }
 
 template <class X>
@@ -191,12 +215,12 @@ void read_rows(CacheReadParams& p, int32_t dim, cudaStream_t s)
 {
     const int64_t row_pieces = int64_t(p.cache.heads) * dim * int64_t(sizeof(Out)) / 16;
     p.block_rows = int32_t(std::max<int64_t>(
-        1, std::min<int64_t>(kReadRows, kReadPieces * kCacheThreads / row_pieces)));
+        1, std::min<int64_t>(kReadRows, kReadPieces<Out> * kCacheThreads / row_pieces)));
     const unsigned blocks = unsigned((p.total + p.block_rows - 1) / p.block_rows);
     if (dim == 64)
-        cache_read_kernel<Out, 64><<<blocks, kCacheThreads, 0, s>>>(p);
+        launch_after(cache_read_kernel<Out, 64>, dim3(blocks), kCacheThreads, 0, s, p);
     else
-        cache_read_kernel<Out, 128><<<blocks, kCacheThreads, 0, s>>>(p);
+        launch_after(cache_read_kernel<Out, 128>, dim3(blocks), kCacheThreads, 0, s, p);
 }
 
 // Key heads that a CTA's warps take: side by side (up to four) where a CTA gets kAttnHeadTiles
@@ -205,48 +229,48 @@ void read_rows(CacheReadParams& p, int32_t dim, cudaStream_t s)
 // 19 (16 rows of up to 16385, 4 heads, 16 bits) 62.6 and 60.5; 9 (64 rows of 2048 selected) 53 and 48.
 constexpr int64_t kAttnHeadTiles = 32;
 
-// A CTA takes 8 query heads of each key head, or 16 where a group has more than 8; the grid is a
-// full wave, or fewer where there are fewer tiles, and a multiple of the chunks of heads.
-template <int kType, int kDim, int kNT>
+// The grid is a full wave, or fewer CTAs where there are fewer tiles, and a multiple of the chunks of
+// heads.
+template <int kType, int kDim, int kNT, int kHq>
 void attention_launch(PagedAttentionParams& p, int sm_count, cudaStream_t s)
 {
-    using S = AttnShape<kType, kDim, kNT>;
-    const int64_t group = p.q_heads / p.k.heads, parts = (group + S::kHeads - 1) / S::kHeads;
+    using S = AttnShape<kType, kDim, kNT, kHq>;
+    const int block = kHq * S::kHeads;
+    const int64_t group = p.q_heads / p.k.heads, parts = (group + block - 1) / block;
     const int64_t wave = attention_wave(sm_count);
     const int64_t longest =
         std::max<int64_t>(1, p.n_indices >= 0 ? p.n_indices : int64_t(p.table.cols) * p.k.page_size);
     p.hw = p.k.heads % 4 == 0 ? 4 : p.k.heads % 2 == 0 ? 2 : 1;
+    p.hw = std::min(p.hw, kAttnWarps / kHq);
     int64_t tile, chunks, tiles;
     for (;; p.hw = 1) {
-        tile = S::kStep * (kAttnWarps / p.hw);
+        tile = S::kStep * (kAttnWarps / (p.hw * kHq));
         chunks = p.k.heads / p.hw * parts;
         tiles = p.B * ((longest + tile - 1) / tile);
         if (p.hw == 1 || tiles * chunks >= kAttnHeadTiles * wave) break;
     }
     const int64_t per_chunk = std::min(tiles, std::max<int64_t>(1, wave / chunks));
-    paged_attention_kernel<kType, kDim, kNT>
-        <<<unsigned(per_chunk * chunks), kAttnThreads, S::kSmem, s>>>(p);
+    launch_after(paged_attention_kernel<kType, kDim, kNT, kHq>, dim3(unsigned(per_chunk * chunks)),
+                 kAttnThreads, S::kSmem, s, p);
     if (per_chunk == 1) return;  // nothing is split
-    // the join is set up while the first kernel runs
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(per_chunk - 1), unsigned(chunks * p.hw * kNT));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, paged_attention_join_kernel<kDim>, p, S::kHeads, int(per_chunk));
+    const dim3 grid(unsigned(per_chunk - 1), unsigned(chunks * p.hw * kHq * kNT));
+    launch_after(paged_attention_join_kernel<kDim>, grid, kJoinThreads, 0, s, p, block, int(per_chunk));
 }
 
+// A warp takes up to 8 query heads of a group, or 16; groups of more than 16 go to two or four warps
+// that share a ring.
 template <int kType, int kDim>
 void attention_heads(PagedAttentionParams& p, int sm_count, cudaStream_t s)
 {
-    if (p.q_heads / p.k.heads <= 8)
-        attention_launch<kType, kDim, 1>(p, sm_count, s);
+    const int group = p.q_heads / p.k.heads;
+    if (group <= 8)
+        attention_launch<kType, kDim, 1, 1>(p, sm_count, s);
+    else if (group <= 16)
+        attention_launch<kType, kDim, 2, 1>(p, sm_count, s);
+    else if (group <= 32)
+        attention_launch<kType, kDim, 2, 2>(p, sm_count, s);
     else
-        attention_launch<kType, kDim, 2>(p, sm_count, s);
+        attention_launch<kType, kDim, 2, 4>(p, sm_count, s);
 }
 
 template <int kType>
@@ -288,11 +312,10 @@ void logits_launch(PagedLogitsParams& p, int sm_count, cudaStream_t s)
     const dim3 grid(unsigned(std::min(work, wave)), unsigned((p.T + kTok - 1) / kTok));
     CUtensorMap map_k = {}, map_q = {};
     if (paged_maps(p, kTok, &map_k, &map_q))
-        paged_logits_kernel<kTok, true>
-            <<<grid, S::kThreads, S::kSmem, s>>>(p, map_k, map_q);
+        launch_after(paged_logits_kernel<kTok, true>, grid, S::kThreads, S::kSmem, s, p, map_k, map_q);
     else
-        paged_logits_kernel<kTok, false>
-            <<<grid, PagedShape<kTok, false>::kThreads, PagedShape<kTok, false>::kSmem, s>>>(p, map_k, map_q);
+        launch_after(paged_logits_kernel<kTok, false>, grid, PagedShape<kTok, false>::kThreads,
+                     PagedShape<kTok, false>::kSmem, s, p, map_k, map_q);
 }
 
 }  // namespace
@@ -456,8 +479,11 @@ uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t kv_hea
     if (!st) return 0;
     // two partial results a CTA (heads x dim sums, and each head's m and l); a launch with more
     // chunks of heads than a wave has CTAs splits no row
-    const uint64_t heads = uint64_t(kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1) *
-                           (q_heads / kv_heads <= 8 ? 8 : kAttnMaxHeads);
+    const int32_t group = q_heads / kv_heads;
+    const uint64_t heads = group > 32   ? 64
+                           : group > 16 ? 32 * (kv_heads % 2 == 0 ? 2 : 1)
+                                        : (group > 8 ? 16 : 8) *
+                                              (kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1);
     return kAttnMaxCtas * sizeof(AttnSplit) +
            2 * uint64_t(attention_wave(st->sm_count)) * heads * uint64_t(dim + 2) * sizeof(float);
 }

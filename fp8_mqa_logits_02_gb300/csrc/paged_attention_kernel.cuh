@@ -25,9 +25,10 @@
 // unrounded); their value scales are taken relative to a running power of two, so the largest
 // keep their 11 bits whatever the scales' size.
 //
-// A CTA's four warps take hw heads (1, 2 or 4) of the same positions, 4 / hw steps of positions
-// each, and keep in step: the heads of a position lie side by side in memory, and reading them
-// together is what DRAM wants.
+// A CTA's four warps take hw key heads (1, 2 or 4) of the same positions and keep in step: the heads
+// of a position lie side by side in memory, and reading them together is what DRAM wants.  Groups of
+// more than 16 query heads are shared out to kHq warps that read one ring, so that the cache's bytes
+// reach an SM once for 32 or 64 heads.  The warps left over (4 / (hw kHq)) take further positions.
 //
 // Split and join: for each chunk of heads the rows' tiles (the CTA's steps) are laid end to end,
 // and its CTAs take equal shares of them; the CTAs of one share number follow one another in the
@@ -43,10 +44,9 @@
 namespace fp8mqa {
 
 constexpr int kAttnThreads = 128, kAttnWarps = kAttnThreads / 32;
-constexpr int kAttnStages = 2;     // steps in a warp's ring
+constexpr int kAttnStages = 2;     // steps in a ring, for each warp that shares it
 constexpr int kAttnCtasPerSm = 3;
 constexpr int kAttnMaxCtas = 512;  // of one launch
-constexpr int kAttnMaxHeads = 16;  // query heads of a key head that a CTA takes
 
 // What CTA `me` of a chunk (me > 0) says of the row that its share begins within: the row's parts
 // are those of CTAs first .. first + parts - 1.  parts = 0: its share begins with a row.
@@ -77,12 +77,14 @@ struct PagedAttentionParams {
     AttnSplit* splits;  // [CTAs of a chunk]
 };
 
-// kType: FP8MQA_E4M3, FP8MQA_BF16 or FP8MQA_F16 of the cache.
-template <int kType, int kDim_, int kNT_>
+// kType: FP8MQA_E4M3, FP8MQA_BF16 or FP8MQA_F16 of the cache.  kNT: eights of heads of a warp.
+// kHq: warps that share a ring, for 8 kNT heads each of one key head.
+template <int kType, int kDim_, int kNT_, int kHq>
 struct AttnShape {
     static constexpr bool kE4m3 = kType == 0, kBf16 = kType == 1;
     static constexpr int kDim = kDim_, kNT = kNT_;
-    static constexpr int kHeads = 8 * kNT;             // heads of a unit
+    static constexpr int kHeads = 8 * kNT;             // heads of a warp
+    static constexpr int kStages = kAttnStages * kHq;
     static constexpr int kStep = kE4m3 ? 32 : 16;      // positions of a warp's step
     static constexpr int kBlocks = kStep / 16;         // of 16 positions
     static constexpr int kRowBytes = kDim * (kE4m3 ? 1 : 2);
@@ -94,9 +96,11 @@ struct AttnShape {
     static constexpr int kRows = kStep * kRowBytes;
     static constexpr int kScales = 2 * kRows, kThere = kScales + (kE4m3 ? 2 * kStep * 4 : 0);
     static constexpr int kStage = (kThere + 16 + 127) / 128 * 128;
-    static constexpr int kRing = kAttnStages * kStage;
-    static constexpr int kSmem = kAttnWarps * kRing;
-    static_assert(kHeads * kDim * 4 <= kRing, "the warps' results take the rings' place");
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kSmem = kAttnWarps / kHq * kRing;
+    // a warp's results take the place of its share of the rings
+    static constexpr int kResult = kRing / kHq;
+    static_assert(kHeads * kDim * 4 <= kResult && kResult % 16 == 0, "room for the results");
 };
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
@@ -174,7 +178,6 @@ template <int kDim>
 __device__ __forceinline__ void attn_store(const PagedAttentionParams& p, int64_t head, int i,
                                            float top, float sum, float4 v)
 {
-    if (4 * i >= kDim) return;
     const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
     uint2 two;
     if (p.q_bf16)
@@ -186,11 +189,11 @@ __device__ __forceinline__ void attn_store(const PagedAttentionParams& p, int64_
         p.lse[head] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int kType, int kDim, int kNT>
+template <int kType, int kDim, int kNT, int kHq>
 __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     paged_attention_kernel(const __grid_constant__ PagedAttentionParams p)
 {
-    using S = AttnShape<kType, kDim, kNT>;
+    using S = AttnShape<kType, kDim, kNT, kHq>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_ml[kAttnWarps][S::kHeads][2];
     __shared__ int64_t s_scan[kAttnWarps];
@@ -198,20 +201,24 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int group = p.q_heads / p.k.heads;
-    const int parts = (group + S::kHeads - 1) / S::kHeads;  // head chunks of a group
+    constexpr int kBlock = kHq * S::kHeads;                  // query heads of a key head in this CTA
+    const int parts = (group + kBlock - 1) / kBlock;         // CTAs that a group takes
     const int hw = p.hw, chunks = p.k.heads / hw * parts;
     const int chunk = blockIdx.x % chunks;
     const int me = blockIdx.x / chunks;                      // of the chunk's CTAs
-    const int kvh = chunk / parts * hw + warp % hw;          // this warp's key head
-    const int part0 = chunk % parts * S::kHeads;             // its first query head of the group
-    const int n_heads = min(S::kHeads, group - part0);
-    const int all_heads = hw * S::kHeads;                    // of the CTA, with the empty ones
-    const int tile = S::kStep * (kAttnWarps / hw);           // positions
-    uint8_t* const ring = smem + warp * S::kRing;
+    const int side = hw * kHq;                               // warps at the same positions
+    const int kvh = chunk / parts * hw + warp % side / kHq;  // this warp's key head
+    const int part0 = chunk % parts * kBlock;                // the CTA's first query head of the group
+    const int h_first = part0 + warp % kHq * S::kHeads;      // this warp's
+    const int n_heads = min(S::kHeads, group - h_first);     // (none: <= 0)
+    const int all_heads = side * S::kHeads;                  // of the CTA, with the empty ones
+    const int tile = S::kStep * (kAttnWarps / side);         // positions
+    uint8_t* const ring = smem + warp / kHq * S::kRing;
     const uint32_t ring_at = ptx::smem_addr(ring);
     const AttnRows rows{p, int64_t(p.table.cols) * p.k.page_size, tile};
 
     asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this kernel's end
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // and this one for the kernel before it
 
     // ---- this CTA's share of the tiles (each thread counts those of some consecutive rows)
     const int64_t per = (p.B + kAttnThreads - 1) / kAttnThreads;
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         const int32_t count = rows.count(b), n_tiles = rows.tiles(b);
         const int32_t lo = int32_t(at - row_start);
         const int32_t hi = int32_t(min(int64_t(n_tiles), end - row_start));
-        const int h0 = kvh * group + part0;
+        const int h0 = kvh * group + h_first;
         const int32_t len = int32_t(min(int64_t(max(__ldg(p.lens + b), 0)), rows.cap));
 
         // ---- Q: the words of this lane's columns, two values each
@@ -295,15 +302,21 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         const uint8_t* const v_base = p.v.data + kvh * p.v.head_stride;
         const int32_t step_end = min(count, hi * tile);
         const int mine = lane % S::kStep;
-        int32_t page = -1, row = 0;
+        // (two steps ahead what `indices` says: its load, the table's and the rows' copies hang on
+        // one another)
+        int32_t page = -1, row = 0, listed = -1;
+        auto list = [&](int32_t i) {
+            listed = -1;
+            if (p.n_indices >= 0 && i + mine < step_end)
+                listed = __ldg(p.indices + b * p.indices_stride + i + mine);
+        };
         auto find = [&](int32_t i) {  // i: the step's first place in the row's list
             page = -1;
-            i += mine;
-            if (i < step_end) {
-                int32_t n = i;
-                if (p.n_indices >= 0) n = __ldg(p.indices + b * p.indices_stride + i);
+            if (i + mine < step_end) {
+                const int32_t n = p.n_indices >= 0 ? listed : i + mine;
                 if (!(n >= 0 && n < len && locate(p.k, p.table, b, n, &page, &row))) page = -1;
             }
+            list(i + tile);
         };
         auto copy = [&](int stage) {  // the rows that find() found
             const bool there = page >= 0;
@@ -313,8 +326,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             constexpr int kPer = 32 / S::kPieces;  // rows in one instruction
             const int c = lane % S::kPieces;
 #pragma unroll
-            for (int j = 0; j < S::kStep / kPer; ++j) {
-                const int r = j * kPer + lane / S::kPieces;
+            for (int j = 0; j < S::kStep / kPer / kHq; ++j) {
+                const int r = (j * kHq + warp % kHq) * kPer + lane / S::kPieces;
                 const uint32_t at = __shfl_sync(~0u, k_at, r);
                 const uint32_t at2 = p.same_rows ? at : __shfl_sync(~0u, v_at, r);
                 const bool ok = at != kNoRow;
@@ -323,7 +336,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                 copy16(to + S::kRows + 16 * v_place<S::kPieces>(r, c),
                        v_base + uint64_t(ok ? at2 : 0) * p.v_units.unit + 16 * c, ok);
             }
-            if constexpr (S::kE4m3) {
+            if (S::kE4m3 && warp % kHq == 0) {
                 const int64_t pg = there ? page : 0, rw = there ? row : 0;
                 copy4(to + S::kScales + 4 * lane,
                       p.k.scale + pg * p.k.scale_page_stride + rw * p.k.scale_row_stride +
@@ -335,14 +348,16 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                       there);
             }
             const uint32_t here = __ballot_sync(~0u, there);
-            if (lane == 0) *reinterpret_cast<uint32_t*>(ring + stage * S::kStage + S::kThere) = here;
+            if (lane == 0 && warp % kHq == 0)
+                *reinterpret_cast<uint32_t*>(ring + stage * S::kStage + S::kThere) = here;
         };
 
-        int32_t i0 = lo * tile + warp / hw * S::kStep;  // the step being computed
-        int32_t ahead = i0;                             // the step that find() found
+        int32_t i0 = lo * tile + warp / side * S::kStep;  // the step being computed
+        int32_t ahead = i0;                               // the step that find() found
+        list(ahead);
         find(ahead);
-#pragma unroll
-        for (int j = 0; j < kAttnStages - 1; ++j) {
+#pragma unroll 1
+        for (int j = 0; j < S::kStages - 1; ++j) {
             if (ahead < step_end) {
                 copy(j);
                 find(ahead += tile);
@@ -395,16 +410,21 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         }
 
         for (int stage = 0, t_left = hi - lo; t_left > 0;
-             --t_left, i0 += tile, stage = (stage + 1) % kAttnStages) {
-            if (hw > 1) __syncthreads();  // the heads' copies go out together
-            if (i0 >= step_end) continue;
+             --t_left, i0 += tile, stage = (stage + 1) % S::kStages) {
+            // a ring of one warp: the next copies go out first; a shared one: all its warps' copies
+            // are there, and all are done with the stage that the next ones fill
+            if (kHq > 1) copy_wait<S::kStages - 2>();
+            if (kHq > 1 || hw > 1) __syncthreads();  // (and the key heads' copies go out together)
             if (ahead < step_end) {
-                copy((stage + kAttnStages - 1) % kAttnStages);
+                copy((stage + S::kStages - 1) % S::kStages);
                 find(ahead += tile);
             }
             copy_commit();
-            copy_wait<kAttnStages - 1>();
-            __syncwarp();
+            if (i0 >= step_end || (kHq > 1 && n_heads <= 0)) continue;
+            if (kHq == 1) {
+                copy_wait<S::kStages - 1>();
+                __syncwarp();
+            }
             const uint8_t* const at_k = ring + stage * S::kStage;
             const uint8_t* const at_v = at_k + S::kRows;
             const uint32_t here = *reinterpret_cast<const uint32_t*>(at_k + S::kThere);
@@ -565,12 +585,14 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                         mma16816<S::kBf16>(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
                 }
             }
-            __syncwarp();  // the stage may be filled again
+            if (kHq == 1) __syncwarp();  // the stage may be filled again
         }
 
         // ---- the warps' results, joined in shared memory
         const float v_back = S::kE4m3 ? __uint_as_float(uint32_t(v_exp) << 23) : 1.0f;
-        float* const s_o = reinterpret_cast<float*>(ring);  // [heads][dim], where the ring was
+        // [heads][dim], where the rings were
+        float* const s_o = reinterpret_cast<float*>(smem + warp * S::kResult);
+        if (kHq > 1) __syncthreads();  // nobody reads the rings any more
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -594,24 +616,24 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             }
         __syncthreads();
         auto finish = [&](int i, int hh, float top, float sum, float4 v) {
-            const int h = hh % S::kHeads;
-            if (h >= n_heads) return;
-            const int64_t head =
-                b * p.q_heads + (chunk / parts * hw + hh / S::kHeads) * group + part0 + h;
-            attn_store<kDim>(p, head, i % (kDim / 4), top, sum, v);
+            const int h = hh % kBlock;
+            if (part0 + h >= group) return;
+            attn_store<kDim>(p, b * p.q_heads + (chunk / parts * hw + hh / kBlock) * group + part0 + h,
+                             i % (kDim / 4), top, sum, v);
         };
         const bool whole = lo == 0 && hi == n_tiles;
         const int64_t slot = 2 * int64_t(blockIdx.x) + (at == first ? 0 : 1);
         for (int i = tid; i < all_heads * (kDim / 4); i += kAttnThreads) {
             const int hh = i / (kDim / 4), h = hh % S::kHeads;
             float top = -CUDART_INF_F;
-            for (int w = hh / S::kHeads; w < kAttnWarps; w += hw) top = fmaxf(top, s_ml[w][h][0]);
+            for (int w = hh / S::kHeads; w < kAttnWarps; w += side) top = fmaxf(top, s_ml[w][h][0]);
             const float ref = top == -CUDART_INF_F ? 0.0f : top;
             float sum = 0.0f;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int w = hh / S::kHeads; w < kAttnWarps; w += hw) {
+            for (int w = hh / S::kHeads; w < kAttnWarps; w += side) {
                 const float f = exp2_fast(s_ml[w][h][0] - ref);
-                const float4 y = reinterpret_cast<const float4*>(smem + w * S::kRing)[i % (S::kHeads * (kDim / 4))];
+                const float4 y = reinterpret_cast<const float4*>(
+                    smem + w * S::kResult)[i % (S::kHeads * (kDim / 4))];
                 sum = fmaf(f, s_ml[w][h][1], sum);
                 v.x = fmaf(f, y.x, v.x);
                 v.y = fmaf(f, y.y, v.y);
@@ -643,7 +665,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 
 // Joins the rows that several CTAs took.  Block (e, k) stands for 8 query heads (k) of share e + 1:
 // the row that the share begins within has `parts` shares, so parts - 1 such blocks, which divide the
-// 8 heads among them; a head's partial results are divided among the block's warps.
+// 8 heads among them (of 33 shares or more, a quarter of a head's columns each).  A head's partial
+// results are divided among the block's warps, and a warp's lanes, so that many loads are under way.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
 template <int kDim>
@@ -651,7 +674,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     paged_attention_join_kernel(const __grid_constant__ PagedAttentionParams p, int heads, int ctas)
 {
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
-    __shared__ __align__(16) float s_o[kJoinWarps][kDim];
+    __shared__ __align__(16) float4 s_o[kJoinWarps][kDim / 4];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int group = p.q_heads / p.k.heads, parts = (group + heads - 1) / heads;
     const int chunks = p.k.heads / p.hw * parts, all_heads = p.hw * heads;
@@ -660,34 +683,38 @@ __global__ void __launch_bounds__(kJoinThreads)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const AttnSplit split = p.splits[me];
     if (split.parts == 0) return;
-    const int n = split.parts, helpers = min(n - 1, 8), helper = me - split.first - 1;
+    const int n = split.parts, slices = n > 32 ? 4 : 1;
+    const int helpers = min(n - 1, 8 * slices), helper = me - split.first - 1;
     if (helper >= helpers) return;
-    const int mine = 8 / helpers + (helper < 8 % helpers);  // heads, helper + j * helpers
+    const int step = helpers / slices;  // this block's heads: helper / slices + j * step
+    const int mine = 8 / step + (helper / slices < 8 % step);
     // a power of two of heads at a time, the warps shared out among them
     const int at_once = mine >= 8 ? 8 : mine >= 4 ? 4 : mine >= 2 ? 2 : 1, share = kJoinWarps / at_once;
+    const int columns = kDim / 4 / slices;                 // float4s of a block's slice: lanes of a member
+    const int sub = lane / columns, subs = 32 / columns;   // members at a time
+    const int col = helper % slices * columns + lane % columns;
     const float* const part_ml = p.partial + int64_t(2) * ctas * chunks * all_heads * kDim;
     for (int j0 = 0; j0 < mine; j0 += at_once) {
         const int j = j0 + warp / share, r = warp % share;
-        const int hh = first_head + helper + j * helpers;
+        const int hh = first_head + helper / slices + j * step;
         float m = -CUDART_INF_F, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (j < mine) {
             constexpr int kBatch = 8;
-            for (int k0 = r; k0 < n; k0 += share * kBatch) {
+            for (int k0 = r * subs + sub; k0 - sub < n; k0 += share * subs * kBatch) {
                 float2 ml[kBatch];
                 float4 x[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int k = k0 + i * share;
+                    const int k = k0 + i * share * subs;
                     ml[i] = make_float2(-CUDART_INF_F, 0.0f);
                     x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (k < n) {
                         const int64_t slot = 2 * (int64_t(split.first + k) * chunks + chunk) +
                                              (k == 0 ? split.first_slot : 0);
                         ml[i] = __ldcg(reinterpret_cast<const float2*>(part_ml) + slot * all_heads + hh);
-                        if (4 * lane < kDim)
-                            x[i] = __ldcg(reinterpret_cast<const float4*>(
-                                              p.partial + (slot * all_heads + hh) * kDim) + lane);
+                        x[i] = __ldcg(reinterpret_cast<const float4*>(
+                                          p.partial + (slot * all_heads + hh) * kDim) + col);
                     }
                 }
                 float top = m;
@@ -711,15 +738,28 @@ __global__ void __launch_bounds__(kJoinThreads)
                 m = top;
             }
         }
+        for (int s = columns; s < 32; s *= 2) {  // the lanes of the warp's other members
+            const float m2 = __shfl_xor_sync(~0u, m, s), top = fmaxf(m, m2);
+            const float ref = top == -CUDART_INF_F ? 0.0f : top;
+            const float a = exp2_fast(m - ref), b = exp2_fast(m2 - ref);
+            // the same sum in the same order in both lanes
+            auto both = [&](float x) {
+                const float y = __shfl_xor_sync(~0u, x, s);
+                return lane & s ? fmaf(b, y, a * x) : fmaf(a, x, b * y);
+            };
+            l = both(l);
+            o = make_float4(both(o.x), both(o.y), both(o.z), both(o.w));
+            m = top;
+        }
         __syncthreads();
         if (lane == 0) {
             s_m[warp] = m;
             s_l[warp] = l;
         }
-        if (4 * lane < kDim) reinterpret_cast<float4*>(s_o[warp])[lane] = o;
+        if (sub == 0) s_o[warp][lane] = o;
         __syncthreads();
         const int h = hh % heads, part0 = chunk % parts * heads;
-        if (j < mine && r == 0 && h < min(heads, group - part0)) {
+        if (j < mine && r == 0 && sub == 0 && part0 + h < group) {
             float top = -CUDART_INF_F;
             for (int w = warp; w < warp + share; ++w) top = fmaxf(top, s_m[w]);
             const float ref = top == -CUDART_INF_F ? 0.0f : top;
@@ -727,18 +767,15 @@ __global__ void __launch_bounds__(kJoinThreads)
             o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int w = warp; w < warp + share; ++w) {
                 const float f = exp2_fast(s_m[w] - ref);
+                const float4 x = s_o[w][lane];
                 l = fmaf(f, s_l[w], l);
-                if (4 * lane < kDim) {
-                    const float4 x = reinterpret_cast<const float4*>(s_o[w])[lane];
-                    o.x = fmaf(f, x.x, o.x);
-                    o.y = fmaf(f, x.y, o.y);
-                    o.z = fmaf(f, x.z, o.z);
-                    o.w = fmaf(f, x.w, o.w);
-                }
+                o.x = fmaf(f, x.x, o.x);
+                o.y = fmaf(f, x.y, o.y);
+                o.z = fmaf(f, x.z, o.z);
+                o.w = fmaf(f, x.w, o.w);
             }
-            const int64_t head =
-                split.row * p.q_heads + (chunk / parts * p.hw + hh / heads) * group + part0 + h;
-            attn_store<kDim>(p, head, lane, top, l, o);
+            attn_store<kDim>(p, split.row * p.q_heads + (chunk / parts * p.hw + hh / heads) * group + part0 + h,
+                             col, top, l, o);
         }
     }
 }

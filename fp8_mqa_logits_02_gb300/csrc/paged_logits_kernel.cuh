@@ -145,6 +145,8 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
     auto bar = [&](int i) { return base + S::kOffBar + 8 * i; };
     PagedItem* const items = reinterpret_cast<PagedItem*>(smem + S::kOffItem);
 
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
     // ---- the rows' costs, in units of about half a kilobyte moved
     const int32_t c_tile = 34 + n_tok, c_fill = 8 * n_tok;
     auto length = [&](int64_t b) {
