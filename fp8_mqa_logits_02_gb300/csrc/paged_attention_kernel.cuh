@@ -100,7 +100,8 @@ struct AttnShape {
     static constexpr int kSmem = kAttnWarps / kHq * kRing;
     // a warp's results take the place of its share of the rings
     static constexpr int kResult = kRing / kHq;
-    static_assert(kHeads * kDim * 4 <= kResult && kResult % 16 == 0, "room for the results");
+    static constexpr int kPitch = kDim + 4;            // floats from head to head: fewer bank conflicts
+    static_assert(kHeads * kPitch * 4 <= kResult && kResult % 16 == 0, "room for the results");
 };
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
@@ -286,14 +287,19 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             const int h = nt * 8 + g;
             const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.q_row_stride +
                                 int64_t(h0 + h) * p.q_head_stride;
+            // word w = 2 s + j (columns of fragment s) is word w % kRun of the run w / kRun of words that
+            // lie together, as in the cache's rows: 16 values of 64, or 8 of 32
+            constexpr int kRun = S::kE4m3 ? 8 : 4;
 #pragma unroll
-            for (int s = 0; s < S::kMT; ++s)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int d = S::kE4m3 ? s / 4 * 64 + t * 16 + s % 4 * 4 + 2 * j
-                                           : (2 * s + j) / 4 * 32 + t * 8 + (2 * s + j) % 4 * 2;
-                    qf[nt][s][j] = h < n_heads ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
-                }
+            for (int w = 0; w < 2 * S::kMT; w += 4) {
+                const int d = w / kRun * (8 * kRun) + t * (2 * kRun) + w % kRun * 2;
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (h < n_heads) x = __ldg(reinterpret_cast<const uint4*>(q + d));
+                qf[nt][w / 2][0] = x.x;
+                qf[nt][w / 2][1] = x.y;
+                qf[nt][w / 2 + 1][0] = x.z;
+                qf[nt][w / 2 + 1][1] = x.w;
+            }
         }
         int32_t v_exp = 1;  // value scales are taken relative to 2^(v_exp - 127)
 
@@ -606,12 +612,14 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                     s_ml[warp][h][0] = m[nt][j];
                     s_ml[warp][h][1] = sum;
                 }
+                // four columns of a head at a time: those of fragments i and i + 1 lie together
 #pragma unroll
-                for (int i = 0; i < S::kMT; ++i) {
+                for (int i = 0; i < S::kMT; i += 2) {
                     const int d = S::kE4m3 ? g * (kDim / 8) + 2 * i
                                            : i / 4 * 64 + g * 8 + 2 * i % 8;
-                    s_o[h * kDim + d] = o[nt][i][j] * v_back;
-                    s_o[h * kDim + d + 1] = o[nt][i][2 + j] * v_back;
+                    *reinterpret_cast<float4*>(s_o + h * S::kPitch + d) =
+                        make_float4(o[nt][i][j] * v_back, o[nt][i][2 + j] * v_back,
+                                    o[nt][i + 1][j] * v_back, o[nt][i + 1][2 + j] * v_back);
                 }
             }
         __syncthreads();
@@ -632,8 +640,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int w = hh / S::kHeads; w < kAttnWarps; w += side) {
                 const float f = exp2_fast(s_ml[w][h][0] - ref);
-                const float4 y = reinterpret_cast<const float4*>(
-                    smem + w * S::kResult)[i % (S::kHeads * (kDim / 4))];
+                const float4 y = *reinterpret_cast<const float4*>(
+                    smem + w * S::kResult + (h * S::kPitch + i % (kDim / 4) * 4) * 4);
                 sum = fmaf(f, s_ml[w][h][1], sum);
                 v.x = fmaf(f, y.x, v.x);
                 v.y = fmaf(f, y.y, v.y);
