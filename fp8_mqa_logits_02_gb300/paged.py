@@ -16,15 +16,15 @@ import struct
 
 import torch
 
-from . import DIM, HEADS, Fp8MqaError, _entry, _on, _stream_ptr
+from . import DIM, HEADS, Fp8MqaError, _entry, _on, _raw_stream, _stream_ptr
 
 _E4M3 = torch.float8_e4m3fn
 _TYPE = {_E4M3: 0, torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
 _pack_cache = struct.Struct("@PPqiiiiqqqqqq").pack  # struct fp8mqa_cache
 
 
-# A call's checks cost about as much as its launch, so each looks at a tensor's attributes once and
-# states what is wrong only after it knows that something is.
+# A call's checks and its launch cost about the same, so each check reads an attribute once and finds
+# out what is wrong only after it knows that something is.
 def _cuda(t, name):
     """The device of a CUDA tensor."""
     if not isinstance(t, torch.Tensor):
@@ -42,15 +42,15 @@ def _on_device(t, name, device):
 
 def _ints(t, name, device, *shape):
     """Checks an int32 tensor of ``shape`` (None: any size) whose last dimension is contiguous."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device:
+        got = t.shape
+        if len(got) == len(shape) and (shape[0] is None or got[0] == shape[0]):
+            if t.stride(-1) == 1 or got[-1] < 2:
+                return
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+        raise ValueError(f"{name} must be {['any' if n is None else n for n in shape]}, got {list(got)}")
     _on_device(t, name, device)
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32, got {t.dtype}")
-    got = t.shape
-    if len(got) != len(shape) or (shape[0] is not None and got[0] != shape[0]):
-        want = ["any" if n is None else n for n in shape]
-        raise ValueError(f"{name} must be {want}, got {list(got)}")
-    if got[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
+    raise TypeError(f"{name} must be int32, got {t.dtype}")
 
 
 def _cache(data, scale, name, device, other=None):
@@ -59,24 +59,32 @@ def _cache(data, scale, name, device, other=None):
     dtype, shape, stride = data.dtype, data.shape, data.stride()
     if len(shape) != 4:
         raise ValueError(f"{name} data must be [pages, page_size, heads, dim], got {list(shape)}")
-    if stride[3] != 1:
+    pages, page, heads, dim = shape
+    x, y, z, one = stride
+    if one != 1:
         raise ValueError(f"{name} data must be contiguous in its last dimension")
-    if dtype == _E4M3:
+    if dtype is _E4M3:
         _on_device(scale, f"{name} scale", device)
-        if scale.dtype != torch.float32 or scale.shape != shape[:3]:
-            raise ValueError(f"{name} scale must be float32 {list(shape[:3])}")
-        at, (a, b, c) = scale.data_ptr(), scale.stride()
-    else:
-        if other is None or dtype != other:
-            raise TypeError(f"{name} data must be {_E4M3}{'' if other is None else f' or {other}'}, got {dtype}")
-        if scale is not None:
-            raise ValueError(f"{name} scale goes with float8_e4m3fn data only")
-        at = a = b = c = 0
-    return _pack_cache(data.data_ptr(), at, *shape, _TYPE[dtype], stride[0], stride[1], stride[2], a, b, c), shape
+        if scale.dtype is not torch.float32 or scale.shape != (pages, page, heads):
+            raise ValueError(f"{name} scale must be float32 {[pages, page, heads]}")
+        a, b, c = scale.stride()
+        return _pack_cache(data.data_ptr(), scale.data_ptr(), pages, page, heads, dim, 0, x, y, z, a, b, c), shape
+    if dtype is not other:
+        raise TypeError(f"{name} data must be {_E4M3}{'' if other is None else f' or {other}'}, got {dtype}")
+    if scale is not None:
+        raise ValueError(f"{name} scale goes with float8_e4m3fn data only")
+    return _pack_cache(data.data_ptr(), 0, pages, page, heads, dim, _TYPE[dtype], x, y, z, 0, 0, 0), shape
+
+
+_current = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _call(name, device, stream, *args):
-    rc = _on(device, _entry(name), *args, _stream_ptr(stream, device))
+    index = device.index
+    if stream is None and _raw_stream is not None and _current() == index:
+        rc = _entry(name)(*args, _raw_stream(index))
+    else:
+        rc = _on(device, _entry(name), *args, _stream_ptr(stream, device))
     if rc != 0:
         raise Fp8MqaError(rc, name)
 
