@@ -1,8 +1,9 @@
-"""Builds the in-tree CUDA library ``libfp8mqa.so`` for sm_103a with nvcc.
+"""Builds the in-tree CUDA library ``libfp8mqa.so`` for sm_103a with nvcc, and with the host
+compiler the paged operators' binding ``_paged_binding.so`` against the installed torch.
 
 Usage: ``python -m fp8_mqa_logits_02_gb300.nvcc_build`` (also called by the package's
-``build()`` helper).  The outputs (``libfp8mqa.so`` and its bounds-checking variant
-``libfp8mqa_debug.so``) land next to this file and are git-ignored.
+``build()`` helper).  The outputs (``libfp8mqa.so``, its bounds-checking variant
+``libfp8mqa_debug.so`` and the binding) land next to this file and are git-ignored.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +22,8 @@ LIB = os.path.join(HERE, "libfp8mqa.so")
 # of the kernel is checked first, and a violation is recorded in the status word
 # (fp8_mqa_logits_check_error then returns FP8MQA_ERR_BOUNDS) instead of being made.
 DEBUG_LIB = os.path.join(HERE, "libfp8mqa_debug.so")
+BINDING_SOURCE = os.path.join(CSRC, "paged_binding.cpp")
+BINDING = os.path.join(HERE, "_paged_binding.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,17 +42,28 @@ def deps() -> list:
     return files + [os.path.join(ROOT, "include", "fp8_mqa_logits.h"), os.path.abspath(__file__)]
 
 
+def torch_dir() -> str:
+    import torch
+    return os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def binding_deps() -> list:
+    """What the binding is compiled from; another torch has other headers and needs a new one."""
+    return [BINDING_SOURCE, os.path.join(ROOT, "include", "fp8_mqa_logits.h"), os.path.abspath(__file__),
+            os.path.join(torch_dir(), "version.py")]
+
+
 def up_to_date(lib: str) -> bool:
     if not os.path.exists(lib):
         return False
     t = os.path.getmtime(lib)
-    return all(os.path.getmtime(d) <= t for d in deps())
+    return all(os.path.getmtime(d) <= t for d in (binding_deps() if lib == BINDING else deps()))
 
 
-def _command(out: str, debug: bool, verbose: bool) -> list:
-    cmd = [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared",
+def _compile(source: str, out: str, debug: bool, verbose: bool) -> list:
+    cmd = [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-c",
            "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-           "-I", os.path.join(ROOT, "include"), "-o", out, *SOURCES]
+           "-I", os.path.join(ROOT, "include"), "-o", out, source]
     if debug:
         cmd.insert(1, "-DFP8MQA_DEBUG_BOUNDS")
     if verbose:
@@ -56,29 +71,57 @@ def _command(out: str, debug: bool, verbose: bool) -> list:
     return cmd
 
 
+def _binding(out: str) -> list:
+    t, cuda = torch_dir(), os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    lib = os.path.join(t, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-I", os.path.join(t, "include"), "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+            "-o", out, BINDING_SOURCE, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool | None = None) -> str:
     """Build the library (debug=False), its bounds-checking variant (debug=True), or both
-    at once (debug=None, the default; returns the regular library's path).  Each is rebuilt
-    only when a source is newer, unless `force`."""
+    at once (debug=None, the default; returns the regular library's path), and the binding.
+    Each is rebuilt only when a source is newer, unless `force`.  All translation units
+    compile at the same time."""
     targets = [False, True] if debug is None else [bool(debug)]
-    jobs = []
+    jobs, links = [], []  # (what, command); (library, temporary, objects)
+    tag = f".tmp{os.getpid()}"
     for dbg in targets:
         lib = DEBUG_LIB if dbg else LIB
         if not force and up_to_date(lib):
             continue
-        tmp = lib + f".tmp{os.getpid()}"
-        proc = subprocess.Popen(_command(tmp, dbg, verbose), stdout=subprocess.PIPE,
-                                stderr=subprocess.STDOUT, text=True)
-        jobs.append((lib, tmp, proc))
+        objects = []
+        for source in SOURCES:
+            objects.append(f"{lib}.{os.path.basename(source)}{tag}.o")
+            jobs.append((f"{os.path.basename(lib)} ({os.path.basename(source)})",
+                         _compile(source, objects[-1], dbg, verbose)))
+        links.append((lib, lib + tag, objects))
+    if force or not up_to_date(BINDING):
+        jobs.append((os.path.basename(BINDING), _binding(BINDING + tag)))
+        links.append((BINDING, BINDING + tag, None))
+    running = [(what, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+               for what, cmd in jobs]
     failed = []
-    for lib, tmp, proc in jobs:
+    for what, proc in running:
         out, _ = proc.communicate()
         if proc.returncode != 0:
-            failed.append(f"nvcc failed for {os.path.basename(lib)}:\n{out}")
-            continue
-        if verbose:
+            failed.append(f"compiling {what} failed:\n{out}")
+        elif verbose:
             sys.stderr.write(out)
+    for lib, tmp, objects in links if not failed else []:
+        if objects is not None:
+            done = subprocess.run([nvcc_path(), *ARCH_FLAGS, "-shared", "-o", tmp, *objects],
+                                  stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+            if done.returncode != 0:
+                failed.append(f"linking {os.path.basename(lib)} failed:\n{done.stdout}")
+                continue
         os.replace(tmp, lib)
+    for _, tmp, objects in links:
+        for path in [tmp, *(objects or [])]:
+            if os.path.exists(path):
+                os.remove(path)
     if failed:
         raise RuntimeError("\n".join(failed))
     return DEBUG_LIB if debug else LIB
