@@ -105,9 +105,7 @@ struct CacheReadParams {
 };
 constexpr int kReadRows = 128;
 
-// Pieces of 16 bytes of output that a thread has under way.
-template <class Out>
-constexpr int kReadPieces = sizeof(Out) == 1 ? 4 : 8;
+constexpr int kReadPieces = 4;  // pieces of 16 bytes of output that a thread has under way
 
 // The sequence of output row r: the last b with starts[b] <= r (B where r is past the end).
 __device__ __forceinline__ int64_t sequence_of(const int32_t* starts, int64_t B, int64_t r)
@@ -143,12 +141,11 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
     constexpr int kPer = 16 / sizeof(Out), kLanes = kDim / kPer;
     const int n = rows * c.heads * kLanes;
     uint4* const out = reinterpret_cast<uint4*>(static_cast<Out*>(p.out) + r0 * c.heads * kDim);
-    constexpr int kPieces = kReadPieces<Out>;
-    for (int i0 = threadIdx.x; i0 < n; i0 += kPieces * kCacheThreads) {
-        uint32_t x[kPieces][kPer / 4];
-        float by[kPieces];
+    for (int i0 = threadIdx.x; i0 < n; i0 += kReadPieces * kCacheThreads) {
+        uint32_t x[kReadPieces][kPer / 4];
+        float by[kReadPieces];
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
+        for (int j = 0; j < kReadPieces; ++j) {
             const int i = i0 + j * kCacheThreads, at = i / kLanes;
 #pragma unroll
             for (int k = 0; k < kPer / 4; ++k) x[j][k] = 0u;
@@ -176,7 +173,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
             }
         }
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
+        for (int j = 0; j < kReadPieces; ++j) {
             const int i = i0 + j * kCacheThreads;
             if (i >= n) break;
             if constexpr (kPer == 16) {

@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     using S = AttnShape<kType, kDim, kNT, kHq>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_ml[kAttnWarps][S::kHeads][2];
-    __shared__ int64_t s_scan[kAttnWarps];
-    __shared__ int64_t s_first[2];  // the first row of this CTA, and the tiles before it
+    __shared__ int32_t s_scan[kAttnWarps];
+    __shared__ int32_t s_first[2];  // the first row of this CTA, and the tiles before it
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int group = p.q_heads / p.k.heads;
@@ -223,16 +223,16 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 
     // ---- this CTA's share of the tiles (each thread counts those of some consecutive rows)
     const int64_t per = (p.B + kAttnThreads - 1) / kAttnThreads;
-    int64_t total, before = 0, mine_sum = 0;  // tiles of all rows, of those before mine, of mine
+    int32_t total, before = 0, mine_sum = 0;  // tiles of all rows, of those before mine, of mine
     if (p.n_indices >= 0) {
-        total = p.B * rows.tiles(0);
+        total = int32_t(p.B) * rows.tiles(0);
     } else {
         const int64_t b1 = min(per * (tid + 1), p.B);
         for (int64_t b = per * tid; b < b1; ++b) mine_sum += rows.tiles(b);
-        int64_t scan = mine_sum;
+        int32_t scan = mine_sum;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-            const int64_t x = __shfl_up_sync(~0u, scan, o);
+            const int32_t x = __shfl_up_sync(~0u, scan, o);
             if (lane >= o) scan += x;
         }
         if (lane == 31) s_scan[warp] = scan;
@@ -244,39 +244,46 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             total += s_scan[w];
         }
     }
-    const int64_t ctas = min(int64_t(gridDim.x / chunks), total);
+    const int32_t ctas = min(int32_t(gridDim.x) / chunks, total);
     if (me >= ctas) {
         if (chunk == 0 && tid == 0) p.splits[me].parts = 0;
         return;
     }
-    const int64_t first = me * total / ctas, end = (me + 1) * total / ctas;
+    // `more` CTAs have each + 1 tiles, the others each
+    const int32_t each = total / ctas, more = total - each * ctas;
+    auto begin_of = [&](int32_t cta) { return cta * each + min(cta, more); };
+    auto owner_of = [&](int32_t t) {
+        return t < more * (each + 1) ? t / (each + 1) : more + (t - more * (each + 1)) / each;
+    };
+    const int32_t first = begin_of(me), end = begin_of(me + 1);
     if (p.n_indices >= 0) {
         if (tid == 0) {
-            const int64_t n = rows.tiles(0);
+            const int32_t n = rows.tiles(0);
             s_first[0] = first / n;
             s_first[1] = first / n * n;
         }
     } else if (before <= first && first < before + mine_sum) {
-        int64_t b = per * tid, at = before;
+        int64_t b = per * tid;
+        int32_t at = before;
         for (;; ++b) {
-            const int64_t n = rows.tiles(b);
+            const int32_t n = rows.tiles(b);
             if (first < at + n) break;
             at += n;
         }
-        s_first[0] = b;
+        s_first[0] = int32_t(b);
         s_first[1] = at;
     }
     __syncthreads();
-    int64_t b = s_first[0], row_start = s_first[1];
+    int64_t b = s_first[0];
+    int32_t row_start = s_first[1];
 
     float* const part_o = p.partial;
     float* const part_ml = p.partial + int64_t(2) * gridDim.x * all_heads * kDim;
 
-    for (int64_t at = first; at < end; ++b) {
+    for (int32_t at = first; at < end; ++b) {
         // ---- one segment: tiles [lo, hi) of row b
         const int32_t count = rows.count(b), n_tiles = rows.tiles(b);
-        const int32_t lo = int32_t(at - row_start);
-        const int32_t hi = int32_t(min(int64_t(n_tiles), end - row_start));
+        const int32_t lo = at - row_start, hi = min(n_tiles, end - row_start);
         const int h0 = kvh * group + h_first;
         const int32_t len = int32_t(min(int64_t(max(__ldg(p.lens + b), 0)), rows.cap));
 
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         const int32_t step_end = min(count, hi * tile);
         const int mine = lane % S::kStep;
         // (two steps ahead what `indices` says: its load, the table's and the rows' copies hang on
-        // one another)
+        // one another, and nothing looks at what a load brings before the next one needs it)
         int32_t page = -1, row = 0, listed = -1;
         auto list = [&](int32_t i) {
             listed = -1;
@@ -317,15 +324,17 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                 listed = __ldg(p.indices + b * p.indices_stride + i + mine);
         };
         auto find = [&](int32_t i) {  // i: the step's first place in the row's list
+            const int32_t n = p.n_indices >= 0 ? listed : i + mine;
             page = -1;
-            if (i + mine < step_end) {
-                const int32_t n = p.n_indices >= 0 ? listed : i + mine;
-                if (!(n >= 0 && n < len && locate(p.k, p.table, b, n, &page, &row))) page = -1;
+            if (i + mine < step_end && n >= 0 && n < len) {
+                const int32_t col = p.table.by_page.of(n);
+                row = n - col * p.k.page_size;
+                page = __ldg(p.table.ids + b * p.table.stride + col);
             }
             list(i + tile);
         };
         auto copy = [&](int stage) {  // the rows that find() found
-            const bool there = page >= 0;
+            const bool there = uint32_t(page) < uint32_t(p.k.pages);
             const uint32_t k_at = there ? page * p.k_units.page + row * p.k_units.row : kNoRow;
             const uint32_t v_at = there ? page * p.v_units.page + row * p.v_units.row : kNoRow;
             const uint32_t to = ring_at + stage * S::kStage;
@@ -661,9 +670,9 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         if (at == first && chunk == 0 && tid == 0 && me > 0) {
             AttnSplit split;
             split.row = b;
-            split.first = int32_t(((row_start + 1) * ctas - 1) / total);
-            split.parts = lo == 0 ? 0 : int32_t(((row_start + n_tiles) * ctas - 1) / total) - split.first + 1;
-            split.first_slot = split.first * total / ctas == row_start ? 0 : 1;
+            split.first = owner_of(row_start);
+            split.parts = lo == 0 ? 0 : owner_of(row_start + n_tiles - 1) - split.first + 1;
+            split.first_slot = begin_of(split.first) == row_start ? 0 : 1;
             p.splits[me] = split;
         }
         at = row_start += hi;
