@@ -149,12 +149,15 @@ int check_cache(const fp8mqa_cache* c)
     return FP8MQA_OK;
 }
 
-PagedView view_of(const fp8mqa_cache& c)
+// A cache as kernels see it.  One without pages has no memory; `valid` stands for it (nothing is read
+// there, but copies of no bytes carry an address).
+PagedView view_of(const fp8mqa_cache& c, const void* valid)
 {
     const int64_t e = size_of(c.type);
     PagedView v;
-    v.data = static_cast<uint8_t*>(c.data);
-    v.scale = c.scale;
+    void* const none = const_cast<void*>(valid);
+    v.data = static_cast<uint8_t*>(c.pages > 0 ? c.data : none);
+    v.scale = c.pages > 0 ? c.scale : static_cast<float*>(none);
     v.page_stride = c.page_stride * e;
     v.row_stride = c.row_stride * e;
     v.head_stride = c.head_stride * e;
@@ -379,8 +382,8 @@ int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const v
     p.row_stride[1] = x2_row_stride;
     p.head_stride[0] = x_head_stride;
     p.head_stride[1] = x2_head_stride;
-    p.cache[0] = view_of(*cache);
-    p.cache[1] = view_of(cache2 ? *cache2 : *cache);
+    p.cache[0] = view_of(*cache, x);
+    p.cache[1] = view_of(cache2 ? *cache2 : *cache, x);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (x_type == FP8MQA_BF16)
         write_rows<__nv_bfloat16>(p, cache->dim, x2 ? 2 : 1, s);
@@ -413,7 +416,7 @@ int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t 
     PagedDevice* st = paged_device(&err);
     if (!st) return err;
     CacheReadParams p;
-    p.cache = view_of(*cache);
+    p.cache = view_of(*cache, out);
     p.table = {table, table_stride, table_cols, FastDiv(uint32_t(cache->page_size))};
     p.starts = starts;
     p.B = B;
@@ -458,7 +461,7 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
     PagedLogitsParams p;
     p.q = q_fp8;
     p.w = w;
-    p.keys = view_of(*keys);
+    p.keys = view_of(*keys, q_fp8);
     p.table = {table, table_stride, table_cols, FastDiv(uint32_t(keys->page_size))};
     p.lens = lens;
     p.out = out;
@@ -536,8 +539,8 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     p.q = q;
     p.q_row_stride = q_row_stride;
     p.q_head_stride = q_head_stride;
-    p.k = view_of(*k);
-    p.v = view_of(*v);
+    p.k = view_of(*k, q);
+    p.v = view_of(*v, q);
     p.k.pages = p.v.pages = p.k.pages < p.v.pages ? p.k.pages : p.v.pages;
     if (!row_units(p.k, &p.k_units) || !row_units(p.v, &p.v_units))
         return FP8MQA_ERR_UNSUPPORTED_SHAPE;

@@ -22,8 +22,9 @@
 //
 // E4M3 values become f16 exactly; a row's key scale multiplies its scores, its value scale its
 // weights.  Weights are rounded to 16 bits for the second product (the fp32 sum takes them
-// unrounded); their value scales are taken relative to a running power of two, so the largest
-// keep their 11 bits whatever the scales' size.
+// unrounded): f16's 11 bits cost 2^-12 of a weight, an eighth of what rounding the result to bfloat16
+// does.  E4M3 weights have the rows' value scales in them, 2^(x + log2 scale), and a running maximum of
+// their own, so that f16's range is enough whatever the scales' size.
 //
 // A CTA's four warps take hw key heads (1, 2 or 4) of the same positions and keep in step: the heads
 // of a position lie side by side in memory, and reading them together is what DRAM wants.  Groups of
@@ -115,6 +116,13 @@ __device__ __forceinline__ float exp2_fast(float x)
 {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float log2_fast(float x)
+{
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -308,7 +316,6 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                 qf[nt][w / 2 + 1][1] = x.w;
             }
         }
-        int32_t v_exp = 1;  // value scales are taken relative to 2^(v_exp - 127)
 
         // ---- a step's rows: lane i finds position i of a step, a step ahead of its copies
         const uint8_t* const k_base = p.k.data + kvh * p.k.head_stride;
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         }
 
         // ---- Q as B fragments, and each head's factor of the scores (in powers of two)
-        float factor[kNT][2], m[kNT][2], l[kNT][2], o[kNT][S::kMT][4];
+        float factor[kNT][2], m[kNT][2], l[kNT][2], w_top[kNT][2], o[kNT][S::kMT][4];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             float by = 1.0f;
@@ -415,7 +422,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             factor[nt][1] = __shfl_sync(~0u, c, 8 * t + 4);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                m[nt][j] = -CUDART_INF_F;
+                m[nt][j] = w_top[nt][j] = -CUDART_INF_F;
                 l[nt][j] = 0.0f;
             }
 #pragma unroll
@@ -486,12 +493,13 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                 }
 
             // ---- softmax: this lane has positions 8r + g, heads 2t and 2t + 1
-            float row_vs[S::kKRows];
+            float row_lv[S::kKRows];  // log2 of the rows' value scales
             const float* const scales = reinterpret_cast<const float*>(at_k + S::kScales);
+            const bool negative = S::kE4m3 && __any_sync(~0u, scales[S::kStep + lane % S::kStep] < 0.0f);
 #pragma unroll
             for (int r = 0; r < S::kKRows; ++r) {
                 const float row_ks = S::kE4m3 ? scales[r * 8 + g] : 1.0f;
-                row_vs[r] = S::kE4m3 ? scales[S::kStep + r * 8 + g] : 1.0f;
+                row_lv[r] = S::kE4m3 ? log2_fast(fabsf(scales[S::kStep + r * 8 + g])) : 0.0f;
                 const bool ok = here >> (r * 8 + g) & 1u;
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt)
@@ -501,41 +509,42 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                         y = ok ? y * (row_ks * factor[nt][j]) : -CUDART_INF_F;
                     }
             }
-            float c_v = 1.0f, v_inv = 1.0f;
             bool moved = false;
-            if constexpr (S::kE4m3) {
-                const uint32_t top =
-                    __reduce_max_sync(~0u, __float_as_uint(scales[S::kStep + lane]) & 0x7FFFFFFFu);
-                const int32_t e = min(max(int32_t(top >> 23), v_exp), 253);
-                if (e > v_exp) {
-                    c_v = exp2_fast(float(v_exp - e));
-                    v_exp = e;
-                    moved = true;
-                }
-                v_inv = __uint_as_float(uint32_t(254 - v_exp) << 23);
-            }
             float c[kNT][2];
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float top = m[nt][j];
+                    // the largest score, and (E4M3) the largest score with the row's value scale in it
+                    float top = m[nt][j], wide = w_top[nt][j];
 #pragma unroll
-                    for (int r = 0; r < S::kKRows; ++r) top = fmaxf(top, x[nt][r / 2][r % 2 * 2 + j]);
-                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-                    moved |= top > m[nt][j];
+                    for (int r = 0; r < S::kKRows; ++r) {
+                        const float y = x[nt][r / 2][r % 2 * 2 + j];
+                        top = fmaxf(top, y);
+                        if (S::kE4m3) wide = fmaxf(wide, y + row_lv[r]);
+                    }
+#pragma unroll
+                    for (int o = 4; o < 32; o *= 2) {
+                        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                        if (S::kE4m3) wide = fmaxf(wide, __shfl_xor_sync(~0u, wide, o));
+                    }
+                    if (!S::kE4m3) wide = top;
                     const float ref = top == -CUDART_INF_F ? 0.0f : top;
-                    c[nt][j] = exp2_fast(m[nt][j] - ref);
+                    const float w_ref = wide == -CUDART_INF_F ? 0.0f : wide;
+                    float sum = l[nt][j] * exp2_fast(m[nt][j] - ref);
+                    moved |= wide > w_top[nt][j];
+                    c[nt][j] = exp2_fast(w_top[nt][j] - w_ref);
                     m[nt][j] = top;
-                    float sum = l[nt][j] * c[nt][j];
+                    w_top[nt][j] = wide;
 #pragma unroll
                     for (int r = 0; r < S::kKRows; ++r) {
                         float& y = x[nt][r / 2][r % 2 * 2 + j];
-                        y = exp2_fast(y - ref);
-                        sum += y;
-                        if (S::kE4m3) y *= row_vs[r] * v_inv;
+                        const float e = exp2_fast(y - ref);
+                        sum += e;
+                        y = S::kE4m3 ? exp2_fast(y + row_lv[r] - w_ref) : e;
+                        if (S::kE4m3 && negative)
+                            y = __uint_as_float(__float_as_uint(y) ^
+                                                (__float_as_uint(scales[S::kStep + r * 8 + g]) & 0x80000000u));
                     }
                     l[nt][j] = sum;
                 }
@@ -545,7 +554,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 #pragma unroll
                     for (int i = 0; i < S::kMT; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) o[nt][i][j] *= c[nt][j % 2] * c_v;
+                        for (int j = 0; j < 4; ++j) o[nt][i][j] *= c[nt][j % 2];
             }
 
             // ---- O^T += V^T P^T
@@ -604,7 +613,6 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         }
 
         // ---- the warps' results, joined in shared memory
-        const float v_back = S::kE4m3 ? __uint_as_float(uint32_t(v_exp) << 23) : 1.0f;
         // [heads][dim], where the rings were
         float* const s_o = reinterpret_cast<float*>(smem + warp * S::kResult);
         if (kHq > 1) __syncthreads();  // nobody reads the rings any more
@@ -612,6 +620,9 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
+                // O is counted in 2^w_top, m and l in 2^m
+                const float v_back =
+                    !S::kE4m3 ? 1.0f : w_top[nt][j] == -CUDART_INF_F ? 0.0f : exp2_fast(w_top[nt][j] - m[nt][j]);
                 float sum = l[nt][j];
                 sum += __shfl_xor_sync(~0u, sum, 4);
                 sum += __shfl_xor_sync(~0u, sum, 8);

@@ -277,6 +277,11 @@ FP8MQA_API int fp8_mqa_topk_ex(const float* logits, int64_t M, int64_t N, int64_
  * n % page_size.  A table entry outside [0, pages) is a page that is not there: its positions
  * are never read.  Table entries past a sequence's length are not read either.
  *
+ * The first paged call on a device sets up its state (kernel attributes and a status word); make
+ * it before any stream capture, as for fp8_mqa_logits.  Kernels are launched so that their set-up
+ * overlaps the end of the kernel before them on the stream; what they read and write is ordered as
+ * ever.
+ *
  * Limits: dim is 64 or 128; data 16-byte aligned with strides of a multiple of 16 bytes;
  * pages * page_size < 2^31; strides are not negative.  Byte offsets are 64-bit throughout;
  * fp8_mqa_attention_paged counts a cache's rows in units of the greatest common divisor of its

@@ -367,6 +367,57 @@ def test_attention_unequal_value_scales():
     check_attention(np.random.default_rng(44), [700, 90], 8, 2, 128, 64, spread=2.0)
 
 
+def test_attention_huge_value_scale_of_a_row_that_the_softmax_rules_out():
+    # key 0 has value scales 2^60 times the others', and a score 200 or more below them: its weight is 0
+    # in 32 bits, and the other rows keep their bits
+    rng = np.random.default_rng(47)
+    kd, ks = cache(rng, 4, 64, 1, 128)
+    vd, vs = cache(rng, 4, 64, 1, 128)
+    q = torch.ones(1, 4, 128, device="cuda").to(torch.bfloat16)
+    kd.view(torch.uint8)[0, 0] = 0xF8                       # -256 in all columns
+    kd.view(torch.uint8)[0, 1:] &= 0x7F                     # the others: positive
+    kd.view(torch.uint8)[1:] &= 0x7F
+    ks.fill_(2.0 ** -4)
+    vs[0, 0] *= 2.0 ** 60
+    table, lens = gpu(np.array([[0, 1, 2, 3]], np.int32)), gpu(np.array([256], np.int32))
+    got = fm.attention_paged(q, kd, vd, table, lens, k_scale=ks, v_scale=vs).double().cpu().numpy()
+    want, _, size, dots = plain.attention(f64(q), as_rows(kd, ks), as_rows(vd, vs) * (np.arange(256).reshape(4, 64, 1, 1) > 0),
+                                          table.cpu().numpy(), [256], 128 ** -0.5)
+    dx = (128 + 8) * U * dots
+    tol = (2 * dx[..., None] + 2.0 ** -20 + 2.0 ** -11) * size + 2.0 ** -14 * size.max(-1, keepdims=True) + 2.0 ** -8 * np.abs(want)
+    assert np.all(np.abs(got - want) <= tol)
+
+
+def test_attention_zero_and_negative_value_scales():
+    rng = np.random.default_rng(48)
+    kd, ks = cache(rng, 2, 64, 2, 128)
+    vd, vs = cache(rng, 2, 64, 2, 128)
+    vs[0, ::3] *= -1.0
+    vs[1, ::2] = 0.0
+    q = torch.from_numpy(rng.standard_normal((2, 8, 128))).to(torch.bfloat16).cuda()
+    table, lens = np.array([[1, 0], [1, 0]], np.int32), np.array([128, 1], np.int32)
+    got = fm.attention_paged(q, kd, vd, gpu(table), gpu(lens), k_scale=ks, v_scale=vs).double().cpu().numpy()
+    want, _, size, dots = plain.attention(f64(q), as_rows(kd, ks), as_rows(vd, vs), table, lens, 128 ** -0.5)
+    tol = (2 * (128 + 8) * U * dots[..., None] + 2.0 ** -20 + 2.0 ** -11) * size + 2.0 ** -14 * size.max(-1, keepdims=True) \
+        + 2.0 ** -8 * np.abs(want)
+    assert np.all(np.abs(got - want) <= tol) and (got[1] == 0).all()
+
+
+def test_no_pages_at_all():
+    kd = torch.empty(0, 64, 2, 128, dtype=F8, device="cuda")
+    ks = torch.empty(0, 64, 2, device="cuda")
+    table, lens = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), gpu(np.array([100, 0], np.int32))
+    out, lse = fm.attention_paged(torch.ones(2, 8, 128, device="cuda").to(torch.bfloat16), kd, kd, table, lens, k_scale=ks,
+                                  v_scale=ks, return_lse=True)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    logits = fm.logits_paged(torch.ones(2, 1, 32, 128, device="cuda").to(F8), kd[:, :, :1], ks[:, :, :1],
+                             torch.ones(2, 1, 32, device="cuda"), table, lens)
+    assert torch.isneginf(logits).all()
+    rows, by = fm.cache_read(kd, ks, table, gpu(np.array([0, 100, 100], np.int32)), 100)
+    assert (rows.view(torch.uint8) == 0).all() and (by == 0).all()
+    fm.cache_write(gpu(np.array([0, 5], np.int32)), torch.ones(2, 2, 128, device="cuda"), kd, ks)
+
+
 def test_attention_beyond_the_length_is_not_read():
     # NaN in the rows past the length, in pages of other sequences and in padding changes nothing
     rng = np.random.default_rng(45)
