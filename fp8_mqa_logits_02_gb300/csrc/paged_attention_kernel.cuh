@@ -695,10 +695,11 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 // the row that the share begins within has `parts` shares, so parts - 1 such blocks, which divide the
 // 8 heads among them (of 33 shares or more, a quarter of a head's columns each).  A head's partial
 // results are divided among the block's warps, and a warp's lanes, so that many loads are under way.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinBatch = 8;  // partial results that a lane has under way
 
-template <int kDim>
-__global__ void __launch_bounds__(kJoinThreads)
+// kJoinWarps: 8, or 4, of which six blocks fit on an SM (most of a large grid's blocks find nothing to do).
+template <int kDim, int kJoinWarps>
+__global__ void __launch_bounds__(32 * kJoinWarps, kJoinWarps == 4 ? 6 : 3)
     paged_attention_join_kernel(const __grid_constant__ PagedAttentionParams p, int heads, int ctas)
 {
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
@@ -717,7 +718,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int step = helpers / slices;  // this block's heads: helper / slices + j * step
     const int mine = 8 / step + (helper / slices < 8 % step);
     // a power of two of heads at a time, the warps shared out among them
-    const int at_once = mine >= 8 ? 8 : mine >= 4 ? 4 : mine >= 2 ? 2 : 1, share = kJoinWarps / at_once;
+    const int at_once = min(kJoinWarps, mine >= 8 ? 8 : mine >= 4 ? 4 : mine >= 2 ? 2 : 1);
+    const int share = kJoinWarps / at_once;
     const int columns = kDim / 4 / slices;                 // float4s of a block's slice: lanes of a member
     const int sub = lane / columns, subs = 32 / columns;   // members at a time
     const int col = helper % slices * columns + lane % columns;
@@ -728,12 +730,11 @@ __global__ void __launch_bounds__(kJoinThreads)
         float m = -CUDART_INF_F, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (j < mine) {
-            constexpr int kBatch = 8;
-            for (int k0 = r * subs + sub; k0 - sub < n; k0 += share * subs * kBatch) {
-                float2 ml[kBatch];
-                float4 x[kBatch];
+            for (int k0 = r * subs + sub; k0 - sub < n; k0 += share * subs * kJoinBatch) {
+                float2 ml[kJoinBatch];
+                float4 x[kJoinBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
+                for (int i = 0; i < kJoinBatch; ++i) {
                     const int k = k0 + i * share * subs;
                     ml[i] = make_float2(-CUDART_INF_F, 0.0f);
                     x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -747,7 +748,7 @@ __global__ void __launch_bounds__(kJoinThreads)
                 }
                 float top = m;
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+                for (int i = 0; i < kJoinBatch; ++i) top = fmaxf(top, ml[i].x);
                 const float ref = top == -CUDART_INF_F ? 0.0f : top, c = exp2_fast(m - ref);
                 l *= c;
                 o.x *= c;
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(kJoinThreads)
                 o.z *= c;
                 o.w *= c;
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
+                for (int i = 0; i < kJoinBatch; ++i) {
                     const float f = exp2_fast(ml[i].x - ref);
                     l = fmaf(f, ml[i].y, l);
                     o.x = fmaf(f, x[i].x, o.x);
