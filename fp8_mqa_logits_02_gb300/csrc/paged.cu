@@ -230,11 +230,12 @@ void read_rows(CacheReadParams& p, int32_t dim, int sm_count, cudaStream_t s)
         launch_after(cache_read_kernel<Out, 128>, dim3(blocks), kCacheThreads, 0, s, p);
 }
 
-// Key heads that a CTA's warps take: side by side (up to four) where a CTA gets kAttnHeadTiles
-// tiles or more that way, else one, with four steps of its positions (fewer partial results).
-// Measured: 90 tiles a CTA (64 rows of up to 20001, 8 heads) 230 us side by side, 244 one by one;
-// 19 (16 rows of up to 16385, 4 heads, 16 bits) 62.6 and 60.5; 9 (64 rows of 2048 selected) 53 and 48.
-constexpr int64_t kAttnHeadTiles = 32;
+// Key heads that a CTA's warps take: two, side by side, where a CTA gets kAttnHeadTiles tiles or more
+// that way (of sequences that fill the table), else one, with four steps of its positions and so fewer
+// partial results.  Measured with 1, 2 and 4 (us): 64 rows of up to 20001 positions, 8 heads: 229, 218,
+// 218; 16 such rows: 67, 66, 67; 8 rows: 40, 40, 44; 32 rows of up to 16385, 4 heads, 16 bits: 97 with 1,
+// 94 with 2; 16 of them: 54, 53, 58; 64 rows of 2048 selected: 44.5, 43.0, 49.6.
+constexpr int64_t kAttnHeadTiles = 8;
 
 // The grid is a full wave, or fewer CTAs where there are fewer tiles, and a multiple of the chunks of
 // heads.
@@ -247,8 +248,7 @@ void attention_launch(PagedAttentionParams& p, int sm_count, cudaStream_t s)
     const int64_t wave = attention_wave(sm_count);
     const int64_t longest =
         std::max<int64_t>(1, p.n_indices >= 0 ? p.n_indices : int64_t(p.table.cols) * p.k.page_size);
-    p.hw = p.k.heads % 4 == 0 ? 4 : p.k.heads % 2 == 0 ? 2 : 1;
-    p.hw = std::min(p.hw, kAttnWarps / kHq);
+    p.hw = p.k.heads % 2 == 0 && kHq <= 2 ? 2 : 1;
     int64_t tile, chunks, tiles;
     for (;; p.hw = 1) {
         tile = S::kStep * (kAttnWarps / (p.hw * kHq));
@@ -499,10 +499,8 @@ uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t kv_hea
     // two partial results a CTA (heads x dim sums, and each head's m and l); a launch with more
     // chunks of heads than a wave has CTAs splits no row
     const int32_t group = q_heads / kv_heads;
-    const uint64_t heads = group > 32   ? 64
-                           : group > 16 ? 32 * (kv_heads % 2 == 0 ? 2 : 1)
-                                        : (group > 8 ? 16 : 8) *
-                                              (kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1);
+    const uint64_t heads =
+        group > 32 ? 64 : (group > 16 ? 32 : group > 8 ? 16 : 8) * (kv_heads % 2 == 0 ? 2 : 1);
     return kAttnMaxCtas * sizeof(AttnSplit) +
            2 * uint64_t(attention_wave(st->sm_count)) * heads * uint64_t(dim + 2) * sizeof(float);
 }

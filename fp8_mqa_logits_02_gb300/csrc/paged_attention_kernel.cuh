@@ -26,7 +26,7 @@
 // does.  E4M3 weights have the rows' value scales in them, 2^(x + log2 scale), and a running maximum of
 // their own, so that f16's range is enough whatever the scales' size.
 //
-// A CTA's four warps take hw key heads (1, 2 or 4) of the same positions and keep in step: the heads
+// A CTA's four warps take hw key heads (1 or 2) of the same positions and keep in step: the heads
 // of a position lie side by side in memory, and reading them together is what DRAM wants.  Groups of
 // more than 16 query heads are shared out to kHq warps that read one ring, so that the cache's bytes
 // reach an SM once for 32 or 64 heads.  The warps left over (4 / (hw kHq)) take further positions.
@@ -62,7 +62,7 @@ struct PagedAttentionParams {
     PagedView k, v;
     RowUnits k_units, v_units;
     int32_t same_rows;  // k_units and v_units are alike
-    int32_t hw;         // key heads that a CTA's warps take: 1, 2 or 4
+    int32_t hw;         // key heads that a CTA's warps take: 1 or 2
     PageTable table;
     const int32_t* lens;
     const int32_t* indices;
