@@ -49,6 +49,8 @@ constexpr int kAttnStages = 2;     // steps in a ring, for each warp that shares
 constexpr int kAttnCtasPerSm = 3;
 constexpr int kAttnMaxCtas = 512;  // of one launch
 
+constexpr float kAttnLag = 8.0f;   // powers of two
+
 // What CTA `me` of a chunk (me > 0) says of the row that its share begins within: the row's parts
 // are those of CTAs first .. first + parts - 1.  parts = 0: its share begins with a row.
 struct AttnSplit {
@@ -529,6 +531,10 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                         if (S::kE4m3) wide = fmaxf(wide, __shfl_xor_sync(~0u, wide, o));
                     }
                     if (!S::kE4m3) wide = top;
+                    // what the weights are relative to lags behind the largest score by kAttnLag at most
+                    // (weights up to 2^8 are as good), which spares most steps the rescaling of O
+                    if (!(top > m[nt][j] + kAttnLag)) top = m[nt][j];
+                    if (!(wide > w_top[nt][j] + kAttnLag)) wide = w_top[nt][j];
                     const float ref = top == -CUDART_INF_F ? 0.0f : top;
                     const float w_ref = wide == -CUDART_INF_F ? 0.0f : wide;
                     float sum = l[nt][j] * exp2_fast(m[nt][j] - ref);
