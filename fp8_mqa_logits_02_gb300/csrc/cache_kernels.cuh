@@ -183,11 +183,15 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
                 // a row that is not there has zeros and a zero scale
                 alignas(16) Out y[kPer];
 #pragma unroll
-                for (int k = 0; k < kPer / 2; ++k) {
-                    const uint32_t two = f16_of_e4m3(x[j][k / 2] >> (k % 2 * 16));
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
-                    y[2 * k] = from_float<Out>(__fmul_rn(f.x, by[j]));
-                    y[2 * k + 1] = from_float<Out>(__fmul_rn(f.y, by[j]));
+                for (int k = 0; k < kPer / 4; ++k) {
+                    uint32_t two[2];
+                    f16_of_e4m3(x[j][k], &two[0], &two[1]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two[h]));
+                        y[4 * k + 2 * h] = from_float<Out>(__fmul_rn(f.x, by[j]));
+                        y[4 * k + 2 * h + 1] = from_float<Out>(__fmul_rn(f.y, by[j]));
+                    }
                 }
                 out[i] = *reinterpret_cast<const uint4*>(y);
             }

@@ -478,10 +478,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                         const int s = j * kSteps + y;
                         uint32_t a0, a1, a2, a3;
                         if constexpr (S::kE4m3) {
-                            a0 = f16_of_e4m3(w0[y]);
-                            a1 = f16_of_e4m3(w1[y]);
-                            a2 = f16_of_e4m3(w0[y] >> 16);
-                            a3 = f16_of_e4m3(w1[y] >> 16);
+                            f16_of_e4m3(w0[y], &a0, &a2);
+                            f16_of_e4m3(w1[y], &a1, &a3);
                         } else {
                             a0 = w0[2 * y];
                             a1 = w1[2 * y];
@@ -598,12 +596,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                     uint32_t a0, a1, a2, a3;
                     if constexpr (S::kE4m3) {
                         const uint32_t sel = i % 2 ? 0x7362 : 0x5140;
-                        const uint32_t lo2 = __byte_perm(w[0][i / 2], w[1][i / 2], sel);
-                        const uint32_t hi2 = __byte_perm(w[2][i / 2], w[3][i / 2], sel);
-                        a0 = f16_of_e4m3(lo2);
-                        a1 = f16_of_e4m3(lo2 >> 16);
-                        a2 = f16_of_e4m3(hi2);
-                        a3 = f16_of_e4m3(hi2 >> 16);
+                        f16_of_e4m3(__byte_perm(w[0][i / 2], w[1][i / 2], sel), &a0, &a1);
+                        f16_of_e4m3(__byte_perm(w[2][i / 2], w[3][i / 2], sel), &a2, &a3);
                     } else {
                         a0 = __byte_perm(w[0][i], w[1][i], 0x5410);
                         a1 = __byte_perm(w[0][i], w[1][i], 0x7632);

@@ -67,12 +67,13 @@ __device__ __forceinline__ bool locate(const PagedView& c, const PageTable& t, i
     return uint32_t(*page) < uint32_t(c.pages);
 }
 
-// Two E4M3 values (the low 16 bits) as two f16 values: exact.
-__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t two)
+// Four E4M3 values as f16 values, the first two in *lo: exact.
+__device__ __forceinline__ void f16_of_e4m3(uint32_t four, uint32_t* lo, uint32_t* hi)
 {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(two)));
-    return r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(*lo), "=r"(*hi)
+        : "r"(four));
 }
 
 template <class T>
