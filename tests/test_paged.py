@@ -491,6 +491,56 @@ def test_attention_is_the_same_every_time_and_on_any_stream():
         assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
 
 
+def test_calls_see_what_the_kernel_before_them_wrote():
+    # steps whose kernels follow one another closely (each is set up while the one before ends) give what
+    # the same steps give with the device idle between any two
+    rng = np.random.default_rng(56)
+    B, page, cols, steps = 3, 16, 8, 60
+    first = {}
+    for name, heads in (("k", 2), ("v", 2), ("i", 1)):
+        first[name] = cache(rng, B * cols, page, heads, 128)
+    table = torch.arange(B * cols, dtype=torch.int32, device="cuda").view(B, cols)
+    x = torch.from_numpy(rng.standard_normal((steps, B, 5, 128))).to(torch.bfloat16).cuda()
+    q = torch.from_numpy(rng.standard_normal((steps, B, 8, 128))).to(torch.bfloat16).cuda()
+    q8 = torch.from_numpy(rng.standard_normal((steps, B, 1, 32, 128))).float().to(F8).cuda()
+    w = torch.from_numpy(rng.standard_normal((steps, B, 1, 32)).astype(np.float32)).cuda()
+
+    def run(pause):
+        c = {n: (d.clone(), s.clone()) for n, (d, s) in first.items()}
+        lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        starts = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+        slots = torch.empty(B, dtype=torch.int32, device="cuda")
+        out = []
+        for t in range(steps):
+            torch.add(torch.arange(B, dtype=torch.int32, device="cuda") * cols * page, lens, out=slots)
+            pause()
+            fm.cache_write(slots, x[t, :, :2], *c["k"], x[t, :, 2:4], *c["v"])
+            pause()
+            fm.cache_write(slots, x[t, :, 4:], *c["i"])
+            pause()
+            lens.add_(1)
+            starts[1:] = lens.cumsum(0)
+            pause()
+            logits = fm.logits_paged(q8[t], *c["i"], w[t], table, lens)
+            pause()
+            idx, _ = fm.topk(logits, 8)
+            pause()
+            out += [logits, idx, fm.attention_paged(q[t], c["k"][0], c["v"][0], table, lens, k_scale=c["k"][1],
+                                                    v_scale=c["v"][1], indices=idx)]
+            pause()
+            out.append(fm.attention_paged(q[t], c["k"][0], c["v"][0], table, lens, k_scale=c["k"][1], v_scale=c["v"][1]))
+            pause()
+            out.append(fm.cache_read(*c["k"], table, starts, B * (t + 1), dtype=torch.float32))
+            pause()
+        torch.cuda.synchronize()
+        return out
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, b in zip(run(lambda: None), want):
+            assert torch.equal(a, b)
+
+
 def test_operators_in_a_graph():
     rng = np.random.default_rng(53)
     a = _attention_inputs(54)
