@@ -576,6 +576,19 @@ def test_operators_in_a_graph():
             assert torch.equal(g, e)
 
 
+def test_the_bounds_checking_library_has_the_operators_too():
+    a = _attention_inputs(57)
+    want = fm.attention_paged(*a)
+    fm.use_debug_library(True)
+    try:
+        got = fm.attention_paged(*a)
+        torch.cuda.synchronize()
+        assert fm.check_error() == 0
+    finally:
+        fm.use_debug_library(False)
+    assert torch.equal(got, want)
+
+
 def test_refusals_on_the_gpu():
     q, kd, vd, table, lens, _, ks, vs = _attention_inputs(55)
     call = fm.attention_paged
