@@ -272,15 +272,22 @@ void attention_launch(PagedAttentionParams& p, int sm_count, cudaStream_t s)
         launch_after(paged_attention_join_kernel<kDim, 4>, grid, 128, 0, s, p, block, int(per_chunk));
 }
 
-// A warp takes up to 8 query heads of a group, or 16; groups of more than 16 go to two or four warps
-// that share a ring.
+// A warp takes up to 8 query heads of a group, or 16.  Groups of more than 16 go to two or four warps
+// that share a ring where the shares are long enough (steps a warp would take if the sequences fill the
+// table), else to CTAs of their own, whose warps wait for nobody.  Measured, shared and not (us): groups
+// of 32 with 176 steps 458 and 492, 36 steps 84.3 and 85.8, 8 steps 58 and 51, 2 steps 23.7 and 22.9;
+// groups of 64 with 22 steps 125 and 132, 9 steps 117 and 130; groups of 128 with 2 steps 73 and 67.
 template <int kType, int kDim>
 void attention_heads(PagedAttentionParams& p, int sm_count, cudaStream_t s)
 {
+    using S = AttnShape<kType, kDim, 2, 1>;
     const int group = p.q_heads / p.k.heads;
+    const int64_t longest = p.n_indices >= 0 ? p.n_indices : int64_t(p.table.cols) * p.k.page_size;
+    const int64_t steps = p.B * ((longest + S::kStep - 1) / S::kStep) * p.k.heads /
+                          (attention_wave(sm_count) * kAttnWarps);
     if (group <= 8)
         attention_launch<kType, kDim, 1, 1>(p, sm_count, s);
-    else if (group <= 16)
+    else if (group <= 16 || steps < (group <= 32 ? 32 : 8))
         attention_launch<kType, kDim, 2, 1>(p, sm_count, s);
     else if (group <= 32)
         attention_launch<kType, kDim, 2, 2>(p, sm_count, s);

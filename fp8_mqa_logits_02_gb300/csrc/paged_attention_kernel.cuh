@@ -28,12 +28,12 @@
 //
 // A CTA's four warps take hw key heads (1 or 2) of the same positions and keep in step: the heads
 // of a position lie side by side in memory, and reading them together is what DRAM wants.  Groups of
-// more than 16 query heads are shared out to kHq warps that read one ring, so that the cache's bytes
+// more than 16 query heads may be shared out to kHq warps that read one ring, so that the cache's bytes
 // reach an SM once for 32 or 64 heads.  The warps left over (4 / (hw kHq)) take further positions.
 //
 // Measured: 64 rows of up to 20001 positions, 64 query and 8 key heads (1.37 GB) 223 us, 6.2 TB/s of 6.7;
 // 16 rows of a 16-bit cache (285 MB) 54 us; 2048 selected of 32768 positions for 64 rows (140 MB in rows
-// of 128 bytes anywhere) 43 us; one row of 131072 positions, 32 query heads of one key head, 24 us, where
+// of 128 bytes anywhere) 43 us; one row of 131072 positions, 32 query heads of one key head, 23 us, where
 // the steps' latency and the join decide.
 //
 // Split and join: for each chunk of heads the rows' tiles (the CTA's steps) are laid end to end,

@@ -266,11 +266,11 @@ def test_logits_feed_topk():
 # ------------------------------------------------------------------------------------ attention
 
 def check_attention(rng, lens, q_heads, heads, dim, page, dtype=torch.bfloat16, kind=F8, layout="plain", select=None,
-                    holes=False, fused=False, shared=False, sharp=1.0, spread=None, indices=None):
+                    holes=False, fused=False, shared=False, sharp=1.0, spread=None, indices=None, cols=None):
     lens = np.asarray(lens, np.int32)
     B = len(lens)
     kind = dtype if kind is None else kind
-    table, pages = tables(rng, lens[:1] if shared else lens, page)
+    table, pages = tables(rng, lens[:1] if shared else lens, page, cols=cols)
     if holes:
         table[0, -1] = -7
         table[-1, 0] = pages
@@ -320,6 +320,30 @@ def test_attention_types_and_lengths(lens, page, dim, dtype, kind):
                                            (128, 2), (64, 8)])
 def test_attention_head_layouts(q_heads, heads, kind):
     check_attention(np.random.default_rng(q_heads), [65, 200], q_heads, heads, 128, 48, kind=kind)
+
+
+@pytest.mark.parametrize("dtype,kind", TYPES)
+@pytest.mark.parametrize("q_heads,heads,dim", [(2, 2, 128), (8, 2, 64), (12, 4, 128), (32, 2, 128), (64, 4, 64), (48, 6, 128)])
+def test_attention_key_heads_side_by_side(q_heads, heads, dim, dtype, kind):
+    # two key heads share a CTA where the shares may be long: room for 16 tiles of 64 positions a CTA
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    cols = 16 * 64 * 3 * sms // (2 * heads // 2 * 64)
+    rng = np.random.default_rng(q_heads + heads)
+    check_attention(rng, [300, 33], q_heads, heads, dim, 64, dtype, kind, cols=cols)
+    check_attention(rng, [4000, 0], q_heads, heads, dim, 64, dtype, kind, cols=cols, layout="heads")
+
+
+@pytest.mark.parametrize("dtype,kind", TYPES)
+@pytest.mark.parametrize("q_heads,heads,dim", [(17, 1, 128), (32, 1, 64), (64, 2, 128), (33, 1, 128), (64, 1, 64), (100, 1, 128),
+                                               (256, 2, 128)])
+def test_attention_groups_that_share_a_ring(q_heads, heads, dim, dtype, kind):
+    # wide groups share a ring where the shares may be long: the table has room for that, the sequences
+    # are short (64 steps a warp of 3 CTAs an SM, of 32 positions)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    cols = 64 * 32 * 4 * 3 * sms // (2 * heads * 64)
+    rng = np.random.default_rng(q_heads)
+    check_attention(rng, [300, 33], q_heads, heads, dim, 64, dtype, kind, cols=cols)
+    check_attention(rng, [4000, 0], q_heads, heads, dim, 64, dtype, kind, cols=cols)
 
 
 @pytest.mark.parametrize("kind", [F8, None])
