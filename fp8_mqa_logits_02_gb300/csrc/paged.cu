@@ -62,8 +62,10 @@ bool attention_smem()
 }
 
 // Launches a kernel that begins with griddepcontrol.wait: it is set up while the one before it ends.
+// Its own result says whether it is under way (the runtime's last error may be an older one of the
+// caller's).
 template <class... Params, class... Args>
-void launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
                   const Args&... args)
 {
     cudaLaunchAttribute attr;
@@ -76,7 +78,7 @@ void launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kernel, args...);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 void init_paged(int dev, PagedDevice& st)
@@ -185,11 +187,18 @@ bool row_units(const PagedView& v, RowUnits* u)
     return true;
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? FP8MQA_OK : FP8MQA_ERR_LAUNCH; }
+// What an entry point returns for its launches' result; a refusal is not left behind for the caller's
+// next look at the last error.
+int launched(cudaError_t e)
+{
+    if (e == cudaSuccess) return FP8MQA_OK;
+    cudaGetLastError();
+    return FP8MQA_ERR_LAUNCH;
+}
 
 // Rows of x that start on 16 bytes are read 16 bytes at a time, others value by value.
 template <class X, int kDim, int kTensors>
-void write_tensors(const CacheWriteParams& p, cudaStream_t s)
+cudaError_t write_tensors(const CacheWriteParams& p, cudaStream_t s)
 {
     const int64_t rows = p.T * p.heads, per = kCacheThreads / (kDim / 16);
     const unsigned blocks = unsigned((rows + per - 1) / per);
@@ -197,19 +206,15 @@ void write_tensors(const CacheWriteParams& p, cudaStream_t s)
     for (int i = 0; i < kTensors; ++i)
         vec = vec && on(p.x[i], 16) && p.row_stride[i] * int64_t(sizeof(X)) % 16 == 0 &&
               p.head_stride[i] * int64_t(sizeof(X)) % 16 == 0;
-    if (vec)
-        launch_after(cache_write_kernel<X, kDim, true, kTensors>, dim3(blocks), kCacheThreads, 0, s, p);
-    else
-        launch_after(cache_write_kernel<X, kDim, false, kTensors>, dim3(blocks), kCacheThreads, 0, s, p);
+    return vec ? launch_after(cache_write_kernel<X, kDim, true, kTensors>, dim3(blocks), kCacheThreads, 0, s, p)
+               : launch_after(cache_write_kernel<X, kDim, false, kTensors>, dim3(blocks), kCacheThreads, 0, s, p);
 }
 
 template <class X>
-void write_rows(const CacheWriteParams& p, int32_t dim, int tensors, cudaStream_t s)
+cudaError_t write_rows(const CacheWriteParams& p, int32_t dim, int tensors, cudaStream_t s)
 {
-    if (dim == 64)
-        tensors == 1 ? write_tensors<X, 64, 1>(p, s) : write_tensors<X, 64, 2>(p, s);
-    else
-        tensors == 1 ? write_tensors<X, 128, 1>(p, s) : write_tensors<X, 128, 2>(p, s);
+    if (dim == 64) return tensors == 1 ? write_tensors<X, 64, 1>(p, s) : write_tensors<X, 64, 2>(p, s);
+    return tensors == 1 ? write_tensors<X, 128, 1>(p, s) : write_tensors<X, 128, 2>(p, s);
 }
 
 // A block packs about kReadTurns x kReadPieces pieces a thread (finding the rows costs a block its
@@ -217,17 +222,15 @@ void write_rows(const CacheWriteParams& p, int32_t dim, int tensors, cudaStream_
 // than leaves two blocks an SM.
 constexpr int64_t kReadTurns = 4;
 template <class Out>
-void read_rows(CacheReadParams& p, int32_t dim, int sm_count, cudaStream_t s)
+cudaError_t read_rows(CacheReadParams& p, int32_t dim, int sm_count, cudaStream_t s)
 {
     const int64_t row_pieces = int64_t(p.cache.heads) * dim * int64_t(sizeof(Out)) / 16;
     const int64_t rows = std::min(kReadTurns * kReadPieces * kCacheThreads / row_pieces,
                                   p.total / (2 * sm_count));
     p.block_rows = int32_t(std::max<int64_t>(1, std::min<int64_t>(kReadRows, rows)));
     const unsigned blocks = unsigned((p.total + p.block_rows - 1) / p.block_rows);
-    if (dim == 64)
-        launch_after(cache_read_kernel<Out, 64>, dim3(blocks), kCacheThreads, 0, s, p);
-    else
-        launch_after(cache_read_kernel<Out, 128>, dim3(blocks), kCacheThreads, 0, s, p);
+    return dim == 64 ? launch_after(cache_read_kernel<Out, 64>, dim3(blocks), kCacheThreads, 0, s, p)
+                     : launch_after(cache_read_kernel<Out, 128>, dim3(blocks), kCacheThreads, 0, s, p);
 }
 
 // Key heads that a CTA's warps take: two, side by side, where a CTA gets kAttnHeadTiles tiles or more
@@ -240,7 +243,7 @@ constexpr int64_t kAttnHeadTiles = 8;
 // The grid is a full wave, or fewer CTAs where there are fewer tiles, and a multiple of the chunks of
 // heads.
 template <int kType, int kDim, int kNT, int kHq>
-void attention_launch(PagedAttentionParams& p, int sm_count, cudaStream_t s)
+cudaError_t attention_launch(PagedAttentionParams& p, int sm_count, cudaStream_t s)
 {
     using S = AttnShape<kType, kDim, kNT, kHq>;
     const int block = kHq * S::kHeads;
@@ -257,9 +260,10 @@ void attention_launch(PagedAttentionParams& p, int sm_count, cudaStream_t s)
         if (p.hw == 1 || tiles * chunks >= kAttnHeadTiles * wave) break;
     }
     const int64_t per_chunk = std::min(tiles, std::max<int64_t>(1, wave / chunks));
-    launch_after(paged_attention_kernel<kType, kDim, kNT, kHq>, dim3(unsigned(per_chunk * chunks)),
-                 kAttnThreads, S::kSmem, s, p);
-    if (per_chunk == 1) return;  // nothing is split
+    const cudaError_t e = launch_after(paged_attention_kernel<kType, kDim, kNT, kHq>,
+                                       dim3(unsigned(per_chunk * chunks)), kAttnThreads, S::kSmem, s, p);
+    // without the first kernel there is nothing in the workspace that the second one could join
+    if (e != cudaSuccess || per_chunk == 1) return e;  // per_chunk 1: nothing is split
     // of a row's blocks 32 at most have work; those of a single row come first
     const int64_t shares = p.B == 1 ? std::min<int64_t>(per_chunk - 1, 32) : per_chunk - 1;
     const dim3 grid(unsigned(shares), unsigned(chunks * p.hw * kHq * kNT));
@@ -267,9 +271,8 @@ void attention_launch(PagedAttentionParams& p, int sm_count, cudaStream_t s)
     // one row of 456 shares takes 14.5 us in all with 8 warps a block and 16.0 with 4, 64 rows of three
     // or four 231 and 223
     if (per_chunk >= 32 * p.B)
-        launch_after(paged_attention_join_kernel<kDim, 8>, grid, 256, 0, s, p, block, int(per_chunk));
-    else
-        launch_after(paged_attention_join_kernel<kDim, 4>, grid, 128, 0, s, p, block, int(per_chunk));
+        return launch_after(paged_attention_join_kernel<kDim, 8>, grid, 256, 0, s, p, block, int(per_chunk));
+    return launch_after(paged_attention_join_kernel<kDim, 4>, grid, 128, 0, s, p, block, int(per_chunk));
 }
 
 // A warp takes up to 8 query heads of a group, or 16.  Groups of more than 16 go to two or four warps
@@ -278,30 +281,23 @@ void attention_launch(PagedAttentionParams& p, int sm_count, cudaStream_t s)
 // of 32 with 176 steps 458 and 492, 36 steps 84.3 and 85.8, 8 steps 58 and 51, 2 steps 23.7 and 22.9;
 // groups of 64 with 22 steps 125 and 132, 9 steps 117 and 130; groups of 128 with 2 steps 73 and 67.
 template <int kType, int kDim>
-void attention_heads(PagedAttentionParams& p, int sm_count, cudaStream_t s)
+cudaError_t attention_heads(PagedAttentionParams& p, int sm_count, cudaStream_t s)
 {
     using S = AttnShape<kType, kDim, 2, 1>;
     const int group = p.q_heads / p.k.heads;
     const int64_t longest = p.n_indices >= 0 ? p.n_indices : int64_t(p.table.cols) * p.k.page_size;
     const int64_t steps = p.B * ((longest + S::kStep - 1) / S::kStep) * p.k.heads /
                           (attention_wave(sm_count) * kAttnWarps);
-    if (group <= 8)
-        attention_launch<kType, kDim, 1, 1>(p, sm_count, s);
-    else if (group <= 16 || steps < (group <= 32 ? 32 : 8))
-        attention_launch<kType, kDim, 2, 1>(p, sm_count, s);
-    else if (group <= 32)
-        attention_launch<kType, kDim, 2, 2>(p, sm_count, s);
-    else
-        attention_launch<kType, kDim, 2, 4>(p, sm_count, s);
+    if (group <= 8) return attention_launch<kType, kDim, 1, 1>(p, sm_count, s);
+    if (group <= 16 || steps < (group <= 32 ? 32 : 8)) return attention_launch<kType, kDim, 2, 1>(p, sm_count, s);
+    if (group <= 32) return attention_launch<kType, kDim, 2, 2>(p, sm_count, s);
+    return attention_launch<kType, kDim, 2, 4>(p, sm_count, s);
 }
 
 template <int kType>
-void attention_dim(PagedAttentionParams& p, int32_t dim, int sm_count, cudaStream_t s)
+cudaError_t attention_dim(PagedAttentionParams& p, int32_t dim, int sm_count, cudaStream_t s)
 {
-    if (dim == 64)
-        attention_heads<kType, 64>(p, sm_count, s);
-    else
-        attention_heads<kType, 128>(p, sm_count, s);
+    return dim == 64 ? attention_heads<kType, 64>(p, sm_count, s) : attention_heads<kType, 128>(p, sm_count, s);
 }
 
 // Whether TMA fetches the keys.  It can where a page's rows lie evenly apart, pages a whole number of
@@ -329,7 +325,7 @@ bool paged_maps(PagedLogitsParams& p, uint32_t tokens, CUtensorMap* map_k, CUten
 
 // One launch of the paged logits, kTok tokens a CTA: a full wave, or a CTA for each tile and span.
 template <int kTok>
-void logits_launch(PagedLogitsParams& p, int sm_count, cudaStream_t s)
+cudaError_t logits_launch(PagedLogitsParams& p, int sm_count, cudaStream_t s)
 {
     using S = PagedShape<kTok, true>;
     const int64_t work = p.B * ((p.N + kPagedTile - 1) / kPagedTile);
@@ -337,10 +333,9 @@ void logits_launch(PagedLogitsParams& p, int sm_count, cudaStream_t s)
     const dim3 grid(unsigned(std::min(work, wave)), unsigned((p.T + kTok - 1) / kTok));
     CUtensorMap map_k = {}, map_q = {};
     if (paged_maps(p, kTok, &map_k, &map_q))
-        launch_after(paged_logits_kernel<kTok, true>, grid, S::kThreads, S::kSmem, s, p, map_k, map_q);
-    else
-        launch_after(paged_logits_kernel<kTok, false>, grid, PagedShape<kTok, false>::kThreads,
-                     PagedShape<kTok, false>::kSmem, s, p, map_k, map_q);
+        return launch_after(paged_logits_kernel<kTok, true>, grid, S::kThreads, S::kSmem, s, p, map_k, map_q);
+    return launch_after(paged_logits_kernel<kTok, false>, grid, PagedShape<kTok, false>::kThreads,
+                        PagedShape<kTok, false>::kSmem, s, p, map_k, map_q);
 }
 
 }  // namespace
@@ -398,13 +393,10 @@ int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const v
     p.cache[0] = view_of(*cache, x);
     p.cache[1] = view_of(cache2 ? *cache2 : *cache, x);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (x_type == FP8MQA_BF16)
-        write_rows<__nv_bfloat16>(p, cache->dim, x2 ? 2 : 1, s);
-    else if (x_type == FP8MQA_F16)
-        write_rows<__half>(p, cache->dim, x2 ? 2 : 1, s);
-    else
-        write_rows<float>(p, cache->dim, x2 ? 2 : 1, s);
-    return launched();
+    const int tensors = x2 ? 2 : 1;
+    return launched(x_type == FP8MQA_BF16  ? write_rows<__nv_bfloat16>(p, cache->dim, tensors, s)
+                    : x_type == FP8MQA_F16 ? write_rows<__half>(p, cache->dim, tensors, s)
+                                           : write_rows<float>(p, cache->dim, tensors, s));
 }
 
 int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t table_stride,
@@ -438,15 +430,10 @@ int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t 
     p.out = out;
     p.out_scale = out_scale;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (out_type == FP8MQA_E4M3)
-        read_rows<uint8_t>(p, cache->dim, st->sm_count, s);
-    else if (out_type == FP8MQA_BF16)
-        read_rows<__nv_bfloat16>(p, cache->dim, st->sm_count, s);
-    else if (out_type == FP8MQA_F16)
-        read_rows<__half>(p, cache->dim, st->sm_count, s);
-    else
-        read_rows<float>(p, cache->dim, st->sm_count, s);
-    return launched();
+    return launched(out_type == FP8MQA_E4M3   ? read_rows<uint8_t>(p, cache->dim, st->sm_count, s)
+                    : out_type == FP8MQA_BF16 ? read_rows<__nv_bfloat16>(p, cache->dim, st->sm_count, s)
+                    : out_type == FP8MQA_F16  ? read_rows<__half>(p, cache->dim, st->sm_count, s)
+                                              : read_rows<float>(p, cache->dim, st->sm_count, s));
 }
 
 int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_t T, int32_t H,
@@ -487,13 +474,9 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
     p.wait_ns = wait_limit_ns();
     if (!row_units(p.keys, &p.units)) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (T == 1)
-        logits_launch<1>(p, st->sm_count, s);
-    else if (T == 2)
-        logits_launch<2>(p, st->sm_count, s);
-    else
-        logits_launch<4>(p, st->sm_count, s);
-    return launched();
+    return launched(T == 1   ? logits_launch<1>(p, st->sm_count, s)
+                    : T == 2 ? logits_launch<2>(p, st->sm_count, s)
+                             : logits_launch<4>(p, st->sm_count, s));
 }
 
 uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t dim)
@@ -570,13 +553,9 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     p.splits = static_cast<AttnSplit*>(workspace);
     p.partial = reinterpret_cast<float*>(p.splits + kAttnMaxCtas);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (k->type == FP8MQA_E4M3)
-        attention_dim<FP8MQA_E4M3>(p, k->dim, st->sm_count, s);
-    else if (k->type == FP8MQA_BF16)
-        attention_dim<FP8MQA_BF16>(p, k->dim, st->sm_count, s);
-    else
-        attention_dim<FP8MQA_F16>(p, k->dim, st->sm_count, s);
-    return launched();
+    return launched(k->type == FP8MQA_E4M3   ? attention_dim<FP8MQA_E4M3>(p, k->dim, st->sm_count, s)
+                    : k->type == FP8MQA_BF16 ? attention_dim<FP8MQA_BF16>(p, k->dim, st->sm_count, s)
+                                             : attention_dim<FP8MQA_F16>(p, k->dim, st->sm_count, s));
 }
 
 }  // extern "C"
