@@ -20,8 +20,7 @@ namespace {
 constexpr int kPagedMaxDevices = 64;
 
 struct PagedDevice {
-    std::once_flag once;
-    int init_status = FP8MQA_OK;
+    std::mutex setting_up;
     int sm_count = 0;
     int32_t* status = nullptr;  // status word of the paged logits
     std::atomic<bool> ready{false};
@@ -81,38 +80,34 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-void init_paged(int dev, PagedDevice& st)
+int init_paged(int dev, PagedDevice& st)
 {
     int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&st.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         cudaGetLastError();
-        st.init_status = FP8MQA_ERR_CUDA;
-        return;
+        return FP8MQA_ERR_CUDA;
     }
-    if (major != 10 || minor != 3) {
-        st.init_status = FP8MQA_ERR_ARCH;
-        return;
-    }
+    if (major != 10 || minor != 3) return FP8MQA_ERR_ARCH;
     if (!attention_smem<FP8MQA_E4M3>() || !attention_smem<FP8MQA_BF16>() ||
         !attention_smem<FP8MQA_F16>() ||
         !logits_smem<1>() || !logits_smem<2>() || !logits_smem<4>()) {
         cudaGetLastError();
-        st.init_status = FP8MQA_ERR_LAUNCH;
-        return;
+        return FP8MQA_ERR_LAUNCH;
     }
     void* buf = nullptr;
     if (cudaMalloc(&buf, 256) != cudaSuccess || cudaMemset(buf, 0, 256) != cudaSuccess) {
-        cudaGetLastError();
         cudaFree(buf);
-        st.init_status = FP8MQA_ERR_CUDA;
-        return;
+        cudaGetLastError();
+        return FP8MQA_ERR_CUDA;
     }
     st.status = static_cast<int32_t*>(buf);
-    st.ready.store(true, std::memory_order_release);
+    return FP8MQA_OK;
 }
 
+// The current device's state, set up by the first call that succeeds in it: what fails once (no memory
+// left, a stream being captured) is tried again by the next call.
 PagedDevice* paged_device(int* err)
 {
     int dev = -1;
@@ -122,9 +117,15 @@ PagedDevice* paged_device(int* err)
         return nullptr;
     }
     PagedDevice& st = g_paged[dev];
-    std::call_once(st.once, [dev, &st] { init_paged(dev, st); });
-    *err = st.init_status;
-    return st.init_status == FP8MQA_OK ? &st : nullptr;
+    *err = FP8MQA_OK;
+    if (st.ready.load(std::memory_order_acquire)) return &st;
+    const std::lock_guard<std::mutex> lock(st.setting_up);
+    if (!st.ready.load(std::memory_order_relaxed)) {
+        *err = init_paged(dev, st);
+        if (*err != FP8MQA_OK) return nullptr;
+        st.ready.store(true, std::memory_order_release);
+    }
+    return &st;
 }
 
 bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }

@@ -107,3 +107,12 @@ def test_an_older_error_is_not_taken_for_a_launch(lib, name):
     lib.fake_set(0, 0, 700)          # some earlier call of the program failed
     assert call() == OK and lib.fake_launches() >= 1
     assert lib.fake_last() == 700    # and its error is still there to be seen
+
+
+def test_a_set_up_that_failed_is_tried_again(lib):
+    # say, in a stream capture or with the memory used up: the calls after it work
+    lib.fake_set(0, 1, 0)
+    assert attention(lib) == CUDA and lib.fake_launches() == 0
+    assert lib.fake_last() == 0
+    assert attention(lib) == OK and lib.fake_launches() == 2
+    assert all(call() == OK for call in calls(lib).values())
