@@ -98,6 +98,14 @@ struct PagedShape {
     static constexpr int kAccFull = kItem + kItems, kAccEmpty = kAccFull + 2;
     static constexpr int kSlotEmpty = kAccEmpty + 2, kBars = kSlotEmpty + kSlots;
     static constexpr uint32_t kSmem = kOffBar + 8 * kBars + 1024;  // slack for aligning the base
+    // The first tile whose copies onto a ring of `ring` places may be under way when the copy warp stops
+    // before tile j, or has ended with it: those of tile i have landed once the copies of tile i + ring
+    // begin, and the end takes its places as a tile does.
+    static constexpr int32_t under_way(int32_t j, bool ended, int32_t ring)
+    {
+        const int32_t i = j - ring + (ended ? 1 : 0);
+        return i > 0 ? i : 0;
+    }
     // D f32, A = B = E4M3, both K-major, M = 128 keys
     static constexpr uint32_t kIdesc = (1u << 4) | ((kN >> 3) << 17) | (uint32_t(kPagedTile >> 4) << 24);
 };
@@ -387,11 +395,12 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
                 ptx::mbar_arrive(bar(S::kFull + j % S::kStages));
                 ptx::mbar_arrive(bar(S::kItem + j % S::kItems));
             }
-            // the copies under way land before this CTA's memory goes, whoever gave up
-            for (int32_t i = max(0, j - S::kStages + (ok ? 1 : 0)); i < j; ++i) {
+            // the copies under way land before this CTA's memory goes, whoever gave up (that a tile has
+            // been multiplied says that its keys have landed, not its scales)
+            for (int32_t i = S::under_way(j, ok, S::kStages); i < j; ++i)
                 drain(bar(S::kFull + i % S::kStages), uint32_t(i / S::kStages) & 1u);
+            for (int32_t i = S::under_way(j, ok, S::kItems); i < j; ++i)
                 drain(bar(S::kItem + i % S::kItems), uint32_t(i / S::kItems) & 1u);
-            }
         } else {
             copy_wait<0>();
             if (ok) report(j + 1);  // the last tiles, and the end
