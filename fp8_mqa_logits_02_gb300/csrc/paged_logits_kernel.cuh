@@ -101,7 +101,7 @@ struct PagedShape {
     // The first tile whose copies onto a ring of `ring` places may be under way when the copy warp stops
     // before tile j, or has ended with it: those of tile i have landed once the copies of tile i + ring
     // begin, and the end takes its places as a tile does.
-    static constexpr int32_t under_way(int32_t j, bool ended, int32_t ring)
+    __host__ __device__ static constexpr int32_t under_way(int32_t j, bool ended, int32_t ring)
     {
         const int32_t i = j - ring + (ended ? 1 : 0);
         return i > 0 ? i : 0;
