@@ -473,6 +473,7 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
     p.clean = clean_logits;
     p.status = st->status;
     p.wait_ns = wait_limit_ns();
+    p.suspend_ns = uint32_t(std::clamp<uint64_t>(p.wait_ns, 32, kPagedSuspendNs));
     if (!row_units(p.keys, &p.units)) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return launched(T == 1   ? logits_launch<1>(p, st->sm_count, s)

@@ -48,6 +48,7 @@ struct PagedLogitsParams {
     int32_t T, clean;
     int32_t* status;
     uint64_t wait_ns;
+    uint32_t suspend_ns;     // of one suspension within a wait, at most
     int32_t box, box_shift;  // kTma: rows of a piece, 2^box_shift
     uint32_t page_rows;      // kTma: rows of the tensor map from page to page
 };
@@ -62,6 +63,9 @@ constexpr int kPagedMmaK = 32;     // E4M3 values of a tcgen05.mma
 constexpr int kPagedFill = 1024;  // columns of a -inf span
 constexpr int32_t kPagedTimeout = 1;           // status bit: a bounded wait gave up
 constexpr uint64_t kPagedDrainNs = 1000000000ull;  // bound of the last wait before a CTA gives up
+// A suspended thread wakes when its phase completes, or after this (a shorter limit of the wait bounds
+// it too) to see whether the wait has run out or another warp has given up.
+constexpr uint32_t kPagedSuspendNs = 20000;
 
 // A tile in the ring.
 struct alignas(16) PagedItem {
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
     auto wait = [&](int i, uint32_t parity) {
         if (ptx::mbar_try_wait(bar(i), parity)) return true;
         const uint64_t start = ptx::globaltimer_ns();
-        while (!ptx::mbar_try_wait_sleep(bar(i), parity, 20000)) {
+        while (!ptx::mbar_try_wait_sleep(bar(i), parity, p.suspend_ns)) {
             if (s_stop) return false;
             if (ptx::globaltimer_ns() - start > p.wait_ns) {
                 s_stop = 1;
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
     // Waits for what is under way, whether or not the CTA gives up, for kPagedDrainNs at most.
     auto drain = [&](uint32_t at, uint32_t parity) {
         const uint64_t start = ptx::globaltimer_ns();
-        while (!ptx::mbar_try_wait_sleep(at, parity, 20000) &&
+        while (!ptx::mbar_try_wait_sleep(at, parity, kPagedSuspendNs) &&
                ptx::globaltimer_ns() - start <= kPagedDrainNs) {
         }
     };
