@@ -444,11 +444,12 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
 #pragma unroll
                 for (int h = 0; h < kPagedHeads; h += 4) {
                     const float4 wh = *reinterpret_cast<const float4*>(w + t * kPagedHeads + h);
-                    y0 = fma2(make_float2(fmaxf(__uint_as_float(x[h]), 0.0f),
-                                          fmaxf(__uint_as_float(x[h + 1]), 0.0f)),
+                    // relu of NaN is NaN, so that it does not pass for data
+                    y0 = fma2(make_float2(max_nan(__uint_as_float(x[h]), 0.0f),
+                                          max_nan(__uint_as_float(x[h + 1]), 0.0f)),
                               make_float2(wh.x, wh.y), y0);
-                    y1 = fma2(make_float2(fmaxf(__uint_as_float(x[h + 2]), 0.0f),
-                                          fmaxf(__uint_as_float(x[h + 3]), 0.0f)),
+                    y1 = fma2(make_float2(max_nan(__uint_as_float(x[h + 2]), 0.0f),
+                                          max_nan(__uint_as_float(x[h + 3]), 0.0f)),
                               make_float2(wh.z, wh.w), y1);
                 }
                 const bool seen = n < len && n < len_full - (p.T - 1 - (t0 + t));

@@ -355,7 +355,8 @@ FP8MQA_API int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* tabl
  *                     for n in [0, lens[b] - (T - 1 - t)),   -inf elsewhere (clean_logits = 1)
  *
  * with k and scale the rows of sequence b (token t of the T newest sees the cache up to itself).
- * Positions on pages that are not there are -inf with either clean_logits.
+ * Positions on pages that are not there are -inf with either clean_logits.  A NaN in a query, a key, a
+ * weight or a scale is NaN in the logits that it belongs to (fp8_mqa_topk passes over them).
  *
  *   q_fp8     DEVICE [B, T, H, D] E4M3, contiguous, 16-byte aligned; H = 32, D = 128.
  *   w         DEVICE [B, T, H] float32, contiguous, 16-byte aligned.
