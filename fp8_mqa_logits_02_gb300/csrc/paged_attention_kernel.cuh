@@ -21,10 +21,15 @@
 // fill a fragment, so a group's heads are taken 8 or 16 at a time.
 //
 // E4M3 values become f16 exactly; a row's key scale multiplies its scores, its value scale its
-// weights.  Weights are rounded to 16 bits for the second product (the fp32 sum takes them
-// unrounded): f16's 11 bits cost 2^-12 of a weight, an eighth of what rounding the result to bfloat16
-// does.  E4M3 weights have the rows' value scales in them, 2^(x + log2 scale), and a running maximum of
-// their own, so that f16's range is enough whatever the scales' size.
+// weights.  Weights are rounded to 16 bits for the second product, which the matrix units want (the fp32
+// sum takes them unrounded).  f16 has 11 bits: 2^-11 of a weight at most, an eighth of what rounding
+// the result to bfloat16 may cost and as much as rounding it to f16 may.  Its range is used to the top: the
+// reference of the weights counts 2^kAttnLift, so that a weight loses bits below 2^-21 of the reference
+// only and is 0 below 2^-32.  (With the reference at 1 it was 2^-14 and 2^-25: 32767 positions of weight
+// 2^-25.4 next to one of 1 lost a quarter of their part of the result.)  E4M3 weights have the rows' value
+// scales in them, 2^(x + log2 scale), and a running maximum of their own, so that this holds whatever the
+// scales' size.  Weights over bfloat16 caches are bfloat16, 8 bits (2^-8 of a weight at most), with fp32's
+// range.
 //
 // A CTA's four warps take hw key heads (1 or 2) of the same positions and keep in step: the heads
 // of a position lie side by side in memory, and reading them together is what DRAM wants.  Groups of
@@ -56,7 +61,10 @@ constexpr int kAttnStages = 2;
 constexpr int kAttnCtasPerSm = 3;
 constexpr int kAttnMaxCtas = 512;  // of one launch
 
-constexpr float kAttnLag = 8.0f;   // powers of two
+// Powers of two: how far the weights' reference may lag behind the largest score, and what the reference
+// counts for in f16 weights; together they keep to f16's range (2^15 < 65504).
+constexpr float kAttnLag = 8.0f;
+constexpr float kAttnLift = 7.0f;
 
 // What CTA `me` of a chunk (me > 0) says of the row that its share begins within: the row's parts
 // are those of CTAs first .. first + parts - 1.  parts = 0: its share begins with a row.
@@ -541,6 +549,9 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                     // with bfloat16 weights, where a largest weight of 1 is one that is not rounded
                     // (16 rows of up to 16385: error 2.0e-3, 2.4e-3 with the lag)
                     if constexpr (!S::kBf16) {
+                        // (l has the reference of the weights where those are its own terms)
+                        if constexpr (!S::kE4m3) top -= kAttnLift;
+                        wide -= kAttnLift;
                         if (!(top > m[nt][j] + kAttnLag)) top = m[nt][j];
                         if (!(wide > w_top[nt][j] + kAttnLag)) wide = w_top[nt][j];
                     }
