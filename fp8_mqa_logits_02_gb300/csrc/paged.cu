@@ -515,9 +515,10 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
         k->dim != v->dim || q_heads % k->heads != 0 ||
         (k->type != FP8MQA_E4M3 && k->type != q_type))
         return FP8MQA_ERR_INVALID_ARG;
-    // tiles (of 16 positions or more) are counted in 32 bits
+    // tiles (of 16 positions or more) are counted in 32 bits, and so are positions, up to a few steps
+    // (of 128 positions at most) past a row's end
     const int64_t longest = n_indices >= 0 ? n_indices : int64_t(table_cols) * k->page_size;
-    if (B >= int64_t(1) << 31 || longest >= int64_t(1) << 31 || B * (longest / 16 + 1) >= int64_t(1) << 31)
+    if (B >= int64_t(1) << 31 || longest > kAttnMaxPositions || B * (longest / 16 + 1) >= int64_t(1) << 31)
         return FP8MQA_ERR_UNSUPPORTED_SHAPE;
     if (B == 0) return FP8MQA_OK;
     if (!q || !lens || !out || !workspace || (table_cols > 0 && !table) ||

@@ -60,6 +60,7 @@ constexpr int kAttnThreads = 128, kAttnWarps = kAttnThreads / 32;
 constexpr int kAttnStages = 2;
 constexpr int kAttnCtasPerSm = 3;
 constexpr int kAttnMaxCtas = 512;  // of one launch
+constexpr int64_t kAttnMaxPositions = INT32_MAX - 1024;  // of a row
 
 // Powers of two: how far the weights' reference may lag behind the largest score, and what the reference
 // counts for in f16 weights; together they keep to f16's range (2^15 < 65504).

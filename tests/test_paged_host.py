@@ -12,7 +12,7 @@ import fp8_mqa_logits_02_gb300 as fm
 from fp8_mqa_logits_02_gb300 import nvcc_build
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-OK, LAUNCH, CUDA = 0, -5, -7
+OK, UNSUPPORTED, LAUNCH, CUDA = 0, -2, -5, -7
 E4M3, BF16 = 0, 1
 P = 0x1000  # an aligned address that is never read
 CALLS = ("cudaGetDevice", "cudaDeviceGetAttribute", "cudaFuncSetAttribute", "cudaMalloc", "cudaFree", "cudaMemset",
@@ -116,3 +116,18 @@ def test_a_set_up_that_failed_is_tried_again(lib):
     assert lib.fake_last() == 0
     assert attention(lib) == OK and lib.fake_launches() == 2
     assert all(call() == OK for call in calls(lib).values())
+
+
+@pytest.mark.parametrize("page", [1, 64, 1024])
+def test_attention_counts_positions_in_32_bits(lib, page):
+    # rows that end within a few steps of 2^31 positions: the places past their end would not be counted
+    c = cache(pages=4, page=page)
+    most = (2 ** 31 - 1025) // page
+    assert attention(lib, cols=most, c=c) == OK and lib.fake_launches() == 2
+    for cols in (most + 1, (2 ** 31 - 1) // page):
+        assert attention(lib, cols=cols, c=c) == UNSUPPORTED and lib.fake_launches() == 2
+
+    def selected(n):
+        return lib.fp8_mqa_attention_paged(P, BF16, 1, 8, 1024, 128, c, c, P, 9, 9, P, P, n, n, 1.0, P, P, P, 1 << 40, None)
+    assert selected(2 ** 31 - 1025) == OK
+    assert selected(2 ** 31 - 1024) == selected(2 ** 31 - 1) == UNSUPPORTED
