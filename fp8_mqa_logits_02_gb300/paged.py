@@ -10,6 +10,8 @@ calls for every layer and token); layouts and limits are stated in ``include/fp8
 A cache is a tensor ``data [pages, page_size, heads, dim]`` (float8_e4m3fn, or for
 ``attention_paged`` also bfloat16 or float16) and, for e4m3, ``scale [pages, page_size, heads]``
 float32.  Strides are free but for the last of ``data``, which is 1.
+
+``stream`` (default: the current one of the tensors' device) is a stream of the tensors' device.
 """
 from __future__ import annotations
 
@@ -49,6 +51,15 @@ def _binding():
     return _compiled
 
 
+def _on(stream, like):
+    """The context of a call on ``stream``.  Its kernels go to the device of the call's tensors (``like`` is
+    one), so a stream of another device is refused."""
+    device = getattr(like, "device", None)
+    if device is not None and device.type == "cuda" and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
+    return torch.cuda.stream(stream)
+
+
 def load() -> None:
     """Load the compiled binding (the first call of any operator does the same)."""
     _binding()
@@ -66,7 +77,7 @@ def cache_write(slots: torch.Tensor, k: torch.Tensor, k_data: torch.Tensor, k_sc
     """
     call = _binding().cache_write
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, k_data):
             return call(slots, k, k_data, k_scale, v, v_data, v_scale)
     return call(slots, k, k_data, k_scale, v, v_data, v_scale)
 
@@ -84,7 +95,7 @@ def cache_read(data: torch.Tensor, scale: torch.Tensor, table: torch.Tensor, sta
     """
     call = _binding().cache_read
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, data):
             return call(data, scale, table, starts, total, dtype)
     return call(data, scale, table, starts, total, dtype)
 
@@ -103,7 +114,7 @@ def logits_paged(q: torch.Tensor, data: torch.Tensor, scale: torch.Tensor, w: to
     """
     call = _binding().logits_paged
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return call(q, data, scale, w, table, lens, max_len, out, clean_logits)
     return call(q, data, scale, w, table, lens, max_len, out, clean_logits)
 
@@ -124,7 +135,7 @@ def attention_paged(q: torch.Tensor, k_data: torch.Tensor, v_data: torch.Tensor,
     """
     call = _binding().attention_paged
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return call(q, k_data, v_data, table, lens, sm_scale, k_scale, v_scale, indices, return_lse)
     return call(q, k_data, v_data, table, lens, sm_scale, k_scale, v_scale, indices, return_lse)
 
