@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -80,50 +81,76 @@ def _binding(out: str) -> list:
             "-o", out, BINDING_SOURCE, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
+def _run(jobs: dict) -> dict:
+    """Runs the commands side by side; their output by name, and whether each succeeded."""
+    running, done = {}, {}
+    for what, cmd in jobs.items():
+        try:
+            running[what] = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+        except OSError as e:  # no such compiler
+            done[what] = (False, str(e))
+    for what, proc in running.items():
+        out, _ = proc.communicate()
+        done[what] = (proc.returncode == 0, out)
+    return done
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool | None = None) -> str:
     """Build the library (debug=False), its bounds-checking variant (debug=True), or both
     at once (debug=None, the default; returns the regular library's path), and the binding.
     Each is rebuilt only when a source is newer, unless `force`.  All translation units
-    compile at the same time."""
+    compile at the same time.
+
+    Each output stands for itself: what compiles is put in place.  A library that does not build
+    raises RuntimeError; the binding needs the host compiler and torch's headers as well, and where it
+    cannot be built there is a warning, the rest of the library works, and the paged operators raise."""
     targets = [False, True] if debug is None else [bool(debug)]
-    jobs, links = [], []  # (what, command); (library, temporary, objects)
     tag = f".tmp{os.getpid()}"
+    jobs, objects = {}, {}  # name: command; library: {name: object}
     for dbg in targets:
         lib = DEBUG_LIB if dbg else LIB
         if not force and up_to_date(lib):
             continue
-        objects = []
+        objects[lib] = {}
         for source in SOURCES:
-            objects.append(f"{lib}.{os.path.basename(source)}{tag}.o")
-            jobs.append((f"{os.path.basename(lib)} ({os.path.basename(source)})",
-                         _compile(source, objects[-1], dbg, verbose)))
-        links.append((lib, lib + tag, objects))
-    if force or not up_to_date(BINDING):
-        jobs.append((os.path.basename(BINDING), _binding(BINDING + tag)))
-        links.append((BINDING, BINDING + tag, None))
-    running = [(what, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
-               for what, cmd in jobs]
+            what = f"{os.path.basename(lib)} ({os.path.basename(source)})"
+            objects[lib][what] = f"{lib}.{os.path.basename(source)}{tag}.o"
+            jobs[what] = _compile(source, objects[lib][what], dbg, verbose)
+    binding, no_binding = os.path.basename(BINDING), ""
+    try:
+        if force or not up_to_date(BINDING):
+            jobs[binding] = _binding(BINDING + tag)
+    except ImportError as e:  # no torch
+        no_binding = str(e)
+    done = _run(jobs)
+    if verbose:
+        sys.stderr.write("".join(out for ok, out in done.values() if ok))
     failed = []
-    for what, proc in running:
-        out, _ = proc.communicate()
-        if proc.returncode != 0:
-            failed.append(f"compiling {what} failed:\n{out}")
-        elif verbose:
-            sys.stderr.write(out)
-    for lib, tmp, objects in links if not failed else []:
-        if objects is not None:
-            done = subprocess.run([nvcc_path(), *ARCH_FLAGS, "-shared", "-o", tmp, *objects],
-                                  stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-            if done.returncode != 0:
-                failed.append(f"linking {os.path.basename(lib)} failed:\n{done.stdout}")
-                continue
-        os.replace(tmp, lib)
-    for _, tmp, objects in links:
-        for path in [tmp, *(objects or [])]:
+    for lib, parts in objects.items():
+        wrong = [f"compiling {what} failed:\n{done[what][1]}" for what in parts if not done[what][0]]
+        if not wrong:
+            ok, out = _run({lib: [nvcc_path(), *ARCH_FLAGS, "-shared", "-o", lib + tag, *parts.values()]})[lib]
+            if ok:
+                os.replace(lib + tag, lib)
+            else:
+                wrong = [f"linking {os.path.basename(lib)} failed:\n{out}"]
+        failed += wrong
+        for path in [lib + tag, *parts.values()]:
+            if os.path.exists(path):
+                os.remove(path)
+    if binding in done:
+        if done[binding][0]:
+            os.replace(BINDING + tag, BINDING)
+        else:
+            no_binding = done[binding][1]
+    if no_binding:
+        for path in (BINDING + tag, BINDING):  # one from other sources would not go with the library
             if os.path.exists(path):
                 os.remove(path)
     if failed:
         raise RuntimeError("\n".join(failed))
+    if no_binding:
+        warnings.warn(f"the paged operators are not available: building {binding} failed:\n{no_binding}", stacklevel=2)
     return DEBUG_LIB if debug else LIB
 
 
