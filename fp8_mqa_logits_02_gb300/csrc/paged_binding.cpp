@@ -85,6 +85,9 @@ const at::Tensor& ints(PyObject* o, const char* name, const c10::Device& device,
                                   (dims == 2 ? ", any], got " : "], got ") + list(t.sizes()));
     if (t.size(dims - 1) > 1 && t.stride(dims - 1) != 1)
         bad(PyExc_ValueError, std::string(name) + " must be contiguous in its last dimension");
+    // the C interface takes the columns as an int32
+    if (dims == 2 && t.size(1) > INT32_MAX)
+        bad(PyExc_ValueError, std::string(name) + " is too large: " + list(t.sizes()));
     return t;
 }
 
