@@ -86,8 +86,9 @@ def build(force: bool = False, verbose: bool = False, debug: bool | None = None)
 
 def use_debug_library(on: bool) -> None:
     """Route every later call of this module through ``libfp8mqa_debug.so``, the build whose
-    kernel checks each global access first and records a violation (``check_error`` then
-    returns FP8MQA_ERR_BOUNDS) instead of making it; ``False`` switches back."""
+    kernels (of the prefill logits and the paged operators; the top-k is the same) check each
+    global access first and record a violation (``check_error`` then returns FP8MQA_ERR_BOUNDS)
+    instead of making it; ``False`` switches back."""
     global _debug
     _debug = bool(on)
 

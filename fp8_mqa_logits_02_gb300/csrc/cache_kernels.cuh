@@ -16,19 +16,23 @@ struct CacheWriteParams {
     const void* x[2];
     int64_t row_stride[2], head_stride[2];
     PagedView cache[2];
+    PagedBounds bounds;
 };
 
 // Lane c's 16 values of a row as floats: pieces c, c + kLanes, ... of 16 bytes, so that the lanes of a
 // row load (and store) side by side.  kVec: x lies on 16 bytes.
 template <class X, bool kVec, int kLanes>
-__device__ __forceinline__ void load16(const X* x, int c, float (&v)[16])
+__device__ __forceinline__ void load16(const PagedBounds& bounds, int kind, const X* x, int c, float (&v)[16])
 {
     constexpr int kPer = 16 / sizeof(X);
 #pragma unroll
     for (int i = 0; i < 16 / kPer; ++i) {
         alignas(16) X raw[kPer];
         const X* const at = x + (c + i * kLanes) * kPer;
-        if constexpr (kVec) {
+        if (!in_bounds(bounds, kind, at, 16)) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) raw[j] = from_float<X>(0.0f);
+        } else if constexpr (kVec) {
             *reinterpret_cast<uint4*>(raw) = __ldcs(reinterpret_cast<const uint4*>(at));
         } else {
 #pragma unroll
@@ -51,11 +55,12 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid
     const bool row = at < uint32_t(p.T * p.heads);
     const int32_t t = row ? p.by_heads.of(int32_t(at)) : 0, h = row ? int32_t(at) - t * p.heads : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int32_t slot = row ? p.slots[t] : -1;
+    const int32_t slot = row && in_bounds(p.bounds, kMemSlots, p.slots + t, 4) ? p.slots[t] : -1;
     float v[kTensors][16];
 #pragma unroll
     for (int i = 0; i < kTensors; ++i)
         load16<X, kVec, kLanes>(
+            p.bounds, kMemRows + i,
             static_cast<const X*>(p.x[i]) + t * p.row_stride[i] + h * p.head_stride[i], c, v[i]);
     const int32_t page = p.by_page.of(max(slot, 0)), r = slot - page * p.cache[0].page_size;
 #pragma unroll
@@ -82,15 +87,20 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid
         uint8_t* const to = cache.data + page * cache.page_stride + r * cache.row_stride +
                             h * cache.head_stride + c * kPer;
         if constexpr (kPer == 8) {
-            *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
-            *reinterpret_cast<uint2*>(to + 8 * kLanes) = make_uint2(out[2], out[3]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (in_bounds(p.bounds, kMemData + i, to + 8 * kLanes * j, 8))
+                    *reinterpret_cast<uint2*>(to + 8 * kLanes * j) = make_uint2(out[2 * j], out[2 * j + 1]);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(to + 4 * kLanes * j) = out[j];
+            for (int j = 0; j < 4; ++j)
+                if (in_bounds(p.bounds, kMemData + i, to + 4 * kLanes * j, 4))
+                    *reinterpret_cast<uint32_t*>(to + 4 * kLanes * j) = out[j];
         }
-        if (c == 0)
-            cache.scale[page * cache.scale_page_stride + r * cache.scale_row_stride +
-                        h * cache.scale_head_stride] = __fmul_rn(a, 1.0f / kE4m3Max);
+        float* const to_scale = cache.scale + page * cache.scale_page_stride +
+                                r * cache.scale_row_stride + h * cache.scale_head_stride;
+        if (c == 0 && in_bounds(p.bounds, kMemScale + i, to_scale, 4))
+            *to_scale = __fmul_rn(a, 1.0f / kE4m3Max);
     }
 }
 
@@ -103,18 +113,20 @@ struct CacheReadParams {
     int32_t block_rows;  // output rows of a block, kReadRows at most
     void* out;
     float* out_scale;
+    PagedBounds bounds;
 };
 constexpr int kReadRows = 128;
 
 constexpr int kReadPieces = 4;  // pieces of 16 bytes of output that a thread has under way
 
 // The sequence of output row r: the last b with starts[b] <= r (B where r is past the end).
-__device__ __forceinline__ int64_t sequence_of(const int32_t* starts, int64_t B, int64_t r)
+template <class Starts>
+__device__ __forceinline__ int64_t sequence_of(const Starts& starts, int64_t B, int64_t r)
 {
     int64_t lo = 0, hi = B + 1;  // the first b with starts[b] > r lies in [lo, hi]
     while (lo < hi) {
         const int64_t mid = (lo + hi) / 2;
-        if (starts[mid] > r) hi = mid;
+        if (starts(mid) > r) hi = mid;
         else lo = mid + 1;
     }
     return lo - 1;
@@ -132,10 +144,11 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
     const int rows = int(min(int64_t(p.block_rows), p.total - r0));
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x < rows) {
-        const int64_t r = r0 + threadIdx.x, b = sequence_of(p.starts, p.B, r);
+        auto starts = [&](int64_t b) { return in_bounds(p.bounds, kMemLens, p.starts + b, 4) ? p.starts[b] : 0; };
+        const int64_t r = r0 + threadIdx.x, b = sequence_of(starts, p.B, r);
         int32_t page = 0, row = 0;
         const bool there =
-            b >= 0 && b < p.B && locate(c, p.table, b, int32_t(r - p.starts[b]), &page, &row);
+            b >= 0 && b < p.B && locate(p.bounds, c, p.table, b, int32_t(r - starts(b)), &page, &row);
         s_data[threadIdx.x] = there ? page * c.page_stride + row * c.row_stride : -1;
         s_scale[threadIdx.x] = page * c.scale_page_stride + row * c.scale_row_stride;
     }
@@ -155,8 +168,10 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
             if (i < n) {
                 const int row = p.by_heads.of(at), h = at - row * c.heads;
                 const int64_t off = s_data[row];
-                if (off >= 0) {
-                    const uint8_t* const src = c.data + off + h * c.head_stride + i % kLanes * kPer;
+                const uint8_t* const src = c.data + off + h * c.head_stride + i % kLanes * kPer;
+                const float* const src_scale = c.scale + s_scale[row] + h * c.scale_head_stride;
+                if (off >= 0 && in_bounds(p.bounds, kMemData, src, kPer) &&
+                    in_bounds(p.bounds, kMemScale, src_scale, 4)) {
                     if constexpr (kPer == 16) {
                         const uint4 y = __ldcs(reinterpret_cast<const uint4*>(src));
                         x[j][0] = y.x;
@@ -170,7 +185,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
                     } else {
                         x[j][0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
                     }
-                    by[j] = *(c.scale + s_scale[row] + h * c.scale_head_stride);
+                    by[j] = *src_scale;
                 }
             }
         }
@@ -178,9 +193,11 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
         for (int j = 0; j < kReadPieces; ++j) {
             const int i = i0 + j * kCacheThreads;
             if (i >= n) break;
+            if (!in_bounds(p.bounds, kMemOut, out + i, 16)) continue;
             if constexpr (kPer == 16) {
                 out[i] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
-                if (i % kLanes == 0) p.out_scale[r0 * c.heads + i / kLanes] = by[j];
+                float* const to_scale = p.out_scale + r0 * c.heads + i / kLanes;
+                if (i % kLanes == 0 && in_bounds(p.bounds, kMemOutScale, to_scale, 4)) *to_scale = by[j];
             } else {
                 // a row that is not there has zeros and a zero scale
                 alignas(16) Out y[kPer];

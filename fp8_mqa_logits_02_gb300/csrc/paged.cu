@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <cstdio>
 #include <mutex>
 #include <numeric>
 
@@ -188,6 +189,45 @@ bool row_units(const PagedView& v, RowUnits* u)
     return true;
 }
 
+// What the bounds-checking build holds a launch's accesses against, from the call's arguments alone; in the
+// library nothing of it is there.
+#ifdef FP8MQA_DEBUG_BOUNDS
+std::atomic<uint64_t> g_short[kMemKinds];  // bytes that a kind's memory is taken to be short of (tests)
+#endif
+void spans(PagedBounds& b, int kind, const void* from, int64_t bytes)
+{
+#ifdef FP8MQA_DEBUG_BOUNDS
+    b.from[kind] = reinterpret_cast<uint64_t>(from);
+    b.bytes[kind] = bytes > 0 ? uint64_t(bytes) - std::min(uint64_t(bytes), g_short[kind].load()) : 0;
+#endif
+}
+PagedBounds bounds_for(const PagedDevice& st)
+{
+    PagedBounds b = {};
+#ifdef FP8MQA_DEBUG_BOUNDS
+    b.status = st.status;
+#endif
+    return b;
+}
+// Bytes from the first to past the last of n0 x n1 x n2 places, `size` bytes each, at strides in bytes.
+int64_t extent(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t size)
+{
+    return n0 > 0 && n1 > 0 && n2 > 0 ? (n0 - 1) * s0 + (n1 - 1) * s1 + (n2 - 1) * s2 + size : 0;
+}
+void spans(PagedBounds& b, int which, const PagedView& c, int64_t row_bytes)
+{
+    spans(b, kMemData + which, c.data,
+          extent(c.pages, c.page_stride, c.page_size, c.row_stride, c.heads, c.head_stride, row_bytes));
+    if (c.scale)
+        spans(b, kMemScale + which, c.scale,
+              extent(c.pages, 4 * c.scale_page_stride, c.page_size, 4 * c.scale_row_stride, c.heads,
+                     4 * c.scale_head_stride, 4));
+}
+void spans(PagedBounds& b, const PageTable& t, int64_t B)
+{
+    spans(b, kMemTable, t.ids, extent(B, 4 * t.stride, t.cols, 4, 1, 0, 4));
+}
+
 // What an entry point returns for its launches' result; a refusal is not left behind for the caller's
 // next look at the last error.
 int launched(cudaError_t e)
@@ -345,16 +385,31 @@ bool paged_take_status(int dev, int32_t* flags)
 {
     const PagedDevice& st = g_paged[dev];
     if (!st.ready.load(std::memory_order_acquire)) return true;
-    int32_t word = 0;
-    if (cudaMemcpy(&word, st.status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return false;
-    if (word != 0 && cudaMemset(st.status, 0, sizeof(word)) != cudaSuccess) return false;
-    *flags |= word;
+    uint64_t word[2] = {0, 0};  // the flags, and the bounds-checking build's record
+    if (cudaMemcpy(word, st.status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return false;
+    if (word[1] != 0)
+        std::fprintf(stderr,
+                     "fp8mqa: bounds violation recorded: paged kind %u, byte offset %lld "
+                     "(kinds: 1 slots, 2-3 rows, 4-5 data, 6-7 scale, 8 table, 9 lens or starts, 10 indices, "
+                     "11 q, 12 w, 13 out, 14 out scale or lse, 15-16 workspace)\n",
+                     unsigned(word[1] >> 48), static_cast<long long>(word[1] << 16) >> 16);
+    if ((word[0] != 0 || word[1] != 0) && cudaMemset(st.status, 0, sizeof(word)) != cudaSuccess) return false;
+    *flags |= int32_t(word[0]);
     return true;
 }
 
 }  // namespace fp8mqa
 
 extern "C" {
+
+#ifdef FP8MQA_DEBUG_BOUNDS
+// For tests of the checks: a kind's memory is taken to end `bytes` earlier in the calls that follow, whose
+// accesses there are then recorded and not made.
+FP8MQA_API void fp8_mqa_debug_bounds_short(int32_t kind, uint64_t bytes)
+{
+    if (kind > 0 && kind < fp8mqa::kMemKinds) fp8mqa::g_short[kind].store(bytes);
+}
+#endif
 
 int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const void* x,
                         int64_t x_row_stride, int64_t x_head_stride, const fp8mqa_cache* cache,
@@ -378,7 +433,8 @@ int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const v
     const uintptr_t e = uintptr_t(size_of(x_type));
     if (!on(slots, 4) || !on(x, e) || (x2 && !on(x2, e))) return FP8MQA_ERR_MISALIGNED;
     int err = FP8MQA_OK;
-    if (!paged_device(&err)) return err;
+    const PagedDevice* st = paged_device(&err);
+    if (!st) return err;
     CacheWriteParams p;
     p.slots = slots;
     p.T = T;
@@ -393,6 +449,13 @@ int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const v
     p.head_stride[1] = x2_head_stride;
     p.cache[0] = view_of(*cache, x);
     p.cache[1] = view_of(cache2 ? *cache2 : *cache, x);
+    p.bounds = bounds_for(*st);
+    spans(p.bounds, kMemSlots, slots, 4 * T);
+    for (int i = 0; i < (x2 ? 2 : 1); ++i) {
+        spans(p.bounds, kMemRows + i, p.x[i],
+              extent(T, p.row_stride[i] * int64_t(e), p.heads, p.head_stride[i] * int64_t(e), 1, 0, cache->dim * int64_t(e)));
+        spans(p.bounds, i, p.cache[i], cache->dim);
+    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int tensors = x2 ? 2 : 1;
     return launched(x_type == FP8MQA_BF16  ? write_rows<__nv_bfloat16>(p, cache->dim, tensors, s)
@@ -430,6 +493,12 @@ int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t 
     p.by_heads = FastDiv(uint32_t(cache->heads));
     p.out = out;
     p.out_scale = out_scale;
+    p.bounds = bounds_for(*st);
+    spans(p.bounds, 0, p.cache, cache->dim);
+    spans(p.bounds, p.table, B);
+    spans(p.bounds, kMemLens, starts, 4 * (B + 1));
+    spans(p.bounds, kMemOut, out, total * cache->heads * cache->dim * size_of(out_type));
+    spans(p.bounds, kMemOutScale, out_scale, 4 * total * cache->heads);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return launched(out_type == FP8MQA_E4M3   ? read_rows<uint8_t>(p, cache->dim, st->sm_count, s)
                     : out_type == FP8MQA_BF16 ? read_rows<__nv_bfloat16>(p, cache->dim, st->sm_count, s)
@@ -475,6 +544,13 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
     p.wait_ns = wait_limit_ns();
     p.suspend_ns = uint32_t(std::clamp<uint64_t>(p.wait_ns, 32, kPagedSuspendNs));
     if (!row_units(p.keys, &p.units)) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
+    p.bounds = bounds_for(*st);
+    spans(p.bounds, 0, p.keys, kPagedDim);
+    spans(p.bounds, p.table, B);
+    spans(p.bounds, kMemLens, lens, 4 * B);
+    spans(p.bounds, kMemQ, q_fp8, B * T * kPagedHeads * kPagedDim);
+    spans(p.bounds, kMemW, w, B * T * kPagedHeads * 4);
+    spans(p.bounds, kMemOut, out, extent(B * T, 4 * ld, N, 4, 1, 0, 4));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return launched(T == 1   ? logits_launch<1>(p, st->sm_count, s)
                     : T == 2 ? logits_launch<2>(p, st->sm_count, s)
@@ -555,6 +631,17 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     p.q_bf16 = q_type == FP8MQA_BF16;
     p.splits = static_cast<AttnSplit*>(workspace);
     p.partial = reinterpret_cast<float*>(p.splits + kAttnMaxCtas);
+    p.bounds = bounds_for(*st);
+    spans(p.bounds, 0, p.k, k->dim * size_of(k->type));
+    spans(p.bounds, 1, p.v, v->dim * size_of(v->type));
+    spans(p.bounds, p.table, B);
+    spans(p.bounds, kMemLens, lens, 4 * B);
+    spans(p.bounds, kMemIndices, indices, extent(B, 4 * indices_stride, n_indices, 4, 1, 0, 4));
+    spans(p.bounds, kMemQ, q, extent(B, 2 * q_row_stride, q_heads, 2 * q_head_stride, 1, 0, 2 * int64_t(k->dim)));
+    spans(p.bounds, kMemOut, out, B * q_heads * k->dim * 2);
+    spans(p.bounds, kMemOutScale, lse, lse ? 4 * B * q_heads : 0);
+    spans(p.bounds, kMemSplits, p.splits, kAttnMaxCtas * int64_t(sizeof(AttnSplit)));
+    spans(p.bounds, kMemPartial, p.partial, int64_t(workspace_bytes - kAttnMaxCtas * sizeof(AttnSplit)));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return launched(k->type == FP8MQA_E4M3   ? attention_dim<FP8MQA_E4M3>(p, k->dim, st->sm_count, s)
                     : k->type == FP8MQA_BF16 ? attention_dim<FP8MQA_BF16>(p, k->dim, st->sm_count, s)

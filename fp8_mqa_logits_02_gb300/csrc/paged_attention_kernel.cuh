@@ -94,6 +94,7 @@ struct PagedAttentionParams {
     float* lse;
     float* partial;  // [2 * CTAs][heads of a CTA][dim], then m and l [2 * CTAs][heads of a CTA][2]
     AttnSplit* splits;  // [CTAs of a chunk]
+    PagedBounds bounds;
 };
 
 // kType: FP8MQA_E4M3, FP8MQA_BF16 or FP8MQA_F16 of the cache.  kNT: eights of heads of a warp.
@@ -193,7 +194,11 @@ struct AttnRows {
     __device__ int32_t count(int64_t b) const
     {
         if (p.n_indices >= 0) return p.n_indices;
-        const int64_t n = p.lens[b];
+        return length(b);
+    }
+    __device__ int32_t length(int64_t b) const
+    {
+        const int64_t n = in_bounds(p.bounds, kMemLens, p.lens + b, 4) ? p.lens[b] : 0;
         return int32_t(n < 0 ? 0 : n < cap ? n : cap);
     }
     // a row with nothing still has one tile, which writes its empty result
@@ -211,8 +216,9 @@ __device__ __forceinline__ void attn_store(const PagedAttentionParams& p, int64_
         two = make_uint2(pack16<true>(v.x * inv, v.y * inv), pack16<true>(v.z * inv, v.w * inv));
     else
         two = make_uint2(pack16<false>(v.x * inv, v.y * inv), pack16<false>(v.z * inv, v.w * inv));
-    static_cast<uint2*>(p.out)[head * (kDim / 4) + i] = two;
-    if (p.lse && i == 0)
+    uint2* const to = static_cast<uint2*>(p.out) + head * (kDim / 4) + i;
+    if (in_bounds(p.bounds, kMemOut, to, 8)) *to = two;
+    if (p.lse && i == 0 && in_bounds(p.bounds, kMemOutScale, p.lse + head, 4))
         p.lse[head] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
@@ -272,7 +278,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     }
     const int32_t ctas = min(int32_t(gridDim.x) / chunks, total);
     if (me >= ctas) {
-        if (chunk == 0 && tid == 0) p.splits[me].parts = 0;
+        if (chunk == 0 && tid == 0 && in_bounds(p.bounds, kMemSplits, p.splits + me, sizeof(AttnSplit)))
+            p.splits[me].parts = 0;
         return;
     }
     // `more` CTAs have each + 1 tiles, the others each
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         const int32_t count = rows.count(b), n_tiles = rows.tiles(b);
         const int32_t lo = at - row_start, hi = min(n_tiles, end - row_start);
         const int h0 = kvh * group + h_first;
-        const int32_t len = int32_t(min(int64_t(max(p.lens[b], 0)), rows.cap));
+        const int32_t len = rows.length(b);
 
         // ---- Q: the words of this lane's columns, two values each
         uint32_t qf[kNT][S::kMT][2];
@@ -327,7 +334,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             for (int w = 0; w < 2 * S::kMT; w += 4) {
                 const int d = w / kRun * (8 * kRun) + t * (2 * kRun) + w % kRun * 2;
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (h < n_heads) x = *(reinterpret_cast<const uint4*>(q + d));
+                if (h < n_heads && in_bounds(p.bounds, kMemQ, q + d, 16))
+                    x = *(reinterpret_cast<const uint4*>(q + d));
                 qf[nt][w / 2][0] = x.x;
                 qf[nt][w / 2][1] = x.y;
                 qf[nt][w / 2 + 1][0] = x.z;
@@ -345,8 +353,10 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         int32_t page = -1, row = 0, listed = -1;
         auto list = [&](int32_t i) {
             listed = -1;
-            if (p.n_indices >= 0 && i + mine < step_end)
-                listed = *(p.indices + b * p.indices_stride + i + mine);
+            if (p.n_indices >= 0 && i + mine < step_end) {
+                const int32_t* const at = p.indices + b * p.indices_stride + i + mine;
+                if (in_bounds(p.bounds, kMemIndices, at, 4)) listed = *at;
+            }
         };
         auto find = [&](int32_t i) {  // i: the step's first place in the row's list
             const int32_t n = p.n_indices >= 0 ? listed : i + mine;
@@ -354,7 +364,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             if (i + mine < step_end && n >= 0 && n < len) {
                 const int32_t col = p.table.by_page.of(n);
                 row = n - col * p.k.page_size;
-                page = *(p.table.ids + b * p.table.stride + col);
+                const int32_t* const at = p.table.ids + b * p.table.stride + col;
+                if (in_bounds(p.bounds, kMemTable, at, 4)) page = *at;
             }
             list(i + tile);
         };
@@ -371,21 +382,22 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                 const uint32_t at = __shfl_sync(~0u, k_at, r);
                 const uint32_t at2 = p.same_rows ? at : __shfl_sync(~0u, v_at, r);
                 const bool ok = at != kNoRow;
-                copy16(to + 16 * k_place<S::kPieces>(r, c),
-                       k_base + uint64_t(ok ? at : 0) * p.k_units.unit + 16 * c, ok);
-                copy16(to + S::kRows + 16 * v_place<S::kPieces>(r, c),
-                       v_base + uint64_t(ok ? at2 : 0) * p.v_units.unit + 16 * c, ok);
+                auto k_from = [&] { return k_base + uint64_t(ok ? at : 0) * p.k_units.unit + 16 * c; };
+                auto v_from = [&] { return v_base + uint64_t(ok ? at2 : 0) * p.v_units.unit + 16 * c; };
+                copy16(to + 16 * k_place<S::kPieces>(r, c), k_from(),
+                       ok && in_bounds(p.bounds, kMemData, k_from(), 16));
+                copy16(to + S::kRows + 16 * v_place<S::kPieces>(r, c), v_from(),
+                       ok && in_bounds(p.bounds, kMemData2, v_from(), 16));
             }
             if (S::kE4m3 && warp % kHq == 0) {
                 const int64_t pg = there ? page : 0, rw = there ? row : 0;
-                copy4(to + S::kScales + 4 * lane,
-                      p.k.scale + pg * p.k.scale_page_stride + rw * p.k.scale_row_stride +
-                          kvh * p.k.scale_head_stride,
-                      there);
-                copy4(to + S::kScales + 4 * (S::kStep + lane),
-                      p.v.scale + pg * p.v.scale_page_stride + rw * p.v.scale_row_stride +
-                          kvh * p.v.scale_head_stride,
-                      there);
+                const float* const k_from = p.k.scale + pg * p.k.scale_page_stride +
+                                            rw * p.k.scale_row_stride + kvh * p.k.scale_head_stride;
+                const float* const v_from = p.v.scale + pg * p.v.scale_page_stride +
+                                            rw * p.v.scale_row_stride + kvh * p.v.scale_head_stride;
+                copy4(to + S::kScales + 4 * lane, k_from, there && in_bounds(p.bounds, kMemScale, k_from, 4));
+                copy4(to + S::kScales + 4 * (S::kStep + lane), v_from,
+                      there && in_bounds(p.bounds, kMemScale2, v_from, 4));
             }
             const uint32_t here = __ballot_sync(~0u, there);
             if (lane == 0 && warp % kHq == 0)
@@ -694,9 +706,10 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             if (whole) {
                 finish(i, hh, top, sum, v);
             } else {
-                reinterpret_cast<float4*>(part_o)[slot * (all_heads * (kDim / 4)) + i] = v;
-                if (i % (kDim / 4) == 0)
-                    reinterpret_cast<float2*>(part_ml)[slot * all_heads + hh] = make_float2(top, sum);
+                float4* const to = reinterpret_cast<float4*>(part_o) + slot * (all_heads * (kDim / 4)) + i;
+                float2* const to_ml = reinterpret_cast<float2*>(part_ml) + slot * all_heads + hh;
+                if (in_bounds(p.bounds, kMemPartial, to, 16)) *to = v;
+                if (i % (kDim / 4) == 0 && in_bounds(p.bounds, kMemPartial, to_ml, 8)) *to_ml = make_float2(top, sum);
             }
         }
 
@@ -707,7 +720,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             split.first = owner_of(row_start);
             split.parts = lo == 0 ? 0 : owner_of(row_start + n_tiles - 1) - split.first + 1;
             split.first_slot = begin_of(split.first) == row_start ? 0 : 1;
-            p.splits[me] = split;
+            if (in_bounds(p.bounds, kMemSplits, p.splits + me, sizeof(split))) p.splits[me] = split;
         }
         at = row_start += hi;
         __syncthreads();  // the results are read: the rings may be filled again
@@ -733,6 +746,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinWarps == 4 ? 6 : 3)
     const int chunk = blockIdx.y * 8 / all_heads, first_head = blockIdx.y * 8 % all_heads;
     const int me = blockIdx.x + 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!in_bounds(p.bounds, kMemSplits, p.splits + me, sizeof(AttnSplit))) return;
     const AttnSplit split = p.splits[me];
     if (split.parts == 0) return;
     const int n = split.parts, slices = n > 32 ? 4 : 1;
@@ -764,9 +778,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinWarps == 4 ? 6 : 3)
                     if (k < n) {
                         const int64_t slot = 2 * (int64_t(split.first + k) * chunks + chunk) +
                                              (k == 0 ? split.first_slot : 0);
-                        ml[i] = __ldcg(reinterpret_cast<const float2*>(part_ml) + slot * all_heads + hh);
-                        x[i] = __ldcg(reinterpret_cast<const float4*>(
-                                          p.partial + (slot * all_heads + hh) * kDim) + col);
+                        const float2* const from_ml = reinterpret_cast<const float2*>(part_ml) + slot * all_heads + hh;
+                        const float4* const from =
+                            reinterpret_cast<const float4*>(p.partial + (slot * all_heads + hh) * kDim) + col;
+                        if (!in_bounds(p.bounds, kMemPartial, from_ml, 8) || !in_bounds(p.bounds, kMemPartial, from, 16))
+                            continue;
+                        ml[i] = __ldcg(from_ml);
+                        x[i] = __ldcg(from);
                     }
                 }
                 float top = m;

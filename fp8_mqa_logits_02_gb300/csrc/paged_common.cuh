@@ -60,12 +60,56 @@ struct RowUnits {
 };
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
+// The bounds-checking build (FP8MQA_DEBUG_BOUNDS) holds every access of a paged kernel to global memory
+// against what the call's arguments span, and records the first one outside instead of making it.
+enum PagedMemory : int32_t {
+    kMemSlots = 1,
+    kMemRows,      // rows to be written, keys, then values; as the two below
+    kMemRows2,
+    kMemData,
+    kMemData2,
+    kMemScale,
+    kMemScale2,
+    kMemTable,
+    kMemLens,      // or the sequences' starts
+    kMemIndices,
+    kMemQ,
+    kMemW,
+    kMemOut,
+    kMemOutScale,  // or the log of the softmax's sum
+    kMemSplits,
+    kMemPartial,
+    kMemKinds
+};
+constexpr int32_t kPagedOutside = 2;  // status bit: an access that was not made
+
+struct PagedBounds {
+#ifdef FP8MQA_DEBUG_BOUNDS
+    int32_t* status;
+    uint64_t from[kMemKinds], bytes[kMemKinds];
+#endif
+};
+
+__device__ __forceinline__ bool in_bounds(const PagedBounds& b, int kind, const void* at, uint64_t n)
+{
+#ifdef FP8MQA_DEBUG_BOUNDS
+    const uint64_t off = reinterpret_cast<uint64_t>(at) - b.from[kind];
+    if (off <= b.bytes[kind] && n <= b.bytes[kind] - off) return true;
+    atomicOr(b.status, kPagedOutside);
+    atomicCAS(reinterpret_cast<unsigned long long*>(b.status + 2), 0ull,
+              static_cast<unsigned long long>(kind) << 48 | (off & 0xFFFFFFFFFFFFull));
+    return false;
+#else
+    return true;
+#endif
+}
+
 // The page and row of position n of sequence b; false if it is not there.
-__device__ __forceinline__ bool locate(const PagedView& c, const PageTable& t, int64_t b, int32_t n,
-                                       int32_t* page, int32_t* row)
+__device__ __forceinline__ bool locate(const PagedBounds& bounds, const PagedView& c, const PageTable& t,
+                                       int64_t b, int32_t n, int32_t* page, int32_t* row)
 {
     const int32_t col = t.by_page.of(n);
-    if (n < 0 || col >= t.cols) return false;
+    if (n < 0 || col >= t.cols || !in_bounds(bounds, kMemTable, t.ids + b * t.stride + col, 4)) return false;
     *page = *(t.ids + b * t.stride + col);
     *row = n - col * c.page_size;
     return uint32_t(*page) < uint32_t(c.pages);

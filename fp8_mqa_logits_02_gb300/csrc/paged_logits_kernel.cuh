@@ -51,6 +51,7 @@ struct PagedLogitsParams {
     uint32_t suspend_ns;     // of one suspension within a wait, at most
     int32_t box, box_shift;  // kTma: rows of a piece, 2^box_shift
     uint32_t page_rows;      // kTma: rows of the tensor map from page to page
+    PagedBounds bounds;
 };
 
 constexpr int kPagedHeads = 32, kPagedDim = 128;
@@ -166,8 +167,11 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
 
     // ---- the rows' costs, in units of about half a kilobyte moved
     const int32_t c_tile = 34 + n_tok, c_fill = 8 * n_tok;
+    auto full_length = [&](int64_t b) -> int64_t {
+        return in_bounds(p.bounds, kMemLens, p.lens + b, 4) ? p.lens[b] : 0;
+    };
     auto length = [&](int64_t b) {
-        const int64_t n = p.lens[b];
+        const int64_t n = full_length(b);
         return int32_t(n < 0 ? 0 : n < cap ? n : cap);
     };
     auto tiles = [&](int64_t b) { return (length(b) + kPagedTile - 1) / kPagedTile; };
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
             // kTma: a lane's piece, else its key
             const int32_t n = tile * kPagedTile + (kTma ? lane << p.box_shift : tid);
             if (!((!kTma || lane < kPagedTile >> p.box_shift) && n < len &&
-                  locate(p.keys, p.table, cur_b, n, &page, &page_row)))
+                  locate(p.bounds, p.keys, p.table, cur_b, n, &page, &page_row)))
                 page = -1;
         };
         int32_t reported = 0;
@@ -339,38 +343,54 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
                 const int64_t q0 = (cur_b * p.T + t0) * kPagedHeads;
                 for (int i = tid; !kTma && i < n_tok * kPagedHeads * 8; i += 32 * S::kCopyWarps)
                     copy16(base + S::kOffQ + slot * S::kQBytes + i / 8 * 128 + 16 * (i % 8 ^ (i / 8 & 7)),
-                           p.q + (q0 + i / 8) * kPagedDim + 16 * (i % 8), true);
+                           p.q + (q0 + i / 8) * kPagedDim + 16 * (i % 8),
+                           in_bounds(p.bounds, kMemQ, p.q + (q0 + i / 8) * kPagedDim + 16 * (i % 8), 16));
                 for (int i = tid; !kTma && i < n_tok * kPagedHeads / 4; i += 32 * S::kCopyWarps)
-                    copy16(base + S::kOffW + slot * S::kN * 4 + 16 * i, p.w + q0 + 4 * i, true);
+                    copy16(base + S::kOffW + slot * S::kN * 4 + 16 * i, p.w + q0 + 4 * i,
+                           in_bounds(p.bounds, kMemW, p.w + q0 + 4 * i, 16));
             }
             if constexpr (kTma) {
-                const bool have = page >= 0;
+                auto piece_row = [&] { return int32_t(uint32_t(page) * p.page_rows + page_row); };
+                auto piece_scales = [&] { return p.keys.scale + page * p.keys.scale_page_stride + page_row; };
+                const bool have =
+                    page >= 0 &&
+                    in_bounds(p.bounds, kMemData, p.keys.data + piece_row() * p.keys.row_stride,
+                              ((1 << p.box_shift) - 1) * p.keys.row_stride + kPagedDim) &&
+                    in_bounds(p.bounds, kMemScale, piece_scales(), 4u << p.box_shift);
+                auto first_query = [&] { return (cur_b * p.T + t0) * kPagedHeads; };
+                const bool fetch =
+                    first &&
+                    in_bounds(p.bounds, kMemQ, p.q + first_query() * kPagedDim, n_tok * kPagedHeads * kPagedDim) &&
+                    in_bounds(p.bounds, kMemW, p.w + first_query(), n_tok * kPagedHeads * 4);
                 const uint32_t pieces = __ballot_sync(~0u, have);
                 const int slot = row % S::kSlots;
                 const uint32_t full = bar(S::kFull + stage), seen = bar(S::kItem + j % S::kItems);
                 const uint32_t n_rows = uint32_t(__popc(pieces)) << p.box_shift;
                 if (lane == 0) {
                     item.there[0] = pieces;
-                    ptx::mbar_arrive_expect_tx(full, n_rows * kPagedDim + (first ? S::kQBytes : 0u));
-                    ptx::mbar_arrive_expect_tx(seen, n_rows * 4 + (first ? n_tok * kPagedHeads * 4 : 0u));
+                    ptx::mbar_arrive_expect_tx(full, n_rows * kPagedDim + (fetch ? S::kQBytes : 0u));
+                    ptx::mbar_arrive_expect_tx(seen, n_rows * 4 + (fetch ? n_tok * kPagedHeads * 4 : 0u));
                 }
                 __syncwarp();
                 if (have) {
                     ptx::tma_load_2d(base + stage * S::kKBytes + (lane << p.box_shift) * kPagedDim, &map_k,
-                                     full, 0, int32_t(uint32_t(page) * p.page_rows + page_row));
-                    ptx::bulk_load(ptx::smem_addr(&item.scale[lane << p.box_shift]),
-                                   p.keys.scale + page * p.keys.scale_page_stride + page_row,
+                                     full, 0, piece_row());
+                    ptx::bulk_load(ptx::smem_addr(&item.scale[lane << p.box_shift]), piece_scales(),
                                    4u << p.box_shift, seen);
                 }
-                if (first && lane == 31) {
-                    const int64_t q0 = (cur_b * p.T + t0) * kPagedHeads;
+                if (fetch && lane == 31) {
+                    const int64_t q0 = first_query();
                     ptx::tma_load_2d(base + S::kOffQ + slot * S::kQBytes, &map_q, full, 0, int32_t(q0));
                     ptx::bulk_load(base + S::kOffW + slot * S::kN * 4, p.w + q0, n_tok * kPagedHeads * 4, seen);
                 }
                 next();
                 continue;
             }
-            const bool there = page >= 0;
+            const float* const at_scale =
+                p.keys.scale + (page >= 0 ? int64_t(page) * p.keys.scale_page_stride +
+                                                int64_t(page_row) * p.keys.scale_row_stride
+                                          : 0);
+            const bool there = page >= 0 && in_bounds(p.bounds, kMemScale, at_scale, 4);
             const uint32_t place = there ? page * p.units.page + page_row * p.units.row : kNoRow;
             const uint32_t dst = base + stage * S::kKBytes + warp * 32 * 128;
             const int c = lane % 8;
@@ -378,15 +398,11 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
             for (int i = 0; i < 8; ++i) {
                 const int r = i * 4 + lane / 8;
                 const uint32_t src = __shfl_sync(~0u, place, r);
-                const bool have = src != kNoRow;
-                copy16(dst + r * 128 + 16 * (c ^ (r & 7)),
-                       p.keys.data + uint64_t(have ? src : 0) * p.units.unit + 16 * c, have);
+                const uint8_t* const at = p.keys.data + uint64_t(src != kNoRow ? src : 0) * p.units.unit + 16 * c;
+                const bool have = src != kNoRow && in_bounds(p.bounds, kMemData, at, 16);
+                copy16(dst + r * 128 + 16 * (c ^ (r & 7)), at, have);
             }
-            copy4(ptx::smem_addr(&item.scale[tid]),
-                  p.keys.scale + (there ? int64_t(page) * p.keys.scale_page_stride +
-                                              int64_t(page_row) * p.keys.scale_row_stride
-                                        : 0),
-                  there);
+            copy4(ptx::smem_addr(&item.scale[tid]), at_scale, there);
             const uint32_t here = __ballot_sync(~0u, there);
             if (lane == 0) item.there[warp] = here;
             copy_commit();
@@ -429,7 +445,7 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
             const float scale = item.scale[quarter * 32 + lane];
             const bool there = kTma ? item.there[0] >> ((quarter * 32 + lane) >> p.box_shift) & 1u
                                     : item.there[quarter] >> lane & 1u;
-            const int64_t len_full = p.lens[b];
+            const int64_t len_full = full_length(b);
             const float* const w =
                 reinterpret_cast<const float*>(smem + S::kOffW) + row % S::kSlots * S::kN;
             float* out = p.out + (b * p.T + t0) * p.ld + n;
@@ -453,7 +469,7 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
                               make_float2(wh.z, wh.w), y1);
                 }
                 const bool seen = n < len && n < len_full - (p.T - 1 - (t0 + t));
-                if (n < p.N && (seen || p.clean))
+                if (n < p.N && (seen || p.clean) && in_bounds(p.bounds, kMemOut, out, 4))
                     __stcs(out, seen && there ? ((y0.x + y0.y) + (y1.x + y1.y)) * scale
                                               : -CUDART_INF_F);
             }
@@ -502,12 +518,15 @@ __global__ void __launch_bounds__(PagedShape<kTok, kTma>::kThreads, PagedShape<k
                 // 16-byte stores between the first and the last 16-byte boundary
                 const int64_t a0 = min(c1, c0 + int64_t((16u - uint32_t(reinterpret_cast<uintptr_t>(out + c0) & 15u)) % 16u / 4u));
                 const int64_t a1 = a0 + (c1 - a0) / 4 * 4;
-                if (c0 + lane < a0) __stcs(out + c0 + lane, -CUDART_INF_F);
+                if (c0 + lane < a0 && in_bounds(p.bounds, kMemOut, out + c0 + lane, 4))
+                    __stcs(out + c0 + lane, -CUDART_INF_F);
 #pragma unroll 4
                 for (int64_t c = a0 + 4 * lane; c < a1; c += 128)
-                    __stcs(reinterpret_cast<float4*>(out + c),
-                           make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F));
-                if (a1 + lane < c1) __stcs(out + a1 + lane, -CUDART_INF_F);
+                    if (in_bounds(p.bounds, kMemOut, out + c, 16))
+                        __stcs(reinterpret_cast<float4*>(out + c),
+                               make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F));
+                if (a1 + lane < c1 && in_bounds(p.bounds, kMemOut, out + a1 + lane, 4))
+                    __stcs(out + a1 + lane, -CUDART_INF_F);
             }
         }
     }

@@ -19,9 +19,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, "fp8_mqa_logits.cu"), os.path.join(CSRC, "paged.cu")]
 LIB = os.path.join(HERE, "libfp8mqa.so")
-# The same library built with FP8MQA_DEBUG_BOUNDS: every global access and TMA coordinate
-# of the kernel is checked first, and a violation is recorded in the status word
-# (fp8_mqa_logits_check_error then returns FP8MQA_ERR_BOUNDS) instead of being made.
+# The same library built with FP8MQA_DEBUG_BOUNDS: every global access and TMA coordinate of the
+# prefill logits' kernel and of the paged operators' kernels is checked first, and a violation is
+# recorded in the status word (fp8_mqa_logits_check_error then returns FP8MQA_ERR_BOUNDS) instead
+# of being made.  (The top-k kernels are the same in both.)
 DEBUG_LIB = os.path.join(HERE, "libfp8mqa_debug.so")
 BINDING_SOURCE = os.path.join(CSRC, "paged_binding.cpp")
 BINDING = os.path.join(HERE, "_paged_binding.so")
