@@ -38,8 +38,8 @@
 //
 // Measured: 64 rows of up to 20001 positions, 64 query and 8 key heads (1.37 GB) 223 us, 6.2 TB/s of 6.7;
 // 16 rows of a 16-bit cache (285 MB) 54 us; 2048 selected of 32768 positions for 64 rows (140 MB in rows
-// of 128 bytes anywhere) 43 us; one row of 131072 positions, 32 query heads of one key head, 23 us, where
-// the steps' latency and the join decide.
+// of 128 bytes anywhere) 43 us; one row of 131072 positions, 32 query heads of one key head, 23.4 us with
+// the rows in L2, 24.7 us from HBM, where the steps' latency and the join decide.
 //
 // Split and join: for each chunk of heads the rows' tiles (the CTA's steps) are laid end to end,
 // and its CTAs take equal shares of them; the CTAs of one share number follow one another in the

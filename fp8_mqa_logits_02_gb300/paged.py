@@ -132,6 +132,8 @@ def attention_paged(q: torch.Tensor, k_data: torch.Tensor, v_data: torch.Tensor,
     to instead of all, in any order, as ``topk`` returns them; entries outside [0, lens[b]) are
     ignored.  Returns out [B, q_heads, dim] in q's type, and with ``return_lse`` the float32
     [B, q_heads] log of the softmax's sum.  A row with nothing to attend to gives 0 and -inf.
+    The work is laid out for rows as long as the table is wide: with a table that was made for much
+    longer rows, pass ``table[:, :columns]``.
     """
     call = _binding().attention_paged
     if stream is not None:

@@ -388,7 +388,9 @@ FP8MQA_API int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_
  *             multiple of the cache's heads.
  *   k, v      caches of one type, page_size, heads and dim, over one page table: E4M3, or q's type.
  *   lens      DEVICE int32 [B]; clamped to [0, table_cols * page_size].
- *             table_cols * page_size, or n_indices, is 2^31 - 1025 at most.
+ *             table_cols * page_size, or n_indices, is 2^31 - 1025 at most.  The work is laid out
+ *             for rows as long as the table is wide: where all are known to be much shorter, a
+ *             smaller table_cols (the table_stride stays) is faster, by up to a fifth.
  *   n_indices -1: each row attends to all of its positions.  Otherwise `indices` is DEVICE int32
  *   indices   with n_indices entries a row, row b at indices + b*indices_stride: the positions that
  *             row b attends to, for all its heads, in any order; entries outside [0, lens[b]) are
