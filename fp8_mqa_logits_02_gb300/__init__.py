@@ -66,6 +66,10 @@ SIGNATURES = {
     "fp8_mqa_attention_paged": (ctypes.c_int, [_P, _I32, _I64, _I32, _I64, _I64, _P, _P, _P, _I64,
                                                _I32, _P, _P, _I64, _I32, ctypes.c_float, _P, _P,
                                                _P, _U64, _P]),
+    "fp8_mqa_pages_update": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P,
+                                            _P, _P, _P, _P]),
+    "fp8_mqa_norm_rotate": (ctypes.c_int, [_P, _P, _I32, _I32, _I64, _I32, _P, _I32, _P, _I32, _I32,
+                                           ctypes.c_float, _P]),
 }
 
 TOPK_MAX_K = 2048
@@ -311,4 +315,5 @@ def fp8_mqa_logits_host(q, k, kv_scale, w, ks, ke, out, workspace: torch.Tensor,
 
 
 # The paged-cache operators are part of the same namespace.
-from .paged import attention_paged, cache_read, cache_write, logits_paged  # noqa: E402,F401
+from .paged import (PagesStep, attention_paged, cache_read, cache_write, logits_paged,  # noqa: E402,F401
+                    norm_rotate, pages_update)

@@ -104,6 +104,81 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid
     }
 }
 
+// The same for E2M1 caches: a lane has a group of 16 values side by side, so that its scale and values need
+// nothing of other lanes but the row's maximum.  With a the row's maximum and m the group's:
+//     G = e4m3(448 m / a);  data = e2m1(2688 x / (G a));  scale = a / 2688
+// What the values and m are divided by is exact, and the quotients are rounded as a division is, so that
+// ties of 16-bit inputs fall as in real arithmetic: rows are first scaled by a power of two that brings a to
+// [1, 2), and then, with y the correctly rounded reciprocal of b, q = y n is off by r = n - q b, which a fused
+// multiply-add gives exactly, and q + y r is the quotient rounded (P. Markstein, IBM J. Res. Dev. 34, 1990).
+// 16384 tokens x 8 heads of bfloat16 keys and values: see the host side.
+template <class X, int kDim, bool kVec, int kTensors>
+__global__ void __launch_bounds__(kCacheThreads) cache_write4_kernel(const __grid_constant__ CacheWriteParams p)
+{
+    constexpr int kLanes = kDim / kGroup, kPer = 16 / sizeof(X);
+    const uint32_t at = blockIdx.x * (kCacheThreads / kLanes) + threadIdx.x / kLanes;  // token and head
+    const int c = threadIdx.x % kLanes;
+    const bool row = at < uint32_t(p.T * p.heads);
+    const int32_t t = row ? p.by_heads.of(int32_t(at)) : 0, h = row ? int32_t(at) - t * p.heads : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t slot = row && in_bounds(p.bounds, kMemSlots, p.slots + t, 4) ? p.slots[t] : -1;
+    float v[kTensors][kGroup];
+#pragma unroll
+    for (int i = 0; i < kTensors; ++i) {
+        const X* const x = static_cast<const X*>(p.x[i]) + t * p.row_stride[i] + h * p.head_stride[i] + c * kGroup;
+#pragma unroll
+        for (int j = 0; j < kGroup; j += kPer) {
+            alignas(16) X raw[kPer];
+            if (!in_bounds(p.bounds, kMemRows + i, x + j, 16)) {
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) raw[k] = from_float<X>(0.0f);
+            } else if constexpr (kVec) {
+                *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(x + j);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) raw[k] = x[j + k];
+            }
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) v[i][j + k] = to_float(raw[k]);
+        }
+    }
+    const int32_t page = p.by_page.of(max(slot, 0)), r = slot - page * p.cache[0].page_size;
+#pragma unroll
+    for (int i = 0; i < kTensors; ++i) {
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) m = max_nan(m, fabsf(v[i][j]));
+        float a = max_nan(m, kTinyMax);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o /= 2) a = max_nan(a, __shfl_xor_sync(~0u, a, o));
+        const PagedView& cache = p.cache[i];
+        if (slot < 0 || page >= cache.pages) continue;
+        // 2^-e of a in [2^e, 2^(e + 1)); the largest ones, and what is not finite, take 2^-126
+        const float down = __uint_as_float((254u - min(__float_as_uint(a) >> 23, 253u)) << 23);
+        const float top = a * down;
+        const uint32_t g = __nv_cvt_float_to_fp8(__fdiv_rn(__fmul_rn(m * down, kE4m3Max), top), __NV_SATFINITE, __NV_E4M3);
+        const float b = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_fp8_storage_t(g), __NV_E4M3))) * top;
+        const float y = b > 0.0f ? __frcp_rn(b) : 0.0f;
+        const float by = down * kE2m1Top;
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+            const float n = v[i][j] * by, q = n * y;
+            v[i][j] = fmaf(fmaf(-q, b, n), y, q);
+        }
+        uint8_t* const to = cache.data + page * cache.page_stride + r * cache.row_stride + h * cache.head_stride + c * 8;
+        if (in_bounds(p.bounds, kMemData + i, to, 8))
+            *reinterpret_cast<uint2*>(to) = make_uint2(e2m1_of(v[i]), e2m1_of(v[i] + 8));
+        uint8_t* const to_group = cache.groups + page * cache.group_page_stride + r * cache.group_row_stride +
+                                  h * cache.group_head_stride + c;
+        if (in_bounds(p.bounds, kMemGroups + i, to_group, 1)) *to_group = uint8_t(g);
+        float* const to_scale = cache.scale + page * cache.scale_page_stride + r * cache.scale_row_stride +
+                                h * cache.scale_head_stride;
+        // (an infinity would leave infinities where it is not among the values that round to 0)
+        if (c == 0 && in_bounds(p.bounds, kMemScale + i, to_scale, 4))
+            *to_scale = a <= 3.402823466e38f ? __fmul_rn(a, 1.0f / kE2m1Top) : __uint_as_float(0x7FC00000u);
+    }
+}
+
 struct CacheReadParams {
     PagedView cache;
     PageTable table;
@@ -214,6 +289,77 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
                 }
                 out[i] = *reinterpret_cast<const uint4*>(y);
             }
+        }
+    }
+}
+
+// The same from an E2M1 cache: a piece is a group, 16 values.
+template <class Out, int kDim>
+__global__ void __launch_bounds__(kCacheThreads) cache_read4_kernel(const __grid_constant__ CacheReadParams p)
+{
+    __shared__ int64_t s_data[kReadRows], s_scale[kReadRows], s_group[kReadRows];  // offsets; s_data -1: not there
+    const PagedView& c = p.cache;
+    const int64_t r0 = int64_t(blockIdx.x) * p.block_rows;
+    const int rows = int(min(int64_t(p.block_rows), p.total - r0));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x < rows) {
+        auto starts = [&](int64_t b) { return in_bounds(p.bounds, kMemLens, p.starts + b, 4) ? p.starts[b] : 0; };
+        const int64_t r = r0 + threadIdx.x, b = sequence_of(starts, p.B, r);
+        int32_t page = 0, row = 0;
+        const bool there =
+            b >= 0 && b < p.B && locate(p.bounds, c, p.table, b, int32_t(r - starts(b)), &page, &row);
+        s_data[threadIdx.x] = there ? page * c.page_stride + row * c.row_stride : -1;
+        s_scale[threadIdx.x] = page * c.scale_page_stride + row * c.scale_row_stride;
+        s_group[threadIdx.x] = page * c.group_page_stride + row * c.group_row_stride;
+    }
+    __syncthreads();
+    constexpr int kLanes = kDim / kGroup;
+    const int n = rows * c.heads * kLanes;
+    Out* const out = static_cast<Out*>(p.out) + r0 * c.heads * kDim;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kReadPieces * kCacheThreads) {
+        uint2 x[kReadPieces];
+        float by[kReadPieces];
+        uint32_t g[kReadPieces];
+#pragma unroll
+        for (int j = 0; j < kReadPieces; ++j) {
+            const int i = i0 + j * kCacheThreads, at = i / kLanes;
+            x[j] = make_uint2(0u, 0u);
+            by[j] = 0.0f;
+            g[j] = 0u;
+            if (i < n) {
+                const int row = p.by_heads.of(at), h = at - row * c.heads;
+                const int64_t off = s_data[row];
+                const uint8_t* const src = c.data + off + h * c.head_stride + i % kLanes * 8;
+                const uint8_t* const src_group = c.groups + s_group[row] + h * c.group_head_stride + i % kLanes;
+                const float* const src_scale = c.scale + s_scale[row] + h * c.scale_head_stride;
+                if (off >= 0 && in_bounds(p.bounds, kMemData, src, 8) && in_bounds(p.bounds, kMemScale, src_scale, 4) &&
+                    in_bounds(p.bounds, kMemGroups, src_group, 1)) {
+                    x[j] = __ldcs(reinterpret_cast<const uint2*>(src));
+                    g[j] = *src_group;
+                    by[j] = *src_scale;
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kReadPieces; ++j) {
+            const int i = i0 + j * kCacheThreads;
+            if (i >= n) break;
+            const uint32_t group = f16x2_of_e4m3x2(g[j] * 0x101u);
+            uint32_t h[8];
+            f16_of_e2m1(x[j].x, *reinterpret_cast<uint32_t(*)[4]>(h));
+            f16_of_e2m1(x[j].y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+            alignas(16) Out y[kGroup];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t two = mul_f16x2(h[k], group);  // exact
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+                y[2 * k] = from_float<Out>(__fmul_rn(f.x, by[j]));
+                y[2 * k + 1] = from_float<Out>(__fmul_rn(f.y, by[j]));
+            }
+            uint4* const to = reinterpret_cast<uint4*>(out + int64_t(i) * kGroup);
+#pragma unroll
+            for (int k = 0; k < int(kGroup * sizeof(Out) / 16); ++k)
+                if (in_bounds(p.bounds, kMemOut, to + k, 16)) to[k] = reinterpret_cast<const uint4*>(y)[k];
         }
     }
 }

@@ -13,6 +13,7 @@
 #include "cache_kernels.cuh"
 #include "paged_attention_kernel.cuh"
 #include "paged_host.h"
+#include "paged_launch.cuh"
 #include "paged_logits_kernel.cuh"
 
 namespace fp8mqa {
@@ -20,14 +21,8 @@ namespace {
 
 constexpr int kPagedMaxDevices = 64;
 
-struct PagedDevice {
-    std::mutex setting_up;
-    int sm_count = 0;
-    int32_t* status = nullptr;  // status word of the paged logits
-    std::atomic<bool> ready{false};
-};
-
 PagedDevice g_paged[kPagedMaxDevices];
+
 template <int kTok>
 bool logits_smem()
 {
@@ -52,33 +47,24 @@ bool attention_smem()
                                 AttnShape<kType, kDim, kNT, kHq>::kSmem) == cudaSuccess;
 }
 
+// Whether groups of more than 32 query heads have four warps to share a ring, or two: a step of E2M1 rows of
+// 64 values has copies for two.
+template <int kType, int kDim>
+constexpr bool kFourShare = kType != FP8MQA_E2M1 || kDim != 64;
+
+template <int kType, int kDim>
+bool attention_smem()
+{
+    if constexpr (kFourShare<kType, kDim>)
+        if (!attention_smem<kType, kDim, 2, 4>()) return false;
+    return attention_smem<kType, kDim, 1, 1>() && attention_smem<kType, kDim, 2, 1>() &&
+           attention_smem<kType, kDim, 2, 2>();
+}
+
 template <int kType>
 bool attention_smem()
 {
-    return attention_smem<kType, 64, 1, 1>() && attention_smem<kType, 64, 2, 1>() &&
-           attention_smem<kType, 64, 2, 2>() && attention_smem<kType, 64, 2, 4>() &&
-           attention_smem<kType, 128, 1, 1>() && attention_smem<kType, 128, 2, 1>() &&
-           attention_smem<kType, 128, 2, 2>() && attention_smem<kType, 128, 2, 4>();
-}
-
-// Launches a kernel that begins with griddepcontrol.wait: it is set up while the one before it ends.
-// Its own result says whether it is under way (the runtime's last error may be an older one of the
-// caller's).
-template <class... Params, class... Args>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                  const Args&... args)
-{
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(unsigned(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    return attention_smem<kType, 64>() && attention_smem<kType, 128>();
 }
 
 int init_paged(int dev, PagedDevice& st)
@@ -92,7 +78,7 @@ int init_paged(int dev, PagedDevice& st)
     }
     if (major != 10 || minor != 3) return FP8MQA_ERR_ARCH;
     if (!attention_smem<FP8MQA_E4M3>() || !attention_smem<FP8MQA_BF16>() ||
-        !attention_smem<FP8MQA_F16>() ||
+        !attention_smem<FP8MQA_F16>() || !attention_smem<FP8MQA_E2M1>() ||
         !logits_smem<1>() || !logits_smem<2>() || !logits_smem<4>()) {
         cudaGetLastError();
         return FP8MQA_ERR_LAUNCH;
@@ -107,8 +93,8 @@ int init_paged(int dev, PagedDevice& st)
     return FP8MQA_OK;
 }
 
-// The current device's state, set up by the first call that succeeds in it: what fails once (no memory
-// left, a stream being captured) is tried again by the next call.
+}  // namespace
+
 PagedDevice* paged_device(int* err)
 {
     int dev = -1;
@@ -129,26 +115,38 @@ PagedDevice* paged_device(int* err)
     return &st;
 }
 
-bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+#ifdef FP8MQA_DEBUG_BOUNDS
+std::atomic<uint64_t> g_short[kMemKinds];
+#endif
 
-int64_t size_of(int32_t type) { return type == FP8MQA_E4M3 ? 1 : type == FP8MQA_F32 ? 4 : 2; }
+namespace {
+
+// Whether a cache of the type has a scale for each row.
+bool scaled(int32_t type) { return type == FP8MQA_E4M3 || type == FP8MQA_E2M1; }
+
+// Bytes of a row of data.
+int64_t row_bytes(const fp8mqa_cache& c) { return c.type == FP8MQA_E2M1 ? c.dim / 2 : c.dim * size_of(c.type); }
 
 // A cache argument: sizes, type, pointers, alignment.
 int check_cache(const fp8mqa_cache* c)
 {
     if (!c || c->pages < 0 || c->page_size < 1 || c->heads < 1) return FP8MQA_ERR_INVALID_ARG;
-    if (c->type != FP8MQA_E4M3 && c->type != FP8MQA_BF16 && c->type != FP8MQA_F16)
+    if (c->type != FP8MQA_E4M3 && c->type != FP8MQA_BF16 && c->type != FP8MQA_F16 && c->type != FP8MQA_E2M1)
         return FP8MQA_ERR_INVALID_ARG;
     if ((c->dim != 64 && c->dim != 128) || c->pages > INT32_MAX / int64_t(c->page_size))
         return FP8MQA_ERR_UNSUPPORTED_SHAPE;
-    if (c->pages > 0 && (!c->data || (c->type == FP8MQA_E4M3 && !c->scale)))
+    const bool four = c->type == FP8MQA_E2M1;  // (the groups' members are not there with other types)
+    if (c->pages > 0 && (!c->data || (scaled(c->type) && !c->scale) || (four && !c->groups)))
         return FP8MQA_ERR_INVALID_ARG;
-    if ((c->type == FP8MQA_E4M3) != (c->scale != nullptr) && c->pages > 0)
-        return FP8MQA_ERR_INVALID_ARG;
+    if (scaled(c->type) != (c->scale != nullptr) && c->pages > 0) return FP8MQA_ERR_INVALID_ARG;
     // the stride of a dimension of one is never used
     const int64_t e = size_of(c->type);
     if (!on(c->data, 16) || !on(c->scale, 4) || (c->pages > 1 && c->page_stride * e % 16) ||
         (c->page_size > 1 && c->row_stride * e % 16) || (c->heads > 1 && c->head_stride * e % 16))
+        return FP8MQA_ERR_MISALIGNED;
+    const int64_t g = c->dim / kGroup;
+    if (four && (!on(c->groups, uintptr_t(g)) || (c->pages > 1 && c->group_page_stride % g) ||
+                 (c->page_size > 1 && c->group_row_stride % g) || (c->heads > 1 && c->group_head_stride % g)))
         return FP8MQA_ERR_MISALIGNED;
     return FP8MQA_OK;
 }
@@ -168,6 +166,11 @@ PagedView view_of(const fp8mqa_cache& c, const void* valid)
     v.scale_page_stride = c.scale_page_stride;
     v.scale_row_stride = c.scale_row_stride;
     v.scale_head_stride = c.scale_head_stride;
+    const bool four = c.type == FP8MQA_E2M1;
+    v.groups = !four ? nullptr : c.pages > 0 ? c.groups : static_cast<uint8_t*>(none);
+    v.group_page_stride = four ? c.group_page_stride : 0;
+    v.group_row_stride = four ? c.group_row_stride : 0;
+    v.group_head_stride = four ? c.group_head_stride : 0;
     v.pages = int32_t(c.pages);
     v.page_size = c.page_size;
     v.heads = c.heads;
@@ -189,35 +192,14 @@ bool row_units(const PagedView& v, RowUnits* u)
     return true;
 }
 
-// What the bounds-checking build holds a launch's accesses against, from the call's arguments alone; in the
-// library nothing of it is there.
-#ifdef FP8MQA_DEBUG_BOUNDS
-std::atomic<uint64_t> g_short[kMemKinds];  // bytes that a kind's memory is taken to be short of (tests)
-#endif
-void spans(PagedBounds& b, int kind, const void* from, int64_t bytes)
-{
-#ifdef FP8MQA_DEBUG_BOUNDS
-    b.from[kind] = reinterpret_cast<uint64_t>(from);
-    b.bytes[kind] = bytes > 0 ? uint64_t(bytes) - std::min(uint64_t(bytes), g_short[kind].load()) : 0;
-#endif
-}
-PagedBounds bounds_for(const PagedDevice& st)
-{
-    PagedBounds b = {};
-#ifdef FP8MQA_DEBUG_BOUNDS
-    b.status = st.status;
-#endif
-    return b;
-}
-// Bytes from the first to past the last of n0 x n1 x n2 places, `size` bytes each, at strides in bytes.
-int64_t extent(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t size)
-{
-    return n0 > 0 && n1 > 0 && n2 > 0 ? (n0 - 1) * s0 + (n1 - 1) * s1 + (n2 - 1) * s2 + size : 0;
-}
-void spans(PagedBounds& b, int which, const PagedView& c, int64_t row_bytes)
+void spans(PagedBounds& b, int which, const PagedView& c, const fp8mqa_cache& arg)
 {
     spans(b, kMemData + which, c.data,
-          extent(c.pages, c.page_stride, c.page_size, c.row_stride, c.heads, c.head_stride, row_bytes));
+          extent(c.pages, c.page_stride, c.page_size, c.row_stride, c.heads, c.head_stride, row_bytes(arg)));
+    if (c.groups)
+        spans(b, kMemGroups + which, c.groups,
+              extent(c.pages, c.group_page_stride, c.page_size, c.group_row_stride, c.heads, c.group_head_stride,
+                     arg.dim / kGroup));
     if (c.scale)
         spans(b, kMemScale + which, c.scale,
               extent(c.pages, 4 * c.scale_page_stride, c.page_size, 4 * c.scale_row_stride, c.heads,
@@ -228,18 +210,9 @@ void spans(PagedBounds& b, const PageTable& t, int64_t B)
     spans(b, kMemTable, t.ids, extent(B, 4 * t.stride, t.cols, 4, 1, 0, 4));
 }
 
-// What an entry point returns for its launches' result; a refusal is not left behind for the caller's
-// next look at the last error.
-int launched(cudaError_t e)
-{
-    if (e == cudaSuccess) return FP8MQA_OK;
-    cudaGetLastError();
-    return FP8MQA_ERR_LAUNCH;
-}
-
 // Rows of x that start on 16 bytes are read 16 bytes at a time, others value by value.
 template <class X, int kDim, int kTensors>
-cudaError_t write_tensors(const CacheWriteParams& p, cudaStream_t s)
+cudaError_t write_tensors(const CacheWriteParams& p, bool four, cudaStream_t s)
 {
     const int64_t rows = p.T * p.heads, per = kCacheThreads / (kDim / 16);
     const unsigned blocks = unsigned((rows + per - 1) / per);
@@ -247,15 +220,19 @@ cudaError_t write_tensors(const CacheWriteParams& p, cudaStream_t s)
     for (int i = 0; i < kTensors; ++i)
         vec = vec && on(p.x[i], 16) && p.row_stride[i] * int64_t(sizeof(X)) % 16 == 0 &&
               p.head_stride[i] * int64_t(sizeof(X)) % 16 == 0;
+    if (four)
+        return vec
+                   ? launch_after(cache_write4_kernel<X, kDim, true, kTensors>, dim3(blocks), kCacheThreads, 0, s, p)
+                   : launch_after(cache_write4_kernel<X, kDim, false, kTensors>, dim3(blocks), kCacheThreads, 0, s, p);
     return vec ? launch_after(cache_write_kernel<X, kDim, true, kTensors>, dim3(blocks), kCacheThreads, 0, s, p)
                : launch_after(cache_write_kernel<X, kDim, false, kTensors>, dim3(blocks), kCacheThreads, 0, s, p);
 }
 
 template <class X>
-cudaError_t write_rows(const CacheWriteParams& p, int32_t dim, int tensors, cudaStream_t s)
+cudaError_t write_rows(const CacheWriteParams& p, int32_t dim, int tensors, bool four, cudaStream_t s)
 {
-    if (dim == 64) return tensors == 1 ? write_tensors<X, 64, 1>(p, s) : write_tensors<X, 64, 2>(p, s);
-    return tensors == 1 ? write_tensors<X, 128, 1>(p, s) : write_tensors<X, 128, 2>(p, s);
+    if (dim == 64) return tensors == 1 ? write_tensors<X, 64, 1>(p, four, s) : write_tensors<X, 64, 2>(p, four, s);
+    return tensors == 1 ? write_tensors<X, 128, 1>(p, four, s) : write_tensors<X, 128, 2>(p, four, s);
 }
 
 // A block packs about kReadTurns x kReadPieces pieces a thread (finding the rows costs a block its
@@ -263,13 +240,18 @@ cudaError_t write_rows(const CacheWriteParams& p, int32_t dim, int tensors, cuda
 // than leaves two blocks an SM.
 constexpr int64_t kReadTurns = 4;
 template <class Out>
-cudaError_t read_rows(CacheReadParams& p, int32_t dim, int sm_count, cudaStream_t s)
+cudaError_t read_rows(CacheReadParams& p, int32_t dim, bool four, int sm_count, cudaStream_t s)
 {
-    const int64_t row_pieces = int64_t(p.cache.heads) * dim * int64_t(sizeof(Out)) / 16;
+    const int64_t row_pieces = four ? int64_t(p.cache.heads) * dim / kGroup
+                                    : int64_t(p.cache.heads) * dim * int64_t(sizeof(Out)) / 16;
     const int64_t rows = std::min(kReadTurns * kReadPieces * kCacheThreads / row_pieces,
                                   p.total / (2 * sm_count));
     p.block_rows = int32_t(std::max<int64_t>(1, std::min<int64_t>(kReadRows, rows)));
     const unsigned blocks = unsigned((p.total + p.block_rows - 1) / p.block_rows);
+    if constexpr (sizeof(Out) > 1)
+        if (four)
+            return dim == 64 ? launch_after(cache_read4_kernel<Out, 64>, dim3(blocks), kCacheThreads, 0, s, p)
+                             : launch_after(cache_read4_kernel<Out, 128>, dim3(blocks), kCacheThreads, 0, s, p);
     return dim == 64 ? launch_after(cache_read_kernel<Out, 64>, dim3(blocks), kCacheThreads, 0, s, p)
                      : launch_after(cache_read_kernel<Out, 128>, dim3(blocks), kCacheThreads, 0, s, p);
 }
@@ -335,8 +317,9 @@ cudaError_t attention_heads(PagedAttentionParams& p, int sm_count, cudaStream_t 
                           (attention_wave(sm_count) * kAttnWarps);
     if (group <= 8) return attention_launch<kType, kDim, 1, 1>(p, sm_count, s);
     if (group <= 16 || steps < (group <= 32 ? 32 : 8)) return attention_launch<kType, kDim, 2, 1>(p, sm_count, s);
-    if (group <= 32) return attention_launch<kType, kDim, 2, 2>(p, sm_count, s);
-    return attention_launch<kType, kDim, 2, 4>(p, sm_count, s);
+    if constexpr (kFourShare<kType, kDim>)
+        if (group > 32) return attention_launch<kType, kDim, 2, 4>(p, sm_count, s);
+    return attention_launch<kType, kDim, 2, 2>(p, sm_count, s);
 }
 
 template <int kType>
@@ -395,7 +378,8 @@ bool paged_take_status(int dev, int32_t* flags)
         std::fprintf(stderr,
                      "fp8mqa: bounds violation recorded: paged kind %u, byte offset %lld "
                      "(kinds: 1 slots, 2-3 rows, 4-5 data, 6-7 scale, 8 table, 9 lens or starts, 10 indices, "
-                     "11 q, 12 w, 13 out, 14 out scale or lse, 15-16 workspace)\n",
+                     "11 q, 12 w, 13 out, 14 out scale or lse, 15-16 workspace, 17-18 groups, 19 positions, 20 frequencies, "
+                     "21-22 norm weights, 23 second out, 24 its scale, 25-26 free pages and their count, 27 starts)\n",
                      unsigned(word[1] >> 48), static_cast<long long>(word[1] << 16) >> 16);
     if ((word[0] != 0 || word[1] != 0) && cudaMemset(st.status, 0, sizeof(word)) != cudaSuccess) return false;
     *flags |= int32_t(word[0]);
@@ -427,8 +411,8 @@ int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const v
     int rc = check_cache(cache);
     if (rc == FP8MQA_OK && cache2) rc = check_cache(cache2);
     if (rc != FP8MQA_OK) return rc;
-    if (cache->type != FP8MQA_E4M3 ||
-        (cache2 && (cache2->type != FP8MQA_E4M3 || cache2->page_size != cache->page_size ||
+    if (!scaled(cache->type) ||
+        (cache2 && (cache2->type != cache->type || cache2->page_size != cache->page_size ||
                     cache2->heads != cache->heads || cache2->dim != cache->dim)))
         return FP8MQA_ERR_INVALID_ARG;
     if (T * cache->heads >= int64_t(1) << 31) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
@@ -458,13 +442,14 @@ int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const v
     for (int i = 0; i < (x2 ? 2 : 1); ++i) {
         spans(p.bounds, kMemRows + i, p.x[i],
               extent(T, p.row_stride[i] * int64_t(e), p.heads, p.head_stride[i] * int64_t(e), 1, 0, cache->dim * int64_t(e)));
-        spans(p.bounds, i, p.cache[i], cache->dim);
+        spans(p.bounds, i, p.cache[i], i ? *cache2 : *cache);
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int tensors = x2 ? 2 : 1;
-    return launched(x_type == FP8MQA_BF16  ? write_rows<__nv_bfloat16>(p, cache->dim, tensors, s)
-                    : x_type == FP8MQA_F16 ? write_rows<__half>(p, cache->dim, tensors, s)
-                                           : write_rows<float>(p, cache->dim, tensors, s));
+    const bool four = cache->type == FP8MQA_E2M1;
+    return launched(x_type == FP8MQA_BF16  ? write_rows<__nv_bfloat16>(p, cache->dim, tensors, four, s)
+                    : x_type == FP8MQA_F16 ? write_rows<__half>(p, cache->dim, tensors, four, s)
+                                           : write_rows<float>(p, cache->dim, tensors, four, s));
 }
 
 int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t table_stride,
@@ -474,7 +459,8 @@ int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t 
     using namespace fp8mqa;
     const int rc = check_cache(cache);
     if (rc != FP8MQA_OK) return rc;
-    if (cache->type != FP8MQA_E4M3 || B < 0 || total < 0 || table_cols < 0 || out_type < 0 ||
+    const bool four = cache->type == FP8MQA_E2M1;
+    if (!scaled(cache->type) || B < 0 || total < 0 || table_cols < 0 || out_type < (four ? FP8MQA_BF16 : 0) ||
         out_type > FP8MQA_F32)
         return FP8MQA_ERR_INVALID_ARG;
     if (total * cache->heads >= int64_t(1) << 31 || B >= int64_t(1) << 31)
@@ -498,16 +484,16 @@ int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t 
     p.out = out;
     p.out_scale = out_scale;
     p.bounds = bounds_for(*st);
-    spans(p.bounds, 0, p.cache, cache->dim);
+    spans(p.bounds, 0, p.cache, *cache);
     spans(p.bounds, p.table, B);
     spans(p.bounds, kMemLens, starts, 4 * (B + 1));
     spans(p.bounds, kMemOut, out, total * cache->heads * cache->dim * size_of(out_type));
     spans(p.bounds, kMemOutScale, out_scale, 4 * total * cache->heads);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launched(out_type == FP8MQA_E4M3   ? read_rows<uint8_t>(p, cache->dim, st->sm_count, s)
-                    : out_type == FP8MQA_BF16 ? read_rows<__nv_bfloat16>(p, cache->dim, st->sm_count, s)
-                    : out_type == FP8MQA_F16  ? read_rows<__half>(p, cache->dim, st->sm_count, s)
-                                              : read_rows<float>(p, cache->dim, st->sm_count, s));
+    return launched(out_type == FP8MQA_E4M3   ? read_rows<uint8_t>(p, cache->dim, four, st->sm_count, s)
+                    : out_type == FP8MQA_BF16 ? read_rows<__nv_bfloat16>(p, cache->dim, four, st->sm_count, s)
+                    : out_type == FP8MQA_F16  ? read_rows<__half>(p, cache->dim, four, st->sm_count, s)
+                                              : read_rows<float>(p, cache->dim, four, st->sm_count, s));
 }
 
 int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_t T, int32_t H,
@@ -549,7 +535,7 @@ int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_t B, int32_
     p.suspend_ns = uint32_t(std::clamp<uint64_t>(p.wait_ns, 32, kPagedSuspendNs));
     if (!row_units(p.keys, &p.units)) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
     p.bounds = bounds_for(*st);
-    spans(p.bounds, 0, p.keys, kPagedDim);
+    spans(p.bounds, 0, p.keys, *keys);
     spans(p.bounds, p.table, B);
     spans(p.bounds, kMemLens, lens, 4 * B);
     spans(p.bounds, kMemQ, q_fp8, B * T * kPagedHeads * kPagedDim);
@@ -593,7 +579,7 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     if (rc != FP8MQA_OK) return rc;
     if (k->type != v->type || k->page_size != v->page_size || k->heads != v->heads ||
         k->dim != v->dim || q_heads % k->heads != 0 ||
-        (k->type != FP8MQA_E4M3 && k->type != q_type))
+        (!scaled(k->type) && k->type != q_type))
         return FP8MQA_ERR_INVALID_ARG;
     // tiles (of 16 positions or more) are counted in 32 bits, and so are positions, up to a few steps
     // (of 128 positions at most) past a row's end
@@ -636,8 +622,8 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     p.splits = static_cast<AttnSplit*>(workspace);
     p.partial = reinterpret_cast<float*>(p.splits + kAttnMaxCtas);
     p.bounds = bounds_for(*st);
-    spans(p.bounds, 0, p.k, k->dim * size_of(k->type));
-    spans(p.bounds, 1, p.v, v->dim * size_of(v->type));
+    spans(p.bounds, 0, p.k, *k);
+    spans(p.bounds, 1, p.v, *v);
     spans(p.bounds, p.table, B);
     spans(p.bounds, kMemLens, lens, 4 * B);
     spans(p.bounds, kMemIndices, indices, extent(B, 4 * indices_stride, n_indices, 4, 1, 0, 4));
@@ -648,6 +634,7 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     spans(p.bounds, kMemPartial, p.partial, int64_t(workspace_bytes - kAttnMaxCtas * sizeof(AttnSplit)));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return launched(k->type == FP8MQA_E4M3   ? attention_dim<FP8MQA_E4M3>(p, k->dim, st->sm_count, s)
+                    : k->type == FP8MQA_E2M1 ? attention_dim<FP8MQA_E2M1>(p, k->dim, st->sm_count, s)
                     : k->type == FP8MQA_BF16 ? attention_dim<FP8MQA_BF16>(p, k->dim, st->sm_count, s)
                                              : attention_dim<FP8MQA_F16>(p, k->dim, st->sm_count, s));
 }

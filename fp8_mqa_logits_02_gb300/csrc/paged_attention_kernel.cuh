@@ -58,6 +58,7 @@ constexpr int kAttnThreads = 128, kAttnWarps = kAttnThreads / 32;
 // Steps in a ring, for each warp that shares it, and CTAs of an SM: what fills the shared memory.  Three
 // steps and two CTAs take as long on the ragged batch and 5 % longer on selected positions.
 constexpr int kAttnStages = 2;
+constexpr int kAttnStages4 = 3;  // of E2M1 caches, whose steps are half as large
 constexpr int kAttnCtasPerSm = 3;
 constexpr int kAttnMaxCtas = 512;  // of one launch
 constexpr int64_t kAttnMaxPositions = INT32_MAX - 1024;  // of a row
@@ -97,24 +98,27 @@ struct PagedAttentionParams {
     PagedBounds bounds;
 };
 
-// kType: FP8MQA_E4M3, FP8MQA_BF16 or FP8MQA_F16 of the cache.  kNT: eights of heads of a warp.
+// kType: FP8MQA_E4M3, FP8MQA_BF16, FP8MQA_F16 or FP8MQA_E2M1 of the cache.  kNT: eights of heads of a warp.
 // kHq: warps that share a ring, for 8 kNT heads each of one key head.
 template <int kType, int kDim_, int kNT_, int kHq>
 struct AttnShape {
-    static constexpr bool kE4m3 = kType == 0, kBf16 = kType == 1;
+    static constexpr bool kE4m3 = kType == 0, kBf16 = kType == 1, kE2m1 = kType == 4;
+    static constexpr bool kScaled = kE4m3 || kE2m1;    // rows have scales
     static constexpr int kDim = kDim_, kNT = kNT_;
     static constexpr int kHeads = 8 * kNT;             // heads of a warp
-    static constexpr int kStages = kAttnStages * kHq;
-    static constexpr int kStep = kE4m3 ? 32 : 16;      // positions of a warp's step
+    static constexpr int kStages = (kE2m1 ? kAttnStages4 : kAttnStages) * kHq;
+    static constexpr int kStep = kScaled ? 32 : 16;    // positions of a warp's step
     static constexpr int kBlocks = kStep / 16;         // of 16 positions
-    static constexpr int kRowBytes = kDim * (kE4m3 ? 1 : 2);
+    static constexpr int kRowBytes = kE2m1 ? kDim / 2 : kDim * (kE4m3 ? 1 : 2);
+    static constexpr int kGroupBytes = kE2m1 ? kDim / kGroup : 0;  // of a row
     static constexpr int kPieces = kRowBytes / 16;
     static constexpr int kKRows = kStep / 8;           // rows of S^T a lane has
     static constexpr int kVWords = kRowBytes / 32;     // words of a V row a lane has
     static constexpr int kMT = kDim / 16;              // 16-blocks of dim
-    // a ring stage: K rows, V rows, their scales, and which rows are there
+    // a ring stage: K rows, V rows, their scales, their groups' scales, and which rows are there
     static constexpr int kRows = kStep * kRowBytes;
-    static constexpr int kScales = 2 * kRows, kThere = kScales + (kE4m3 ? 2 * kStep * 4 : 0);
+    static constexpr int kScales = 2 * kRows, kGroups = kScales + (kScaled ? 2 * kStep * 4 : 0);
+    static constexpr int kThere = kGroups + 2 * kStep * kGroupBytes;
     static constexpr int kStage = (kThere + 16 + 127) / 128 * 128;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kSmem = kAttnWarps / kHq * kRing;
@@ -184,6 +188,14 @@ template <int kPieces>
 __device__ __forceinline__ int v_place(int r, int c)
 {
     return r * kPieces + (kPieces >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
+}
+// The same for E2M1 rows of 64 or 32 bytes, of which a lane takes 8 or 4 (a read of V takes them of every
+// second of eight rows): rows change places, so that those four rows fill the banks.
+template <int kPieces>
+__device__ __forceinline__ int v_place4(int r, int c)
+{
+    return kPieces == 4 ? ((r & ~3) | (r & 1) << 1 | (r >> 1 & 1)) * 4 + (c ^ (r >> 1 & 2))
+                        : ((r & ~7) | (r & 1) << 2 | (r >> 1 & 3)) * 2 + c;
 }
 
 // The rows' positions and tiles.
@@ -329,7 +341,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                                 int64_t(h0 + h) * p.q_head_stride;
             // word w = 2 s + j (columns of fragment s) is word w % kRun of the run w / kRun of words that
             // lie together, as in the cache's rows: 16 values of 64, or 8 of 32
-            constexpr int kRun = S::kE4m3 ? 8 : 4;
+            // (E2M1: all of a lane's values, 32 or 16)
+            constexpr int kRun = S::kE2m1 ? kDim / 8 : S::kE4m3 ? 8 : 4;
 #pragma unroll
             for (int w = 0; w < 2 * S::kMT; w += 4) {
                 const int d = w / kRun * (8 * kRun) + t * (2 * kRun) + w % kRun * 2;
@@ -386,11 +399,26 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                 auto v_from = [&] { return v_base + uint64_t(ok ? at2 : 0) * p.v_units.unit + 16 * c; };
                 copy16(to + 16 * k_place<S::kPieces>(r, c), k_from(),
                        ok && in_bounds(p.bounds, kMemData, k_from(), 16));
-                copy16(to + S::kRows + 16 * v_place<S::kPieces>(r, c), v_from(),
+                const int v_to = S::kE2m1 ? v_place4<S::kPieces>(r, c) : v_place<S::kPieces>(r, c);
+                copy16(to + S::kRows + 16 * v_to, v_from(),
                        ok && in_bounds(p.bounds, kMemData2, v_from(), 16));
             }
-            if (S::kE4m3 && warp % kHq == 0) {
+            if (S::kScaled && warp % kHq == 0) {
                 const int64_t pg = there ? page : 0, rw = there ? row : 0;
+                if constexpr (S::kE2m1) {
+                    const uint8_t* const k_group = p.k.groups + pg * p.k.group_page_stride +
+                                                   rw * p.k.group_row_stride + kvh * p.k.group_head_stride;
+                    const uint8_t* const v_group = p.v.groups + pg * p.v.group_page_stride +
+                                                   rw * p.v.group_row_stride + kvh * p.v.group_head_stride;
+                    auto copy_groups = [&](uint32_t at, const uint8_t* from, bool ok) {
+                        if constexpr (S::kGroupBytes == 8) copy8(at, from, ok);
+                        else copy4(at, from, ok);
+                    };
+                    copy_groups(to + S::kGroups + S::kGroupBytes * lane, k_group,
+                                there && in_bounds(p.bounds, kMemGroups, k_group, S::kGroupBytes));
+                    copy_groups(to + S::kGroups + S::kGroupBytes * (S::kStep + lane), v_group,
+                                there && in_bounds(p.bounds, kMemGroups2, v_group, S::kGroupBytes));
+                }
                 const float* const k_from = p.k.scale + pg * p.k.scale_page_stride +
                                             rw * p.k.scale_row_stride + kvh * p.k.scale_head_stride;
                 const float* const v_from = p.v.scale + pg * p.v.scale_page_stride +
@@ -422,7 +450,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             float by = 1.0f;
-            if (S::kE4m3 && p.q_bf16) {
+            if (S::kScaled && p.q_bf16) {
                 // bfloat16 -> f16: exact but for the range, so each head is brought to a largest
                 // magnitude of 2^12 .. 2^13 by a power of two (what then falls below f16's range
                 // is under 2^-36 of the largest)
@@ -489,6 +517,51 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                 for (int mb = 0; mb < S::kBlocks; ++mb)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[nt][mb][j] = 0.0f;
+            if constexpr (S::kE2m1) {
+                // a lane's values of a row are one or two whole groups: kWords words of eight
+                constexpr int kWords = S::kRowBytes / 16;
+                const uint8_t* const k_groups = at_k + S::kGroups;
+#pragma unroll
+                for (int mb = 0; mb < S::kBlocks; ++mb) {
+                    uint32_t w[2][kWords], by[2][kWords];  // of rows g and g + 8
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = 16 * mb + 8 * i + g;
+                        if constexpr (kWords == 4) {
+                            const uint4 y = *reinterpret_cast<const uint4*>(at_k + 16 * k_place<S::kPieces>(r, t));
+                            w[i][0] = y.x;
+                            w[i][1] = y.y;
+                            w[i][2] = y.z;
+                            w[i][3] = y.w;
+                            const uint32_t two =
+                                f16x2_of_e4m3x2(*reinterpret_cast<const uint16_t*>(k_groups + r * 8 + 2 * t));
+                            by[i][0] = by[i][1] = __byte_perm(two, two, 0x1010);
+                            by[i][2] = by[i][3] = __byte_perm(two, two, 0x3232);
+                        } else {
+                            const uint2 y = *reinterpret_cast<const uint2*>(at_k + r * 32 + 8 * t);
+                            w[i][0] = y.x;
+                            w[i][1] = y.y;
+                            by[i][0] = by[i][1] = f16x2_of_e4m3x2(k_groups[r * 4 + t] * 0x101u);
+                        }
+                    }
+#pragma unroll
+                    for (int y = 0; y < kWords; ++y) {
+                        uint32_t a[2][4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            f16_of_e2m1(w[i][y], a[i]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) a[i][j] = mul_f16x2(a[i][j], by[i][y]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int nt = 0; nt < kNT; ++nt)
+                                mma16816<false>(x[nt][mb], a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1],
+                                                qf[nt][2 * y + j][0], qf[nt][2 * y + j][1]);
+                    }
+                }
+            } else {
 #pragma unroll
             for (int mb = 0; mb < S::kBlocks; ++mb)
 #pragma unroll
@@ -519,15 +592,16 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                             mma16816<S::kBf16>(x[nt][mb], a0, a1, a2, a3, qf[nt][s][0], qf[nt][s][1]);
                     }
                 }
+            }
 
             // ---- softmax: this lane has positions 8r + g, heads 2t and 2t + 1
             float row_lv[S::kKRows];  // log2 of the rows' value scales
             const float* const scales = reinterpret_cast<const float*>(at_k + S::kScales);
-            const bool negative = S::kE4m3 && __any_sync(~0u, scales[S::kStep + lane % S::kStep] < 0.0f);
+            const bool negative = S::kScaled && __any_sync(~0u, scales[S::kStep + lane % S::kStep] < 0.0f);
 #pragma unroll
             for (int r = 0; r < S::kKRows; ++r) {
-                const float row_ks = S::kE4m3 ? scales[r * 8 + g] : 1.0f;
-                row_lv[r] = S::kE4m3 ? log2_fast(fabsf(scales[S::kStep + r * 8 + g])) : 0.0f;
+                const float row_ks = S::kScaled ? scales[r * 8 + g] : 1.0f;
+                row_lv[r] = S::kScaled ? log2_fast(fabsf(scales[S::kStep + r * 8 + g])) : 0.0f;
                 const bool ok = here >> (r * 8 + g) & 1u;
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt)
@@ -549,21 +623,21 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                     for (int r = 0; r < S::kKRows; ++r) {
                         const float y = x[nt][r / 2][r % 2 * 2 + j];
                         top = fmaxf(top, y);
-                        if (S::kE4m3) wide = fmaxf(wide, y + row_lv[r]);
+                        if (S::kScaled) wide = fmaxf(wide, y + row_lv[r]);
                     }
 #pragma unroll
                     for (int o = 4; o < 32; o *= 2) {
                         top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-                        if (S::kE4m3) wide = fmaxf(wide, __shfl_xor_sync(~0u, wide, o));
+                        if (S::kScaled) wide = fmaxf(wide, __shfl_xor_sync(~0u, wide, o));
                     }
-                    if (!S::kE4m3) wide = top;
+                    if (!S::kScaled) wide = top;
                     // what the weights are relative to lags behind the largest score by kAttnLag at most
                     // (weights up to 2^8 are as good), which spares most steps the rescaling of O; not
                     // with bfloat16 weights, where a largest weight of 1 is one that is not rounded
                     // (16 rows of up to 16385: error 2.0e-3, 2.4e-3 with the lag)
                     if constexpr (!S::kBf16) {
                         // (l has the reference of the weights where those are its own terms)
-                        if constexpr (!S::kE4m3) top -= kAttnLift;
+                        if constexpr (!S::kScaled) top -= kAttnLift;
                         wide -= kAttnLift;
                         if (!(top > m[nt][j] + kAttnLag)) top = m[nt][j];
                         if (!(wide > w_top[nt][j] + kAttnLag)) wide = w_top[nt][j];
@@ -580,8 +654,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                         float& y = x[nt][r / 2][r % 2 * 2 + j];
                         const float e = exp2_fast(y - ref);
                         sum += e;
-                        y = S::kE4m3 ? exp2_fast(y + row_lv[r] - w_ref) : e;
-                        if (S::kE4m3 && negative)
+                        y = S::kScaled ? exp2_fast(y + row_lv[r] - w_ref) : e;
+                        if (S::kScaled && negative)
                             y = __uint_as_float(__float_as_uint(y) ^
                                                 (__float_as_uint(scales[S::kStep + r * 8 + g]) & 0x80000000u));
                     }
@@ -606,10 +680,22 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                     pf[nt][1] = transpose8(pack16<S::kBf16>(x[nt][mb][2], x[nt][mb][3]));
                 }
                 uint32_t w[4][S::kVWords];
+                uint32_t group[4];  // E2M1: the scale of the lane's columns, an E4M3 code
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int key = 16 * mb + r / 2 * 8 + 2 * t + r % 2;
-                    if constexpr (S::kVWords == 2) {
+                    if constexpr (S::kE2m1) {
+                        if constexpr (S::kVWords == 2) {
+                            const uint2 y = *reinterpret_cast<const uint2*>(
+                                at_v + 16 * v_place4<S::kPieces>(key, g / 2) + g % 2 * 8);
+                            w[r][0] = y.x;
+                            w[r][1] = y.y;
+                        } else {
+                            w[r][0] = *reinterpret_cast<const uint32_t*>(
+                                at_v + 16 * v_place4<S::kPieces>(key, g / 4) + g % 4 * 4);
+                        }
+                        group[r] = at_k[S::kGroups + (S::kStep + key) * S::kGroupBytes + g * S::kGroupBytes / 8];
+                    } else if constexpr (S::kVWords == 2) {
                         const uint2 y = *reinterpret_cast<const uint2*>(
                             at_v + 16 * v_place<S::kPieces>(key, g / 2) + g % 2 * 8);
                         w[r][0] = y.x;
@@ -626,6 +712,28 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                         }
                     }
                 }
+                if constexpr (S::kE2m1) {
+                    const uint32_t by01 = f16x2_of_e4m3x2(group[0] | group[1] << 8);
+                    const uint32_t by23 = f16x2_of_e4m3x2(group[2] | group[3] << 8);
+#pragma unroll
+                    for (int y = 0; y < S::kVWords; ++y) {
+                        // bytes of one column of two rows: columns 0, 2, 4 and 6 of a word's, then 1, 3, 5 and 7
+                        constexpr uint32_t kLow = 0x0F0F0F0Fu;
+                        uint32_t a[4][4];
+                        f16_of_e2m1((w[0][y] & kLow) | (w[1][y] << 4 & ~kLow), a[0]);
+                        f16_of_e2m1((w[0][y] >> 4 & kLow) | (w[1][y] & ~kLow), a[1]);
+                        f16_of_e2m1((w[2][y] & kLow) | (w[3][y] << 4 & ~kLow), a[2]);
+                        f16_of_e2m1((w[2][y] >> 4 & kLow) | (w[3][y] & ~kLow), a[3]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a0 = mul_f16x2(a[0][j], by01), a1 = mul_f16x2(a[1][j], by01);
+                            const uint32_t a2 = mul_f16x2(a[2][j], by23), a3 = mul_f16x2(a[3][j], by23);
+#pragma unroll
+                            for (int nt = 0; nt < kNT; ++nt)
+                                mma16816<false>(o[nt][4 * y + j], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                        }
+                    }
+                } else {
 #pragma unroll
                 for (int i = 0; i < S::kMT; ++i) {
                     uint32_t a0, a1, a2, a3;
@@ -643,6 +751,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                     for (int nt = 0; nt < kNT; ++nt)
                         mma16816<S::kBf16>(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
                 }
+                }
             }
             if (kHq == 1) __syncwarp();  // the stage may be filled again
         }
@@ -657,7 +766,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             for (int j = 0; j < 2; ++j) {
                 // O is counted in 2^w_top, m and l in 2^m
                 const float v_back =
-                    !S::kE4m3 ? 1.0f : w_top[nt][j] == -CUDART_INF_F ? 0.0f : exp2_fast(w_top[nt][j] - m[nt][j]);
+                    !S::kScaled ? 1.0f : w_top[nt][j] == -CUDART_INF_F ? 0.0f : exp2_fast(w_top[nt][j] - m[nt][j]);
                 float sum = l[nt][j];
                 sum += __shfl_xor_sync(~0u, sum, 4);
                 sum += __shfl_xor_sync(~0u, sum, 8);
@@ -670,7 +779,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                 // four columns of a head at a time: those of fragments i and i + 1 lie together
 #pragma unroll
                 for (int i = 0; i < S::kMT; i += 2) {
-                    const int d = S::kE4m3 ? g * (kDim / 8) + 2 * i
+                    const int d = S::kScaled ? g * (kDim / 8) + 2 * i
                                            : i / 4 * 64 + g * 8 + 2 * i % 8;
                     *reinterpret_cast<float4*>(s_o + h * S::kPitch + d) =
                         make_float4(o[nt][i][j] * v_back, o[nt][i][2 + j] * v_back,

@@ -27,6 +27,8 @@ struct Entries {
     decltype(&fp8_mqa_logits_paged) logits_paged = nullptr;
     decltype(&fp8_mqa_attention_paged_workspace_bytes) workspace_bytes = nullptr;
     decltype(&fp8_mqa_attention_paged) attention_paged = nullptr;
+    decltype(&fp8_mqa_pages_update) pages_update = nullptr;
+    decltype(&fp8_mqa_norm_rotate) norm_rotate = nullptr;
 } g_entry;
 
 PyObject* g_error = nullptr;  // Fp8MqaError
@@ -99,13 +101,15 @@ int32_t type_of(at::ScalarType t)
         case at::kBFloat16: return FP8MQA_BF16;
         case at::kHalf: return FP8MQA_F16;
         case at::kFloat: return FP8MQA_F32;
+        case at::ScalarType::Float4_e2m1fn_x2: return FP8MQA_E2M1;
         default: return -1;
     }
 }
 
-// A cache of e4m3 data and its scales, or of the type `other` without.
-fp8mqa_cache cache_of(PyObject* data_o, PyObject* scale_o, const char* name, const c10::Device& device,
-                      at::ScalarType other = at::kFloat8_e4m3fn)
+// A cache of e4m3 data and its scales, of e2m1 data (unless groups_o is NULL, where such caches are not taken) with
+// its groups' scales too, or of the type `other` without.
+fp8mqa_cache cache_of(PyObject* data_o, PyObject* scale_o, PyObject* groups_o, const char* name,
+                      const c10::Device& device, at::ScalarType other = at::kFloat8_e4m3fn)
 {
     const std::string what(name);
     const at::Tensor& data = cuda_tensor(data_o, (what + " data").c_str(), &device);
@@ -121,13 +125,34 @@ fp8mqa_cache cache_of(PyObject* data_o, PyObject* scale_o, const char* name, con
         if (data.size(i) > INT32_MAX) bad(PyExc_ValueError, what + " data is too large: " + list(data.sizes()));
     c.page_size = int32_t(data.size(1));
     c.heads = int32_t(data.size(2));
-    c.dim = int32_t(data.size(3));
     c.type = type_of(dtype);
+    const bool four = c.type == FP8MQA_E2M1 && groups_o;
+    // two values an element
+    if (four && data.size(3) > INT32_MAX / 2)
+        bad(PyExc_ValueError, what + " data is too large: " + list(data.sizes()));
+    c.dim = int32_t(data.size(3)) * (four ? 2 : 1);
     c.page_stride = data.stride(0);
     c.row_stride = data.stride(1);
     c.head_stride = data.stride(2);
     c.scale_page_stride = c.scale_row_stride = c.scale_head_stride = 0;
-    if (dtype == at::kFloat8_e4m3fn) {
+    c.groups = nullptr;
+    c.group_page_stride = c.group_row_stride = c.group_head_stride = 0;
+    if (!four && groups_o && groups_o != Py_None)
+        bad(PyExc_ValueError, what + " groups go with float4_e2m1fn_x2 data only");
+    if (four) {
+        const at::Tensor& groups = cuda_tensor(groups_o, (what + " groups").c_str(), &device);
+        if (groups.scalar_type() != at::kFloat8_e4m3fn || groups.dim() != 4 || groups.size(0) != data.size(0) ||
+            groups.size(1) != data.size(1) || groups.size(2) != data.size(2) || groups.size(3) != c.dim / 16)
+            bad(PyExc_ValueError, what + " groups must be float8_e4m3fn " +
+                                      list({data.size(0), data.size(1), data.size(2), c.dim / 16}));
+        if (groups.size(3) > 1 && groups.stride(3) != 1)
+            bad(PyExc_ValueError, what + " groups must be contiguous in their last dimension");
+        c.groups = static_cast<uint8_t*>(groups.data_ptr());
+        c.group_page_stride = groups.stride(0);
+        c.group_row_stride = groups.stride(1);
+        c.group_head_stride = groups.stride(2);
+    }
+    if (dtype == at::kFloat8_e4m3fn || four) {
         const at::Tensor& scale = cuda_tensor(scale_o, (what + " scale").c_str(), &device);
         if (scale.scalar_type() != at::kFloat || scale.dim() != 3 || scale.size(0) != data.size(0) ||
             scale.size(1) != data.size(1) || scale.size(2) != data.size(2))
@@ -139,9 +164,10 @@ fp8mqa_cache cache_of(PyObject* data_o, PyObject* scale_o, const char* name, con
     } else {
         if (dtype != other)
             bad(PyExc_TypeError, what + " data must be " + name_of(at::kFloat8_e4m3fn) +
-                                     (other == at::kFloat8_e4m3fn ? "" : " or " + name_of(other)) + ", got " +
+                                     (groups_o ? ", torch.float4_e2m1fn_x2" : "") + (other == at::kFloat8_e4m3fn ? "" : " or " + name_of(other)) + ", got " +
                                      name_of(dtype));
-        if (scale_o != Py_None) bad(PyExc_ValueError, what + " scale goes with float8_e4m3fn data only");
+        if (scale_o != Py_None) bad(PyExc_ValueError, what + " scale goes with float8_e4m3fn" +
+                                                   std::string(groups_o ? " or float4_e2m1fn_x2" : "") + " data only");
     }
     return c;
 }
@@ -173,20 +199,20 @@ void expect(Py_ssize_t n, Py_ssize_t want)
     if (!g_entry.attention_paged) bad(PyExc_RuntimeError, "the library's entry points are not bound");
 }
 
-// slots, k, k_data, k_scale, v, v_data, v_scale
+// slots, k, k_data, k_scale, v, v_data, v_scale, k_groups, v_groups
 PyObject* cache_write(PyObject* const* a, Py_ssize_t n)
 {
-    expect(n, 7);
+    expect(n, 9);
     const c10::Device device = cuda_tensor(a[2], "k data").device();
-    const fp8mqa_cache ck = cache_of(a[2], a[3], "k", device);
+    const fp8mqa_cache ck = cache_of(a[2], a[3], a[7], "k", device);
     const at::Tensor& slots = ints(a[0], "slots", device, 1, -1);
     const bool pair = a[4] != Py_None;
-    if (pair != (a[5] != Py_None) || pair != (a[6] != Py_None))
+    if (pair != (a[5] != Py_None) || pair != (a[6] != Py_None) || (!pair && a[8] != Py_None))
         bad(PyExc_ValueError, "v, v_data and v_scale go together");
     auto rows = [&](PyObject* o, const char* name, const at::Tensor* like) -> const at::Tensor& {
         const at::Tensor& x = cuda_tensor(o, name, &device);
         const int32_t type = type_of(x.scalar_type());
-        if (type < 0 || type == FP8MQA_E4M3 || (like && x.scalar_type() != like->scalar_type()))
+        if (type < 0 || type == FP8MQA_E4M3 || type == FP8MQA_E2M1 || (like && x.scalar_type() != like->scalar_type()))
             bad(PyExc_TypeError, std::string(name) + " must be bfloat16, float16 or float32" +
                                      (like ? " as k is" : "") + ", got " + name_of(x.scalar_type()));
         if (x.dim() != 3 || x.size(0) != slots.size(0) || x.size(1) != ck.heads || x.size(2) != ck.dim)
@@ -201,7 +227,8 @@ PyObject* cache_write(PyObject* const* a, Py_ssize_t n)
     const void* v_ptr = nullptr;
     int64_t v_row = 0, v_head = 0;
     if (pair) {
-        cv = cache_of(a[5], a[6], "v", device);
+        cv = cache_of(a[5], a[6], a[8], "v", device);
+        if (cv.type != ck.type) bad(PyExc_TypeError, "v data must be of k data's type");
         if (cv.page_size != ck.page_size || cv.heads != ck.heads || cv.dim != ck.dim)
             bad(PyExc_ValueError, "v data must be " + list({ck.page_size, ck.heads, ck.dim}) + " a page, as k data is");
         const at::Tensor& v = rows(a[4], "v", &k);
@@ -223,17 +250,19 @@ PyObject* cache_write(PyObject* const* a, Py_ssize_t n)
     Py_RETURN_NONE;
 }
 
-// data, scale, table, starts, total, dtype
+// data, scale, table, starts, total, dtype, groups
 PyObject* cache_read(PyObject* const* a, Py_ssize_t n)
 {
-    expect(n, 6);
+    expect(n, 7);
     const c10::Device device = cuda_tensor(a[0], "data").device();
-    const fp8mqa_cache c = cache_of(a[0], a[1], "cache", device);
+    const fp8mqa_cache c = cache_of(a[0], a[1], a[6], "cache", device);
     const at::Tensor& table = ints(a[2], "table", device, 2, -1);
     const at::Tensor& starts = ints(a[3], "starts", device, 1, table.size(0) + 1);
     const int32_t type = THPDtype_Check(a[5]) ? type_of(reinterpret_cast<THPDtype*>(a[5])->scalar_type) : -1;
-    if (type < 0)
-        bad(PyExc_TypeError, "dtype must be float8_e4m3fn, bfloat16, float16 or float32");
+    if (type < 0 || type == FP8MQA_E2M1 || (type == FP8MQA_E4M3 && c.type == FP8MQA_E2M1))
+        bad(PyExc_TypeError, c.type == FP8MQA_E2M1
+                                 ? "dtype must be bfloat16, float16 or float32 for a cache in 4 bits"
+                                 : "dtype must be float8_e4m3fn, bfloat16, float16 or float32");
     const at::ScalarType dtype = reinterpret_cast<THPDtype*>(a[5])->scalar_type;
     const long long total = PyLong_AsLongLong(a[4]);
     if (total == -1 && PyErr_Occurred()) throw Raised{};
@@ -268,7 +297,7 @@ PyObject* logits_paged(PyObject* const* a, Py_ssize_t n)
     if (w.scalar_type() != at::kFloat || w.dim() != 3 || w.size(0) != B || w.size(1) != T ||
         w.size(2) != kHeads || !w.is_contiguous())
         bad(PyExc_ValueError, "w must be contiguous float32 " + list({B, T, kHeads}));
-    const fp8mqa_cache c = cache_of(a[1], a[2], "key", device);
+    const fp8mqa_cache c = cache_of(a[1], a[2], nullptr, "key", device);
     if (c.heads != 1 || c.dim != kDim) bad(PyExc_ValueError, "key data must be [pages, page_size, 1, 128]");
     const at::Tensor& table = ints(a[4], "table", device, 2, B);
     const at::Tensor& lens = ints(a[5], "lens", device, 1, B);
@@ -313,10 +342,10 @@ PyObject* logits_paged(PyObject* const* a, Py_ssize_t n)
     return THPVariable_Wrap(std::move(out));
 }
 
-// q, k_data, v_data, table, lens, sm_scale, k_scale, v_scale, indices, return_lse
+// q, k_data, v_data, table, lens, sm_scale, k_scale, v_scale, indices, return_lse, k_groups, v_groups
 PyObject* attention_paged(PyObject* const* a, Py_ssize_t n)
 {
-    expect(n, 10);
+    expect(n, 12);
     const at::Tensor& q = cuda_tensor(a[0], "q");
     const c10::Device device = q.device();
     const at::ScalarType dtype = q.scalar_type();
@@ -325,7 +354,8 @@ PyObject* attention_paged(PyObject* const* a, Py_ssize_t n)
     if (q.dim() != 3 || q.stride(2) != 1)
         bad(PyExc_ValueError, "q must be [B, q_heads, dim], contiguous in its last dimension");
     const int64_t B = q.size(0), heads = q.size(1), dim = q.size(2);
-    const fp8mqa_cache k = cache_of(a[1], a[6], "k", device, dtype), v = cache_of(a[2], a[7], "v", device, dtype);
+    const fp8mqa_cache k = cache_of(a[1], a[6], a[10], "k", device, dtype),
+                       v = cache_of(a[2], a[7], a[11], "v", device, dtype);
     if (k.pages != v.pages || k.page_size != v.page_size || k.heads != v.heads || k.dim != v.dim || k.type != v.type)
         bad(PyExc_ValueError, "k data and v data must have one shape and type");
     if (k.dim != dim || heads == 0 || heads > INT32_MAX || k.heads == 0 || heads % k.heads != 0)
@@ -371,27 +401,181 @@ PyObject* attention_paged(PyObject* const* a, Py_ssize_t n)
     return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(out)), THPVariable_Wrap(std::move(lse)));
 }
 
+// table, lens, change, free, n_free, page_size, total
+PyObject* pages_update(PyObject* const* a, Py_ssize_t n)
+{
+    expect(n, 7);
+    const c10::Device device = cuda_tensor(a[0], "table").device();
+    const at::Tensor& table = ints(a[0], "table", device, 2, -1);
+    const int64_t B = table.size(0), cols = table.size(1);
+    const at::Tensor& lens = ints(a[1], "lens", device, 1, B);
+    const at::Tensor& change = ints(a[2], "change", device, 1, B);
+    const at::Tensor& pool = ints(a[3], "free", device, 1, -1);
+    const at::Tensor& n_free = ints(a[4], "n_free", device, 1, 1);
+    const long long page = PyLong_AsLongLong(a[5]);
+    if (page == -1 && PyErr_Occurred()) throw Raised{};
+    const long long total = PyLong_AsLongLong(a[6]);
+    if (total == -1 && PyErr_Occurred()) throw Raised{};
+    if (page < 1 || page > INT32_MAX) bad(PyExc_ValueError, "page_size must be 1 or more");
+    if (total < 0) bad(PyExc_ValueError, "total must not be negative");
+    if (B > 1 && table.stride(0) < cols) bad(PyExc_ValueError, "the rows of table must not overlap: they are written");
+    const c10::cuda::CUDAGuard guard(device);
+    at::Tensor out[5] = {empty({total}, at::kInt, device), empty({total}, at::kInt, device),
+                         empty({total}, at::kInt, device), empty({B + 1}, at::kInt, device),
+                         empty({B}, at::kInt, device)};
+    int32_t* to[5];
+    for (int i = 0; i < 5; ++i) to[i] = static_cast<int32_t*>(out[i].data_ptr());
+    auto *ids = static_cast<int32_t*>(table.data_ptr()), *len = static_cast<int32_t*>(lens.data_ptr());
+    auto *stack = static_cast<int32_t*>(pool.data_ptr()), *height = static_cast<int32_t*>(n_free.data_ptr());
+    const auto* by = static_cast<const int32_t*>(change.data_ptr());
+    const int64_t pitch = table.stride(0), capacity = pool.size(0);
+    void* stream = current_stream(device);
+    done(unlocked([&] {
+             return g_entry.pages_update(ids, pitch, int32_t(cols), int32_t(page), len, by, B, stack, capacity, height,
+                                         total, to[0], to[1], to[2], to[3], to[4], stream);
+         }),
+         "fp8_mqa_pages_update");
+    return Py_BuildValue("(NNNNN)", THPVariable_Wrap(std::move(out[0])), THPVariable_Wrap(std::move(out[1])),
+                         THPVariable_Wrap(std::move(out[2])), THPVariable_Wrap(std::move(out[3])),
+                         THPVariable_Wrap(std::move(out[4])));
+}
+
+// q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, q_out, k_out
+PyObject* norm_rotate(PyObject* const* a, Py_ssize_t n)
+{
+    expect(n, 11);
+    const at::Tensor& q = cuda_tensor(a[0], "q");
+    const c10::Device device = q.device();
+    const at::ScalarType type = q.scalar_type();
+    if (type != at::kBFloat16 && type != at::kHalf && type != at::kFloat)
+        bad(PyExc_TypeError, "q must be bfloat16, float16 or float32, got " + name_of(type));
+    at::ScalarType to = type;
+    if (a[8] != Py_None) {
+        to = THPDtype_Check(a[8]) ? reinterpret_cast<THPDtype*>(a[8])->scalar_type : at::kByte;
+        if (to != type && to != at::kFloat8_e4m3fn)
+            bad(PyExc_TypeError, "dtype must be float8_e4m3fn or q's, " + name_of(type));
+    }
+    const bool e4m3 = to == at::kFloat8_e4m3fn;
+    if (q.dim() != 3) bad(PyExc_ValueError, "q must be [T, heads, dim], got " + list(q.sizes()));
+    const int64_t T = q.size(0), dim = q.size(2);
+    if (dim != 64 && dim != 128) bad(PyExc_ValueError, "q must have heads of 64 or 128 values, got " + list(q.sizes()));
+    const at::Tensor& positions = cuda_tensor(a[2], "positions", &device);
+    if (positions.scalar_type() != at::kInt && positions.scalar_type() != at::kLong)
+        bad(PyExc_TypeError, "positions must be int32 or int64, got " + name_of(positions.scalar_type()));
+    if (positions.dim() != 1 || positions.size(0) != T || (T > 1 && positions.stride(0) != 1))
+        bad(PyExc_ValueError, "positions must be contiguous " + list({T}) + ", got " + list(positions.sizes()));
+    const at::Tensor& freq = cuda_tensor(a[3], "inv_freq", &device);
+    if (freq.scalar_type() != at::kFloat) bad(PyExc_TypeError, "inv_freq must be float32, got " + name_of(freq.scalar_type()));
+    if (freq.dim() != 1 || !freq.is_contiguous() || 2 * freq.size(0) > dim || freq.size(0) % 8 != 0)
+        bad(PyExc_ValueError, "inv_freq must be contiguous, a multiple of 8 and at most dim / 2 frequencies, got " +
+                                  list(freq.sizes()));
+    const double eps = PyFloat_AsDouble(a[6]);
+    if (eps == -1.0 && PyErr_Occurred()) throw Raised{};
+    const int interleaved = PyObject_IsTrue(a[7]);
+    if (interleaved < 0) throw Raised{};
+    const c10::cuda::CUDAGuard guard(device);
+    fp8mqa_heads heads[2] = {};
+    at::Tensor out[2], scale[2];
+    PyObject* given[2] = {nullptr, nullptr};
+    for (int i = 0; i < 2; ++i) {
+        const std::string name(i ? "k" : "q");
+        if (i && a[1] == Py_None) {
+            if (a[5] != Py_None || a[10] != Py_None) bad(PyExc_ValueError, "k_weight and k_out go with k");
+            continue;
+        }
+        const at::Tensor& x = cuda_tensor(a[i], name.c_str(), &device);
+        if (x.scalar_type() != type) bad(PyExc_TypeError, "k must be " + name_of(type) + " as q is, got " + name_of(x.scalar_type()));
+        if (x.dim() != 3 || x.size(0) != T || x.size(2) != dim || x.size(1) > INT32_MAX)
+            bad(PyExc_ValueError, name + " must be " + list({T, x.dim() == 3 ? x.size(1) : 1, dim}) + ", got " + list(x.sizes()));
+        if (x.stride(2) != 1) bad(PyExc_ValueError, name + " must be contiguous in its last dimension");
+        fp8mqa_heads& h = heads[i];
+        h.x = x.data_ptr();
+        h.row_stride = x.stride(0);
+        h.head_stride = x.stride(1);
+        h.heads = int32_t(x.size(1));
+        h.weight_type = type_of(type);
+        if (a[4 + i] != Py_None) {
+            const at::Tensor& w = cuda_tensor(a[4 + i], (name + "_weight").c_str(), &device);
+            if (w.scalar_type() != type && w.scalar_type() != at::kFloat)
+                bad(PyExc_TypeError, name + "_weight must be " + name_of(type) + " or torch.float32, got " + name_of(w.scalar_type()));
+            if (w.dim() != 1 || w.size(0) != dim || w.stride(0) != 1)
+                bad(PyExc_ValueError, name + "_weight must be contiguous " + list({dim}) + ", got " + list(w.sizes()));
+            h.weight = w.data_ptr();
+            h.weight_type = type_of(w.scalar_type());
+        }
+        if (a[9 + i] != Py_None) {
+            const at::Tensor& o = cuda_tensor(a[9 + i], (name + "_out").c_str(), &device);
+            if (e4m3) bad(PyExc_ValueError, name + "_out does not go with float8_e4m3fn results");
+            if (o.scalar_type() != type || o.dim() != 3 || o.size(0) != T || o.size(1) != x.size(1) || o.size(2) != dim ||
+                o.stride(2) != 1)
+                bad(PyExc_ValueError, name + "_out must be " + name_of(type) + " " + list(x.sizes()) +
+                                          ", contiguous in its last dimension");
+            // written: nothing of it may overlap
+            if ((T > 1 && o.stride(0) < dim) || (x.size(1) > 1 && o.stride(1) < dim))
+                bad(PyExc_ValueError, name + "_out must not overlap");
+            given[i] = a[9 + i];
+            h.out = o.data_ptr();
+            h.out_row_stride = o.stride(0);
+            h.out_head_stride = o.stride(1);
+        } else {
+            out[i] = empty({T, x.size(1), dim}, to, device);
+            h.out = out[i].data_ptr();
+            h.out_row_stride = out[i].stride(0);
+            h.out_head_stride = out[i].stride(1);
+            if (e4m3) {
+                scale[i] = empty({T, x.size(1)}, at::kFloat, device);
+                h.out_scale = static_cast<float*>(scale[i].data_ptr());
+            }
+        }
+    }
+    const void* pos = positions.data_ptr();
+    const auto* f = static_cast<const float*>(freq.data_ptr());
+    const int32_t wide = positions.scalar_type() == at::kLong ? 8 : 4, rotated = int32_t(2 * freq.size(0));
+    void* stream = current_stream(device);
+    done(unlocked([&] {
+             return g_entry.norm_rotate(&heads[0], a[1] == Py_None ? nullptr : &heads[1], type_of(type), type_of(to), T,
+                                        int32_t(dim), pos, wide, f, rotated, interleaved, float(eps), stream);
+         }),
+         "fp8_mqa_norm_rotate");
+    PyObject* result[2];
+    for (int i = 0; i < 2; ++i) {
+        if (given[i]) {
+            Py_INCREF(given[i]);
+            result[i] = given[i];
+        } else if (!out[i].defined()) {
+            Py_INCREF(Py_None);
+            result[i] = Py_None;
+        } else {
+            result[i] = THPVariable_Wrap(std::move(out[i]));
+            if (e4m3) result[i] = Py_BuildValue("(NN)", result[i], THPVariable_Wrap(std::move(scale[i])));
+        }
+    }
+    return Py_BuildValue("(NN)", result[0], result[1]);
+}
+
 // The entry points' addresses (cache_write, cache_read, logits_paged, workspace_bytes,
-// attention_paged) and the error class.
+// attention_paged, pages_update, norm_rotate) and the error class.
 PyObject* bind(PyObject* const* a, Py_ssize_t n)
 {
-    if (n != 6) bad(PyExc_TypeError, "wrong number of arguments");
-    void* p[5];
-    for (int i = 0; i < 5; ++i) {
+    if (n != 8) bad(PyExc_TypeError, "wrong number of arguments");
+    void* p[7];
+    for (int i = 0; i < 7; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null entry point");
             throw Raised{};
         }
     }
-    Py_INCREF(a[5]);
+    Py_INCREF(a[7]);
     Py_XDECREF(g_error);
-    g_error = a[5];
+    g_error = a[7];
     g_entry.cache_write = reinterpret_cast<decltype(g_entry.cache_write)>(p[0]);
     g_entry.cache_read = reinterpret_cast<decltype(g_entry.cache_read)>(p[1]);
     g_entry.logits_paged = reinterpret_cast<decltype(g_entry.logits_paged)>(p[2]);
     g_entry.workspace_bytes = reinterpret_cast<decltype(g_entry.workspace_bytes)>(p[3]);
     g_entry.attention_paged = reinterpret_cast<decltype(g_entry.attention_paged)>(p[4]);
+    g_entry.pages_update = reinterpret_cast<decltype(g_entry.pages_update)>(p[5]);
+    g_entry.norm_rotate = reinterpret_cast<decltype(g_entry.norm_rotate)>(p[6]);
     Py_RETURN_NONE;
 }
 
@@ -416,6 +600,7 @@ PyMethodDef method(const char* name)
 
 PyMethodDef g_methods[] = {method<cache_write>("cache_write"), method<cache_read>("cache_read"),
                            method<logits_paged>("logits_paged"), method<attention_paged>("attention_paged"),
+                           method<pages_update>("pages_update"), method<norm_rotate>("norm_rotate"),
                            method<bind>("bind"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_paged_binding", nullptr, -1, g_methods,

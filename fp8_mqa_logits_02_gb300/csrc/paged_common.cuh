@@ -17,12 +17,19 @@ namespace fp8mqa {
 constexpr float kE4m3Max = 448.0f;
 constexpr float kTinyMax = 1e-30f;  // the least row maximum that a scale is made from
 
-// A cache as a kernel sees it; data strides in bytes.
+// E2M1 rows: values 0, 0.5, 1, 1.5, 2, 3, 4 and 6 with a sign, two a byte (the first one low), an E4M3 scale for
+// each 16 of them (a group) and an fp32 scale for the row: value = data * group * scale.
+constexpr int kGroup = 16;
+constexpr float kE2m1Top = 2688.0f;  // of data * group: 6 * 448
+
+// A cache as a kernel sees it; data strides in bytes.  `groups` is there for E2M1.
 struct PagedView {
     uint8_t* data;
     float* scale;
+    uint8_t* groups;
     int64_t page_stride, row_stride, head_stride;
     int64_t scale_page_stride, scale_row_stride, scale_head_stride;
+    int64_t group_page_stride, group_row_stride, group_head_stride;
     int32_t pages, page_size, heads;
 };
 
@@ -79,6 +86,17 @@ enum PagedMemory : int32_t {
     kMemOutScale,  // or the log of the softmax's sum
     kMemSplits,
     kMemPartial,
+    kMemGroups,    // scales of 16 values
+    kMemGroups2,
+    kMemPositions,
+    kMemFreq,
+    kMemWeight,    // a norm's
+    kMemWeight2,
+    kMemOut2,
+    kMemOutScale2,
+    kMemFree,      // the stack of free pages
+    kMemFreeCount,
+    kMemStarts,    // where they are written
     kMemKinds
 };
 constexpr int32_t kPagedOutside = 2;  // status bit: an access that was not made
@@ -124,6 +142,44 @@ __device__ __forceinline__ void f16_of_e4m3(uint32_t four, uint32_t* lo, uint32_
         : "r"(four));
 }
 
+// Two E4M3 values (the low bytes) as f16 values: exact.
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t two)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+
+// Eight E2M1 values as f16 values, in order: exact.
+__device__ __forceinline__ void f16_of_e2m1(uint32_t eight, uint32_t (&h)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(eight));
+}
+
+// Eight values as E2M1, each to the nearest (ties to even), within +-6.
+__device__ __forceinline__ uint32_t e2m1_of(const float* x)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 template <class T>
 __device__ __forceinline__ float to_float(T x) { return float(x); }
 template <>
@@ -153,6 +209,12 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
 {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 8 : 0)
                  : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there)

@@ -1,0 +1,214 @@
+// Host side of a serving step's other entry points declared in include/fp8_mqa_logits.h: page tables,
+// and norms with rotation.  Argument checks, the choice of kernel, and the launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/fp8_mqa_logits.h"
+#include "norm_rotate_kernel.cuh"
+#include "pages_kernel.cuh"
+#include "paged_launch.cuh"
+
+namespace fp8mqa {
+namespace {
+
+// A cluster of 8 CTAs where there is enough to write, else one, which has no barrier to wait for.
+constexpr int kPagesCluster = 8;
+constexpr int64_t kPagesOneCta = 4096;  // tokens and requests
+
+cudaError_t pages_launch(const PagesParams& p, cudaStream_t s)
+{
+    const unsigned ctas = int64_t(p.total) + p.B > kPagesOneCta ? kPagesCluster : 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kPagesThreads);
+    cfg.dynamicSmemBytes = 3 * size_t(p.B + 1) * sizeof(int32_t);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, pages_update_kernel, p);
+}
+
+// What a call that needs more shared memory than a kernel gets unasked sets up once for each device.
+bool pages_smem()
+{
+    return cudaFuncSetAttribute(pages_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                int(3 * (kPagesMaxRows + 1) * sizeof(int32_t))) == cudaSuccess;
+}
+
+template <class X, int kDim, bool kE4m3>
+cudaError_t rotate_launch(NormRotateParams& p, bool vec, int sm_count, cudaStream_t s)
+{
+    // Heads that a group of lanes takes: sine and cosine are made once for them, but there should be
+    // groups for every SM.
+    constexpr int64_t kGroups = kRotateThreads / (kDim / 8);
+    const int64_t rows = p.T * (int64_t(p.heads[0]) + p.heads[1]);
+    const int64_t most = std::max(p.heads[0], p.heads[1]);
+    p.per_unit = int32_t(std::clamp<int64_t>(rows / (kGroups * 4 * sm_count), 1, std::min<int64_t>(8, most)));
+    for (int i = 0; i < 2; ++i) p.units[i] = (p.heads[i] + p.per_unit - 1) / p.per_unit;
+    const int64_t units = int64_t(p.units[0]) + p.units[1];
+    p.by_units = FastDiv(uint32_t(units));
+    const dim3 grid(unsigned((p.T * units + kGroups - 1) / kGroups));
+    return vec ? launch_after(norm_rotate_kernel<X, kDim, kE4m3, true>, grid, kRotateThreads, 0, s, p)
+               : launch_after(norm_rotate_kernel<X, kDim, kE4m3, false>, grid, kRotateThreads, 0, s, p);
+}
+
+template <class X>
+cudaError_t rotate_type(NormRotateParams& p, int32_t dim, bool e4m3, bool vec, int sm_count, cudaStream_t s)
+{
+    if (dim == 64)
+        return e4m3 ? rotate_launch<X, 64, true>(p, vec, sm_count, s) : rotate_launch<X, 64, false>(p, vec, sm_count, s);
+    return e4m3 ? rotate_launch<X, 128, true>(p, vec, sm_count, s) : rotate_launch<X, 128, false>(p, vec, sm_count, s);
+}
+
+int check_heads(const fp8mqa_heads* h, int32_t x_type, int32_t out_type)
+{
+    if (!h || h->heads < 0) return FP8MQA_ERR_INVALID_ARG;
+    if (h->heads == 0) return FP8MQA_OK;
+    if (!h->x || !h->out || (out_type == FP8MQA_E4M3) != (h->out_scale != nullptr)) return FP8MQA_ERR_INVALID_ARG;
+    if (h->weight && h->weight_type != x_type && h->weight_type != FP8MQA_F32) return FP8MQA_ERR_INVALID_ARG;
+    const uintptr_t e = uintptr_t(size_of(x_type));
+    if (!on(h->x, e) || !on(h->out_scale, 4) || (h->weight && !on(h->weight, uintptr_t(size_of(h->weight_type)))))
+        return FP8MQA_ERR_MISALIGNED;
+    if (out_type != FP8MQA_E4M3) return on(h->out, e) ? FP8MQA_OK : FP8MQA_ERR_MISALIGNED;
+    // E4M3 goes four values at a time
+    return on(h->out, 4) && h->out_row_stride % 4 == 0 && h->out_head_stride % 4 == 0 ? FP8MQA_OK : FP8MQA_ERR_MISALIGNED;
+}
+
+}  // namespace
+}  // namespace fp8mqa
+
+extern "C" {
+
+int fp8_mqa_pages_update(int32_t* table, int64_t table_stride, int32_t table_cols, int32_t page_size, int32_t* lens,
+                         const int32_t* change, int64_t B, int32_t* free_pages, int64_t capacity, int32_t* n_free,
+                         int64_t total, int32_t* slots, int32_t* positions, int32_t* rows, int32_t* starts,
+                         int32_t* changed, void* stream)
+{
+    using namespace fp8mqa;
+    if (B < 0 || table_cols < 0 || page_size < 1 || capacity < 0 || total < 0) return FP8MQA_ERR_INVALID_ARG;
+    if (B > kPagesMaxRows || int64_t(table_cols) * page_size > INT32_MAX || capacity > INT32_MAX || total > INT32_MAX)
+        return FP8MQA_ERR_UNSUPPORTED_SHAPE;
+    if ((B > 0 && (!lens || !change || !changed)) || (B > 0 && table_cols > 0 && !table) || (capacity > 0 && !free_pages) ||
+        !n_free || !starts || (total > 0 && (!slots || !positions || !rows)))
+        return FP8MQA_ERR_INVALID_ARG;
+    // rows are written: they may not share memory
+    if (B > 1 && table_stride < table_cols) return FP8MQA_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(table), static_cast<const void*>(lens), static_cast<const void*>(change),
+                          static_cast<const void*>(free_pages), static_cast<const void*>(n_free),
+                          static_cast<const void*>(slots), static_cast<const void*>(positions),
+                          static_cast<const void*>(rows), static_cast<const void*>(starts),
+                          static_cast<const void*>(changed)})
+        if (!on(p, 4)) return FP8MQA_ERR_MISALIGNED;
+    int err = FP8MQA_OK;
+    const PagedDevice* st = paged_device(&err);
+    if (!st) return err;
+    // (what a kernel gets unasked is 48 KB)
+    if (3 * (B + 1) * 4 > 47 * 1024 && !pages_smem()) return launched(cudaErrorInvalidValue);
+    PagesParams p;
+    p.table = table;
+    p.table_stride = table_stride;
+    p.cols = table_cols;
+    p.page_size = page_size;
+    p.by_page = FastDiv(uint32_t(page_size));
+    p.lens = lens;
+    p.change = change;
+    p.B = int32_t(B);
+    p.free_pages = free_pages;
+    p.capacity = int32_t(capacity);
+    p.n_free = n_free;
+    p.total = int32_t(total);
+    p.slots = slots;
+    p.positions = positions;
+    p.rows = rows;
+    p.starts = starts;
+    p.changed = changed;
+    p.bounds = bounds_for(*st);
+    spans(p.bounds, kMemTable, table, extent(B, 4 * table_stride, table_cols, 4, 1, 0, 4));
+    spans(p.bounds, kMemLens, lens, 4 * B);
+    spans(p.bounds, kMemIndices, change, 4 * B);
+    spans(p.bounds, kMemFree, free_pages, 4 * capacity);
+    spans(p.bounds, kMemFreeCount, n_free, 4);
+    spans(p.bounds, kMemSlots, slots, 4 * total);
+    spans(p.bounds, kMemPositions, positions, 4 * total);
+    spans(p.bounds, kMemRows, rows, 4 * total);
+    spans(p.bounds, kMemStarts, starts, 4 * (B + 1));
+    spans(p.bounds, kMemOut, changed, 4 * B);
+    return launched(pages_launch(p, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8_mqa_norm_rotate(const fp8mqa_heads* q, const fp8mqa_heads* k, int32_t x_type, int32_t out_type, int64_t T,
+                        int32_t dim, const void* positions, int32_t position_bytes, const float* inv_freq,
+                        int32_t rotated, int32_t interleaved, float eps, void* stream)
+{
+    using namespace fp8mqa;
+    if (T < 0 || rotated < 0 || (interleaved != 0 && interleaved != 1) || (position_bytes != 4 && position_bytes != 8))
+        return FP8MQA_ERR_INVALID_ARG;
+    if ((x_type != FP8MQA_BF16 && x_type != FP8MQA_F16 && x_type != FP8MQA_F32) ||
+        (out_type != x_type && out_type != FP8MQA_E4M3))
+        return FP8MQA_ERR_INVALID_ARG;
+    if ((dim != 64 && dim != 128) || rotated > dim || rotated % 16 != 0) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
+    int rc = check_heads(q, x_type, out_type);
+    if (rc == FP8MQA_OK && k) rc = check_heads(k, x_type, out_type);
+    if (rc != FP8MQA_OK) return rc;
+    const int64_t heads = int64_t(q->heads) + (k ? k->heads : 0);
+    if (T >= int64_t(1) << 31 || T * heads >= int64_t(1) << 31) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0 || heads == 0) return FP8MQA_OK;
+    if (rotated > 0 && (!positions || !inv_freq)) return FP8MQA_ERR_INVALID_ARG;
+    if (!on(positions, uintptr_t(position_bytes)) || !on(inv_freq, 4)) return FP8MQA_ERR_MISALIGNED;
+    int err = FP8MQA_OK;
+    const PagedDevice* st = paged_device(&err);
+    if (!st) return err;
+    NormRotateParams p = {};
+    p.bounds = bounds_for(*st);
+    const int64_t e = size_of(x_type), eo = size_of(out_type);
+    bool vec = true;
+    for (int i = 0; i < 2; ++i) {
+        const fp8mqa_heads* const h = i ? k : q;
+        if (!h || h->heads == 0) continue;
+        p.x[i] = h->x;
+        p.row_stride[i] = h->row_stride;
+        p.head_stride[i] = h->head_stride;
+        p.weight[i] = h->weight;
+        p.weight_f32[i] = h->weight_type == FP8MQA_F32;
+        p.out[i] = h->out;
+        p.out_row_stride[i] = h->out_row_stride;
+        p.out_head_stride[i] = h->out_head_stride;
+        p.out_scale[i] = h->out_scale;
+        p.heads[i] = h->heads;
+        // strides of dimensions of one are never used
+        const uintptr_t four = uintptr_t(4 * e);
+        vec = vec && on(h->x, four) && (T == 1 || h->row_stride % 4 == 0) && (h->heads == 1 || h->head_stride % 4 == 0);
+        if (out_type != FP8MQA_E4M3)
+            vec = vec && on(h->out, four) && (T == 1 || h->out_row_stride % 4 == 0) &&
+                  (h->heads == 1 || h->out_head_stride % 4 == 0);
+        spans(p.bounds, kMemRows + i, h->x, extent(T, h->row_stride * e, h->heads, h->head_stride * e, 1, 0, dim * e));
+        spans(p.bounds, i ? kMemOut2 : kMemOut, h->out,
+              extent(T, h->out_row_stride * eo, h->heads, h->out_head_stride * eo, 1, 0, dim * eo));
+        spans(p.bounds, i ? kMemOutScale2 : kMemOutScale, h->out_scale, 4 * T * h->heads);
+        spans(p.bounds, kMemWeight + i, h->weight, dim * size_of(h->weight_type));
+    }
+    p.T = T;
+    p.positions = positions;
+    p.wide_positions = position_bytes == 8;
+    p.inv_freq = inv_freq;
+    p.rotated = rotated;
+    p.interleaved = interleaved;
+    p.eps = eps;
+    spans(p.bounds, kMemPositions, positions, rotated > 0 ? T * position_bytes : 0);
+    spans(p.bounds, kMemFreq, inv_freq, 4 * int64_t(rotated / 2));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool e4m3 = out_type == FP8MQA_E4M3;
+    return launched(x_type == FP8MQA_BF16  ? rotate_type<__nv_bfloat16>(p, dim, e4m3, vec, st->sm_count, s)
+                    : x_type == FP8MQA_F16 ? rotate_type<__half>(p, dim, e4m3, vec, st->sm_count, s)
+                                           : rotate_type<float>(p, dim, e4m3, vec, st->sm_count, s));
+}
+
+}  // extern "C"

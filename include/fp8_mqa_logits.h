@@ -273,6 +273,13 @@ FP8MQA_API int fp8_mqa_topk_ex(const float* logits, int64_t M, int64_t N, int64_
  * stands for data * scale.  The strides are free, so keys and values may share one tensor
  * ([pages, 2, page_size, heads, dim]) and heads may come before rows.
  *
+ * An E2M1 cache holds 4 bits a value: byte j of a row's dim / 2 has value 2j in its low half and value
+ * 2j + 1 in its high half, and the data's strides count bytes.  Beside the row's scale there is an E4M3
+ * scale for each 16 values (a group), the dim / 16 bytes of a row at groups + p*group_page_stride +
+ * r*group_row_stride + h*group_head_stride.  A value stands for data * group * scale.  A row of 128 takes
+ * 76 bytes (132 in E4M3).  fp8_mqa_cache_write, fp8_mqa_cache_read and fp8_mqa_attention_paged take such
+ * caches; the indexer's keys stay E4M3.
+ *
  * Position n of sequence b lies in page table[b*table_stride + n / page_size], row
  * n % page_size.  A table entry outside [0, pages) is a page that is not there: its positions
  * are never read.  Table entries past a sequence's length are not read either.
@@ -282,7 +289,8 @@ FP8MQA_API int fp8_mqa_topk_ex(const float* logits, int64_t M, int64_t N, int64_
  * overlaps the end of the kernel before them on the stream; what they read and write is ordered as
  * ever.
  *
- * Limits: dim is 64 or 128; data 16-byte aligned with strides of a multiple of 16 bytes;
+ * Limits: dim is 64 or 128; data 16-byte aligned with strides of a multiple of 16 bytes; groups and
+ * their strides a multiple of dim / 16 bytes;
  * pages * page_size < 2^31; strides are not negative.  Byte offsets are 64-bit throughout;
  * fp8_mqa_attention_paged counts a cache's rows in units of the greatest common divisor of its
  * page and row strides, of which a cache may span up to 2^32 - 2 (64 GB even at 16 bytes).
@@ -293,26 +301,34 @@ FP8MQA_API int fp8_mqa_topk_ex(const float* logits, int64_t M, int64_t N, int64_
 #define FP8MQA_BF16 1
 #define FP8MQA_F16 2
 #define FP8MQA_F32 3
+#define FP8MQA_E2M1 4 /* 4 bits: 0, 0.5, 1, 1.5, 2, 3, 4 and 6 with a sign */
 
 typedef struct fp8mqa_cache {
     void* data;          /* DEVICE */
-    float* scale;        /* DEVICE; NULL unless type is FP8MQA_E4M3 */
+    float* scale;        /* DEVICE; NULL unless type is FP8MQA_E4M3 or FP8MQA_E2M1 */
     int64_t pages;
     int32_t page_size;
     int32_t heads;
     int32_t dim;
-    int32_t type;        /* FP8MQA_E4M3, FP8MQA_BF16 or FP8MQA_F16 */
+    int32_t type;        /* FP8MQA_E4M3, FP8MQA_BF16, FP8MQA_F16 or FP8MQA_E2M1 */
     int64_t page_stride, row_stride, head_stride;                    /* elements of data */
     int64_t scale_page_stride, scale_row_stride, scale_head_stride;  /* elements of scale */
+    /* From here on for FP8MQA_E2M1 alone; with other types these are not read, and need not be there. */
+    uint8_t* groups;     /* DEVICE, E4M3 */
+    int64_t group_page_stride, group_row_stride, group_head_stride;  /* bytes */
 } fp8mqa_cache;
 
 /*
- * fp8_mqa_cache_write -- quantises T token rows and writes them into one or two E4M3 caches.
+ * fp8_mqa_cache_write -- quantises T token rows and writes them into one or two E4M3 or E2M1 caches.
  *
  * For each token t and head h, with x its `dim` values in fp32:
  *     a = max(max_d |x_d|, 1e-30);  data_d = e4m3(x_d * (448 / a));  scale = a * (1 / 448)
- * each step rounded to fp32, e4m3() to the nearest even, within +-448.  A row that holds a NaN
- * or an infinity reads back as NaN, so that it does not pass for data.
+ * each step rounded to fp32, e4m3() to the nearest even, within +-448.  Into E2M1 caches, with m the
+ * largest |x_d| of a group,
+ *     group = e4m3(m * 448 / a);  data_d = e2m1(x_d * 2688 / (group * a));  scale = a * (1 / 2688)
+ * (data_d = 0 where group is 0), where products are rounded to fp32 (they are exact for 16-bit rows) and
+ * quotients are those of an fp32 division; e2m1() to the nearest even, within +-6.  A row that holds a
+ * NaN or an infinity reads back as NaN, so that it does not pass for data.
  *
  *   slots    DEVICE int32 [T]: page * page_size + row.  A slot outside [0, pages * page_size)
  *            is skipped (padding).  Tokens of one call must not share a slot: what such a row
@@ -321,7 +337,7 @@ typedef struct fp8mqa_cache {
  *            t*x_row_stride + h*x_head_stride + d; aligned to its type.
  *   cache    where x goes.
  *   x2, cache2   NULL, or a second tensor (values next to keys) of x's type and its cache,
- *            with cache's page_size, heads and dim and the same slots: one launch writes both.
+ *            with cache's type, page_size, heads and dim and the same slots: one launch writes both.
  * T = 0 enqueues nothing.  No workspace, no allocation; may be captured into a graph.
  */
 FP8MQA_API int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const void* x,
@@ -331,7 +347,7 @@ FP8MQA_API int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_ty
                                    const fp8mqa_cache* cache2, void* stream);
 
 /*
- * fp8_mqa_cache_read -- packs the rows of B sequences, one after the other, out of an E4M3 cache.
+ * fp8_mqa_cache_read -- packs the rows of B sequences, one after the other, out of an E4M3 or E2M1 cache.
  *
  *   table, table_stride, table_cols   DEVICE int32 page table, B rows of table_cols entries.
  *   starts     DEVICE int32 [B + 1], ascending from 0: sequence b's positions 0, 1, ... go to
@@ -340,7 +356,8 @@ FP8MQA_API int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_ty
  *   out        DEVICE [total, heads, dim] of out_type, contiguous, 16-byte aligned:
  *              FP8MQA_E4M3: the stored values, with their scales in out_scale [total, heads]
  *              (with heads = 1 the k_fp8 and kv_scale that fp8_mqa_logits takes);
- *              BF16, F16 or F32: data * scale in fp32, rounded to the type (out_scale is NULL).
+ *              BF16, F16 or F32: data * scale in fp32, rounded to the type (out_scale is NULL);
+ *              the only ones for an E2M1 cache (data * group, which is exact, then * scale).
  * Positions on pages that are not there, or past the table, are zero (and their scale).
  */
 FP8MQA_API int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table,
@@ -386,7 +403,7 @@ FP8MQA_API int fp8_mqa_logits_paged(const uint8_t* q_fp8, const float* w, int64_
  *   q         DEVICE [B, q_heads, dim] of q_type (BF16 or F16), element (b, h, d) at
  *             b*q_row_stride + h*q_head_stride + d; 16-byte aligned, strides too.  q_heads is a
  *             multiple of the cache's heads.
- *   k, v      caches of one type, page_size, heads and dim, over one page table: E4M3, or q's type.
+ *   k, v      caches of one type, page_size, heads and dim, over one page table: E4M3, E2M1, or q's type.
  *   lens      DEVICE int32 [B]; clamped to [0, table_cols * page_size].
  *             table_cols * page_size, or n_indices, is 2^31 - 1025 at most.  The work is laid out
  *             for rows as long as the table is wide: where all are known to be much shorter, a
@@ -416,6 +433,90 @@ FP8MQA_API int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B,
  * capability 10.3).  It does not depend on the rows or their lengths. */
 FP8MQA_API uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int32_t kv_heads,
                                                             int32_t dim);
+
+/* ------------------------------------------------------------------------------------------
+ * A step's other operators: its page tables, and what comes between a layer's projection and
+ * the caches.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * fp8_mqa_pages_update -- changes the lengths of B requests, gives and takes their pages, and says where
+ * their new tokens go.
+ *
+ * Request b of length n holds the pages table[b*table_stride + c], c < ceil(n / page_size).  The pages
+ * that nobody holds are the first *n_free entries of free_pages, a stack.  With to = max(0, lens[b] +
+ * change[b]):
+ *   1. requests with change < 0 shrink; the pages that they need no more go onto the stack, in the order
+ *      of requests and of columns (what does not go into `capacity` entries is dropped);
+ *   2. the others grow; the pages that they need go from the top of the stack into their row, in the same
+ *      order.  A request that needs more than table_cols pages does not fit.  From the first request on
+ *      for which the stack is too short, requests that need new pages do not fit either (those that stay
+ *      on their last page do).  One that does not fit keeps its length and takes nothing;
+ *   3. lens and *n_free are brought up to date.
+ * Table entries past a request's length, and entries of free_pages past *n_free, are left as they are.
+ *
+ *   table       DEVICE int32, written; rows do not overlap (table_stride >= table_cols).
+ *   lens        DEVICE int32 [B], written; values are taken within [0, table_cols * page_size].
+ *   change      DEVICE int32 [B]: 1 or more for a decode step, a prompt chunk's tokens, minus the length
+ *               for a request that ends, minus the drafted tokens that were not accepted, 0 for nothing.
+ *   free_pages, capacity, n_free   DEVICE int32 [capacity], written, and its count, DEVICE int32, written.
+ *   total       rows of the three arrays below; rows past starts[B] are padding, tokens past `total`
+ *               have no row.
+ *   slots       DEVICE int32 [total]: where fp8_mqa_cache_write puts each new token, request after
+ *               request; -1 for those of a request that does not fit, and for padding.
+ *   positions   DEVICE int32 [total]: each new token's position in its request (0 for padding).
+ *   rows        DEVICE int32 [total]: each new token's request (0 for padding).
+ *   starts      DEVICE int32 [B + 1]: request b's new tokens are rows starts[b] .. starts[b + 1] - 1 (sums
+ *               stop at 2^31 - 1).
+ *   changed     DEVICE int32 [B]: by how much the length changed (0 for a request that does not fit).
+ * Limits: B <= 8192 (FP8MQA_ERR_UNSUPPORTED_SHAPE), table_cols * page_size < 2^31.  Arrays do not overlap.
+ * The result is always the same for the same arguments.  No workspace, no allocation; may be captured
+ * into a graph.
+ */
+FP8MQA_API int fp8_mqa_pages_update(int32_t* table, int64_t table_stride, int32_t table_cols,
+                                    int32_t page_size, int32_t* lens, const int32_t* change,
+                                    int64_t B, int32_t* free_pages, int64_t capacity,
+                                    int32_t* n_free, int64_t total, int32_t* slots,
+                                    int32_t* positions, int32_t* rows, int32_t* starts,
+                                    int32_t* changed, void* stream);
+
+/* Rows [T, heads, dim] of a tensor and where their results go; strides in elements. */
+typedef struct fp8mqa_heads {
+    const void* x;        /* DEVICE, aligned to its type */
+    const void* weight;   /* DEVICE [dim], or NULL: rows are not normed */
+    void* out;            /* DEVICE, aligned to its type (E4M3: to 4 bytes, strides too); may be x itself,
+                             with x's strides, where the type is x's */
+    float* out_scale;     /* DEVICE [T, heads] for E4M3 results, else NULL */
+    int64_t row_stride, head_stride;
+    int64_t out_row_stride, out_head_stride;
+    int32_t heads;
+    int32_t weight_type;  /* x's, or FP8MQA_F32 */
+} fp8mqa_heads;
+
+/*
+ * fp8_mqa_norm_rotate -- norms each head of queries and keys and rotates it by its token's position.
+ *
+ *     y = x * (mean_d(x_d^2) + eps)^-1/2 * weight       (y = x without a weight)
+ *     out_a = y_a cos t - y_b sin t,  out_b = y_b cos t + y_a sin t,   t = positions[token] * inv_freq[i]
+ *
+ * for the pairs i < rotated / 2 of the first `rotated` values: (a, b) = (i, i + rotated / 2), or
+ * (2i, 2i + 1) with interleaved = 1; the other values are y.  All in fp32 (t to fp32 precision of a turn at
+ * any position), rounded once to x's type, or to E4M3 with a scale a row as fp8_mqa_cache_write does: the
+ * q_fp8 of fp8_mqa_logits with dim 128, whose scales the caller multiplies into w.  Sums of squares are
+ * fp32 and want values under 10^18.
+ *
+ *   q, k        the tensors; k may be NULL, and heads 0.
+ *   x_type      FP8MQA_BF16, FP8MQA_F16 or FP8MQA_F32, of both.  out_type: x_type or FP8MQA_E4M3.
+ *   dim         64 or 128.  rotated: a multiple of 16, at most dim; 0 only norms.
+ *   positions   DEVICE int32 or int64 [T] (position_bytes 4 or 8); any value, negative ones too.
+ *   inv_freq    DEVICE float32 [rotated / 2], radians a position.
+ * T * (all heads) < 2^31.  No workspace, no allocation; may be captured into a graph.
+ */
+FP8MQA_API int fp8_mqa_norm_rotate(const fp8mqa_heads* q, const fp8mqa_heads* k, int32_t x_type,
+                                   int32_t out_type, int64_t T, int32_t dim,
+                                   const void* positions, int32_t position_bytes,
+                                   const float* inv_freq, int32_t rotated, int32_t interleaved,
+                                   float eps, void* stream);
 
 /* fp8_mqa_logits_strerror -- a static, human-readable name for a status code. */
 FP8MQA_API const char* fp8_mqa_logits_strerror(int status);
