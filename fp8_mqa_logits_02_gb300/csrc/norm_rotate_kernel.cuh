@@ -1,28 +1,44 @@
 // Norms of queries and keys, head by head, with the position rotation in the same pass:
 //
 //   y = x (mean(x^2) + eps)^-1/2 w   for each row x of `dim` values (y = x without a weight w), then
-//   (y_a cos t - y_b sin t, y_b cos t + y_a sin t)   for each pair (a, b) of the first `rotated` values,
+//   (y_u cos t - y_v sin t, y_v cos t + y_u sin t)   for each pair (u, v) of the first `rotated` values,
 //
 // t = position * inv_freq of the pair.  The result is rounded to x's type, or quantised to E4M3 with a
 // scale a row as cache_write does.
 //
-// Bound by the bytes: each value is read and written once, with some 10 instructions a value between.  A
-// row goes to dim / 8 lanes, each with two runs of four values that lie `rotated / 2` apart (side by side
-// for interleaved pairs and past the rotated values), so both values of a pair are in one lane and nothing
-// but the sum of squares (and the largest magnitude) crosses lanes.  Such a group of lanes takes several
-// heads of one token: sine and cosine, and their products with the weights, are made once for them.
+// Bound by the bytes where the instructions allow it: each value is read and written once, but a row of 128
+// takes some 60 warp instructions for two.  A row goes to dim / 8 lanes, each with two runs of four values
+// that lie `rotated / 2` apart (side by side for interleaved pairs and past the rotated values), so both
+// values of a pair are in one lane and nothing but the sum of squares (and the largest magnitude) crosses
+// lanes.  Such a group of lanes takes up to 10 heads (of 16 bits) of one tensor and token, which all come into
+// shared memory at once, and keeps the sines' and cosines' products with the weights in registers; a block's
+// tokens share a table of sines and cosines, made by all of its threads while the rows are on their way.
+//
+// Measured: 16384 tokens x 40 heads of 128 in bfloat16 (336 MB) 53.7 us, 6.2 TB/s of 6.8; with rows loaded straight
+// into registers 82, heads of both tensors in one group 64.  8192 tokens x 32 heads to E4M3 (102 MB) 25.9 us, where
+// the instructions decide (72 % of the issue slots).
 //
 // Far positions: a product position * inv_freq of 10^5 has no correct digit past the fifth in 32 bits.
-// The frequency is taken as a 64-bit fraction of a turn (one fp64 product, correct to 2^-52 of it), so that
-// its product with an integer position wraps around by itself; what is left is under half a turn, exact to
-// 32 bits of it.
+// The frequency is taken as a 64-bit fraction of a turn, so that its product with an integer position wraps
+// around by itself; what is left is under half a turn, exact to 32 bits of it.  (In integers: the fp64 units
+// are few, and made 16384 tokens x 40 heads take 107 us with one product, floor and conversion a pair.)
 #pragma once
 
+#include <type_traits>
+
 #include "paged_common.cuh"
+#include "sm103_ptx.cuh"
 
 namespace fp8mqa {
 
 constexpr int kRotateThreads = 256;
+
+// Heads of a group of lanes, at most, and the shared memory for `rows` of each: with the table, what a kernel gets
+// unasked (48 KB).
+template <class X>
+constexpr int kRotateHeads = 20 / int(sizeof(X));
+template <class X>
+constexpr int rotate_smem(int rows) { return kRotateThreads * 8 * int(sizeof(X)) * rows; }
 
 struct NormRotateParams {
     const void* x[2];
@@ -33,214 +49,284 @@ struct NormRotateParams {
     int64_t out_row_stride[2], out_head_stride[2];
     float* out_scale[2];  // [T, heads], for E4M3
     int32_t heads[2];
-    int32_t units[2];     // of a token's heads of each tensor
-    int32_t per_unit;     // heads
-    FastDiv by_units;     // all units of a token
-    int64_t T;
+    int32_t units[2];     // groups of lanes that a token's heads of each tensor go to,
+    int32_t per_unit;     // so many each
+    FastDiv by_units;     // all of a token
+    int32_t T;
     const void* positions;
     int32_t wide_positions;  // 64 bits
     const float* inv_freq;
-    int32_t rotated, interleaved;
+    int32_t rotated;
     float eps;
     PagedBounds bounds;
 };
 
-// Four values side by side, as floats; kVec: they lie on their own size.
-template <class X, bool kVec>
-__device__ __forceinline__ void load4(const PagedBounds& bounds, int kind, const X* x, float (&v)[4])
+// f radians as a 64-bit fraction of a turn, f = m 2^e / 2 pi with the 24 bits m of f's mantissa: m times
+// round(2^66 / 2 pi), shifted into place, correct to one in its last place or 2^-64 of itself.
+__device__ __forceinline__ uint64_t turn_of(float f)
 {
-    alignas(16) X raw[4];
-    if (!in_bounds(bounds, kind, x, sizeof(raw))) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) raw[j] = from_float<X>(0.0f);
-    } else if constexpr (kVec && sizeof(X) == 4) {
-        *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(x);
-    } else if constexpr (kVec) {
-        *reinterpret_cast<uint2*>(raw) = *reinterpret_cast<const uint2*>(x);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) raw[j] = x[j];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = to_float(raw[j]);
+    constexpr uint64_t kTurn = 0xA2F9836E4E44152AULL;
+    const uint32_t bits = __float_as_uint(f);
+    const int e = int(bits >> 23 & 0xFFu);
+    const uint32_t m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+    const uint64_t lo = m * (kTurn & 0xFFFFFFFFu), mid = m * (kTurn >> 32) + (lo >> 32);
+    // the product, 88 bits, is mid 2^32 + (lo mod 2^32), in units of 2^-s of a place
+    const int s = 152 - max(e, 1);
+    uint64_t turn;
+    if (s >= 32) turn = s < 96 ? mid >> (s - 32) : 0;
+    else if (s >= 0) turn = (mid << (32 - s)) | (uint32_t(lo) >> s);
+    else turn = s > -64 ? ((mid << 32) | uint32_t(lo)) << -s : 0;
+    return bits >> 31 ? 0 - turn : turn;
 }
 
-template <class X, bool kVec>
-__device__ __forceinline__ void store4(const PagedBounds& bounds, int kind, X* to, const float (&v)[4])
+// A lane's eight values of a row, two runs of four.
+template <class X>
+struct alignas(16) Eight {
+    X v[8];
+};
+
+// From shared memory, or (kVec: on 16 bytes) from the weights.  kAside: the second run follows the first.
+template <class X, bool kVec, bool kAside>
+__device__ __forceinline__ Eight<X> load8(const X* a, const X* b)
 {
-    if (!in_bounds(bounds, kind, to, 4 * sizeof(X))) return;
-    alignas(16) X raw[4];
+    Eight<X> r;
+    uint4* const q = reinterpret_cast<uint4*>(&r);
+    if constexpr (!kVec) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) raw[j] = from_float<X>(v[j]);
-    if constexpr (kVec && sizeof(X) == 4) {
-        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(raw);
-    } else if constexpr (kVec) {
-        *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(raw);
+        for (int j = 0; j < 8; ++j) r.v[j] = j < 4 ? a[j] : b[j - 4];
+    } else if constexpr (sizeof(X) == 4) {
+        q[0] = *reinterpret_cast<const uint4*>(a);
+        q[1] = *reinterpret_cast<const uint4*>(b);
+    } else if constexpr (kAside) {
+        q[0] = *reinterpret_cast<const uint4*>(a);
     } else {
+        const uint2 lo = *reinterpret_cast<const uint2*>(a), hi = *reinterpret_cast<const uint2*>(b);
+        q[0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+    return r;
+}
+
+template <class X>
+__device__ __forceinline__ Eight<X> eight_of(const float* y)
+{
+    Eight<X> r;
+    if constexpr (sizeof(X) == 4) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) to[j] = raw[j];
+        for (int j = 0; j < 8; ++j) r.v[j] = y[j];
+    } else {
+        constexpr bool kBf16 = std::is_same_v<X, __nv_bfloat16>;
+        *reinterpret_cast<uint4*>(&r) = make_uint4(pack16<kBf16>(y[0], y[1]), pack16<kBf16>(y[2], y[3]),
+                                                   pack16<kBf16>(y[4], y[5]), pack16<kBf16>(y[6], y[7]));
+    }
+    return r;
+}
+
+template <class X, bool kVec, bool kAside>
+__device__ __forceinline__ void store8(const PagedBounds& bounds, int kind, X* a, X* b, const Eight<X>& r)
+{
+    if (!in_bounds(bounds, kind, a, 4 * sizeof(X)) || !in_bounds(bounds, kind, b, 4 * sizeof(X))) return;
+    const uint4* const q = reinterpret_cast<const uint4*>(&r);
+    if constexpr (!kVec) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) (j < 4 ? a[j] : b[j - 4]) = r.v[j];
+    } else if constexpr (sizeof(X) == 4) {
+        *reinterpret_cast<uint4*>(a) = q[0];
+        *reinterpret_cast<uint4*>(b) = q[1];
+    } else if constexpr (kAside) {
+        *reinterpret_cast<uint4*>(a) = q[0];
+    } else {
+        *reinterpret_cast<uint2*>(a) = make_uint2(q[0].x, q[0].y);
+        *reinterpret_cast<uint2*>(b) = make_uint2(q[0].z, q[0].w);
     }
 }
 
-// X: x's type.  kE4m3: the result is E4M3 with scales, else of x's type.  kVec: x and the result lie on 4 values.
-template <class X, int kDim, bool kE4m3, bool kVec>
-__global__ void __launch_bounds__(kRotateThreads) norm_rotate_kernel(const __grid_constant__ NormRotateParams p)
+// X: x's type.  kE4m3: the result is E4M3 with scales, else of x's type.  kVec: x, its weights and the result lie on
+// 16 bytes (E4M3: on 8).  kInterleaved: how values pair, side by side or apart.
+template <class X, int kDim, bool kE4m3, bool kVec, bool kInterleaved>
+__global__ void __launch_bounds__(kRotateThreads, 4) norm_rotate_kernel(const __grid_constant__ NormRotateParams p)
 {
-    constexpr int kLanes = kDim / 8;
-    const uint32_t unit = blockIdx.x * (kRotateThreads / kLanes) + threadIdx.x / kLanes;  // token and heads
-    const int lane = threadIdx.x % kLanes;
+    constexpr int kLanes = kDim / 8, kGroups = kRotateThreads / kLanes;
+    constexpr int kRows = 2;  // worked on at once
+    extern __shared__ __align__(16) uint8_t s_rows[];  // [group][row][kDim]
+    __shared__ float2 s_turns[kGroups][kDim / 2];      // sine and cosine of the block's tokens
+    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    const int64_t unit0 = int64_t(blockIdx.x) * kGroups;  // the block's first (under 2^31)
     const int units = p.units[0] + p.units[1];
-    const bool there = unit < uint32_t(p.T * units);
-    const int32_t t = there ? p.by_units.of(int32_t(unit)) : 0;
-    int32_t part = there ? int32_t(unit) - t * units : 0;
-    const int which = part >= p.units[0];
-    if (which) part -= p.units[0];
-    const int h0 = part * p.per_unit, h1 = there ? min(h0 + p.per_unit, p.heads[which]) : h0;
+    const int64_t unit = unit0 + group;
+    const bool there = unit < int64_t(p.T) * units;
+    const int32_t t0 = p.by_units.of(int32_t(unit0));     // its token
+    const int32_t t = there ? p.by_units.of(int32_t(unit)) : t0;
+    const int part = int(unit - int64_t(t) * units);      // of the token's units
+    const int which = there && part >= p.units[0];
+    const int h0 = (which ? part - p.units[0] : part) * p.per_unit;
+    const int n = there ? min(p.per_unit, p.heads[which] - h0) : 0;  // heads
 
-    // ---- where the lane's two runs of four values lie; pair j is (a j, b j), or values 2 j and 2 j + 1 of them all
+    // ---- the lane's two runs of four values; for pairs (i, i + rotated / 2) they are as far apart
     const bool turns = 8 * lane < p.rotated;
-    const bool apart = turns && !p.interleaved;
+    const bool apart = !kInterleaved && turns;
     const int at_a = apart ? 4 * lane : 8 * lane, at_b = apart ? p.rotated / 2 + 4 * lane : 8 * lane + 4;
+    using Out = std::conditional_t<kE4m3, uint8_t, X>;
+    X* const s_mine = reinterpret_cast<X*>(s_rows) + group * p.per_unit * kDim;
 
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // ---- the unit's first row (each one is loaded while the one before it is worked on)
-    const X* const x = static_cast<const X*>(p.x[which]) + t * p.row_stride[which];
-    float next_a[4] = {}, next_b[4] = {};
-    auto load = [&](int h) {
-        if (h >= h1) return;
-        load4<X, kVec>(p.bounds, kMemRows + which, x + h * p.head_stride[which] + at_a, next_a);
-        load4<X, kVec>(p.bounds, kMemRows + which, x + h * p.head_stride[which] + at_b, next_b);
-    };
-    load(h0);
 
-    float c[4], s[4];  // of the pairs
+    // ---- the heads come into shared memory, a lane's eight values of each next to those of the lane before
+    {
+        const int64_t step = p.head_stride[which];
+        const X* from = static_cast<const X*>(p.x[which]) + t * p.row_stride[which] + h0 * step + 8 * lane;
+        X* to = s_mine + 8 * lane;
+        for (int i = 0; i < n; ++i, from += step, to += kDim) {
+            const bool ok = in_bounds(p.bounds, kMemRows + which, from, 8 * sizeof(X));
+            if constexpr (kVec) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        c[j] = 1.0f;
-        s[j] = 0.0f;
+                for (int j = 0; j < 8; j += 16 / sizeof(X)) copy16(ptx::smem_addr(to + j), from + j, ok);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) to[j] = ok ? from[j] : from_float<X>(0.0f);
+            }
+        }
+        copy_commit();
     }
-    if (turns && there) {
+
+    // ---- the block's tokens' sines and cosines
+    constexpr int kPairs = kDim / 2;
+    const int pair = threadIdx.x % kPairs;
+    const int64_t unit_end = min(unit0 + kGroups, int64_t(p.T) * units);
+    const int64_t t_end = p.by_units.of(int32_t(unit_end - 1)) + int64_t(1);
+    for (int token = threadIdx.x / kPairs; t0 + token < t_end && 2 * pair < p.rotated; token += kRotateThreads / kPairs) {
         int64_t pos = 0;
         if (p.wide_positions) {
-            const int64_t* const at = static_cast<const int64_t*>(p.positions) + t;
+            const int64_t* const at = static_cast<const int64_t*>(p.positions) + t0 + token;
             if (in_bounds(p.bounds, kMemPositions, at, 8)) pos = *at;
         } else {
-            const int32_t* const at = static_cast<const int32_t*>(p.positions) + t;
+            const int32_t* const at = static_cast<const int32_t*>(p.positions) + t0 + token;
             if (in_bounds(p.bounds, kMemPositions, at, 4)) pos = *at;
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float* const at = p.inv_freq + 4 * lane + j;
-            const double f = in_bounds(p.bounds, kMemFreq, at, 4) ? double(*at) * 0.15915494309189533577 : 0.0;  // turns
-            const uint64_t turn = uint64_t((f - floor(f)) * 18446744073709551616.0);
-            // in halves of a turn, [-1, 1)
-            const float half = float(int32_t((turn * uint64_t(pos)) >> 32)) * 0x1p-31f;
-            sincospif(half, &s[j], &c[j]);
-        }
+        const float* const at = p.inv_freq + pair;
+        const uint64_t turn = in_bounds(p.bounds, kMemFreq, at, 4) ? turn_of(*at) : 0;
+        // in halves of a turn, [-1, 1)
+        const float half = float(int32_t((turn * uint64_t(pos)) >> 32)) * 0x1p-31f;
+        float2 sc;
+        sincospif(half, &sc.x, &sc.y);
+        s_turns[token][pair] = sc;
     }
-    // ---- the pairs' factors: out_a = x_a ca - x_b sb, out_b = x_b cb + x_a sa
-    float ca[4], sa[4], cb[4], sb[4];
+    __syncthreads();
+
+    copy_wait<0>();
+    __syncwarp();
+
+    // ---- the pairs' factors: out_u = u cu - v sv, out_v = v cv + u su, with the weights in them.  Pair j is value
+    // j of either run, or values 2 j and 2 j + 1 of the two runs
+    float cu[4], su[4], cv[4], sv[4];
     const bool norm = p.weight[which] != nullptr;
     {
-        float wa[4] = {1.0f, 1.0f, 1.0f, 1.0f}, wb[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+        float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
         if (norm) {
-            if (p.weight_f32[which]) {
-                load4<float, false>(p.bounds, kMemWeight + which, static_cast<const float*>(p.weight[which]) + at_a, wa);
-                load4<float, false>(p.bounds, kMemWeight + which, static_cast<const float*>(p.weight[which]) + at_b, wb);
-            } else {
-                load4<X, false>(p.bounds, kMemWeight + which, static_cast<const X*>(p.weight[which]) + at_a, wa);
-                load4<X, false>(p.bounds, kMemWeight + which, static_cast<const X*>(p.weight[which]) + at_b, wb);
-            }
-        }
-        if (p.interleaved) {  // pairs (a0, a1), (a2, a3), (b0, b1), (b2, b3): as (a, b) each
-            const float w[8] = {wa[0], wa[1], wa[2], wa[3], wb[0], wb[1], wb[2], wb[3]};
+            const auto values = [&](auto* from) {
+                if (in_bounds(p.bounds, kMemWeight + which, from, kDim * sizeof(*from))) {
+                    using W = std::remove_cv_t<std::remove_pointer_t<decltype(from)>>;
+                    const Eight<W> e = load8<W, kVec, kInterleaved>(from + at_a, from + at_b);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                wa[j] = w[2 * j];
-                wb[j] = w[2 * j + 1];
-            }
+                    for (int j = 0; j < 8; ++j) w[j] = to_float(e.v[j]);
+                }
+            };
+            if (p.weight_f32[which]) values(static_cast<const float*>(p.weight[which]));
+            else values(static_cast<const X*>(p.weight[which]));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            ca[j] = wa[j] * c[j];
-            sa[j] = wa[j] * s[j];
-            cb[j] = wb[j] * c[j];
-            sb[j] = wb[j] * s[j];
+            const float wu = w[kInterleaved ? 2 * j : j], wv = w[kInterleaved ? 2 * j + 1 : 4 + j];
+            const float2 sc = turns ? s_turns[t - t0][4 * lane + j] : make_float2(0.0f, 1.0f);
+            cu[j] = wu * sc.y;
+            su[j] = wu * sc.x;
+            cv[j] = wv * sc.y;
+            sv[j] = wv * sc.x;
         }
     }
 
-    // all lanes of a warp go round together (they exchange sums); a group past its end does nothing
-    for (int i = 0; i < p.per_unit; ++i) {
-        const int h = h0 + i;
-        const bool mine = h < h1;
-        float a[4], b[4];
+    // ---- the heads, all lanes of a warp together (they exchange sums): a group past its last one does nothing
+    const int64_t out_step = p.out_head_stride[which];
+    Out* out = static_cast<Out*>(p.out[which]) + t * p.out_row_stride[which] + h0 * out_step;
+    float* out_scale = kE4m3 ? p.out_scale[which] + int64_t(t) * p.heads[which] + h0 : nullptr;
+    const X* row = s_mine;
+    for (int i = 0; i < p.per_unit; i += kRows, row += kRows * kDim) {
+        float y[kRows][8], by[kRows], top[kRows];  // y: as it lies in the runs
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            a[j] = next_a[j];
-            b[j] = next_b[j];
-        }
-        load(h + 1);
-        float by = 1.0f;
-        float sum = 0.0f;
+        for (int r = 0; r < kRows; ++r) {
+            const X* const from = i + r < n ? row + r * kDim : row;
+            const Eight<X> raw = load8<X, true, kInterleaved>(from + at_a, from + at_b);
+            by[r] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum = fmaf(a[j], a[j], fmaf(b[j], b[j], sum));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
-        if (norm) by = rsqrtf(fmaf(sum, 1.0f / kDim, p.eps));
-        if (p.interleaved) {
-            const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                a[j] = v[2 * j];
-                b[j] = v[2 * j + 1];
+            for (int j = 0; j < 8; ++j) {
+                y[r][j] = to_float(raw.v[j]);
+                by[r] = fmaf(y[r][j], y[r][j], by[r]);
             }
         }
-        float ya[4], yb[4];
+        if (norm) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            // (values that do not turn have nothing to do with one another: b may be infinite)
-            ya[j] = by * (turns ? a[j] * ca[j] - b[j] * sb[j] : a[j] * ca[j]);
-            yb[j] = by * (turns ? b[j] * cb[j] + a[j] * sa[j] : b[j] * cb[j]);
+            for (int o = kLanes / 2; o > 0; o /= 2)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) by[r] += __shfl_xor_sync(~0u, by[r], o);
         }
-        if (p.interleaved) {
-            const float v[8] = {ya[0], yb[0], ya[1], yb[1], ya[2], yb[2], ya[3], yb[3]};
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            by[r] = norm ? rsqrtf(fmaf(by[r], 1.0f / kDim, p.eps)) : 1.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                ya[j] = v[j];
-                yb[j] = v[4 + j];
+                float &u = y[r][kInterleaved ? 2 * j : j], &v = y[r][kInterleaved ? 2 * j + 1 : 4 + j];
+                float nu = u * cu[j], nv = v * cv[j];
+                if (turns) {  // (others have nothing to do with one another: one may be infinite)
+                    nu = fmaf(-v, sv[j], nu);
+                    nv = fmaf(u, su[j], nv);
+                }
+                u = nu * by[r];
+                v = nv * by[r];
             }
         }
-        const int64_t to = t * p.out_row_stride[which] + h * p.out_head_stride[which];
         if constexpr (kE4m3) {
-            float top = kTinyMax;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = max_nan(top, max_nan(fabsf(ya[j]), fabsf(yb[j])));
+            for (int r = 0; r < kRows; ++r) {
+                top[r] = kTinyMax;
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o /= 2) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
-            const float inv = __fdiv_rn(kE4m3Max, top);
-            auto pack = [&](const float (&y)[4]) {
-                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(y[0], inv), __fmul_rn(y[1], inv)),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(y[2], inv), __fmul_rn(y[3], inv)),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                return lo | hi << 16;
-            };
-            if (mine) {
-                uint8_t* const out = static_cast<uint8_t*>(p.out[which]) + to;
-                const int kind = which ? kMemOut2 : kMemOut;
-                if (in_bounds(p.bounds, kind, out + at_a, 4)) *reinterpret_cast<uint32_t*>(out + at_a) = pack(ya);
-                if (in_bounds(p.bounds, kind, out + at_b, 4)) *reinterpret_cast<uint32_t*>(out + at_b) = pack(yb);
-                float* const scale = p.out_scale[which] + int64_t(t) * p.heads[which] + h;
-                if (lane == 0 && in_bounds(p.bounds, which ? kMemOutScale2 : kMemOutScale, scale, 4))
-                    *scale = __fmul_rn(top, 1.0f / kE4m3Max);
+                for (int j = 0; j < 8; ++j) top[r] = max_nan(top[r], fabsf(y[r][j]));
             }
-        } else if (mine) {
-            X* const out = static_cast<X*>(p.out[which]) + to;
-            store4<X, kVec>(p.bounds, which ? kMemOut2 : kMemOut, out + at_a, ya);
-            store4<X, kVec>(p.bounds, which ? kMemOut2 : kMemOut, out + at_b, yb);
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o /= 2)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) top[r] = max_nan(top[r], __shfl_xor_sync(~0u, top[r], o));
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            if (i + r >= n) break;
+            const int kind = which ? kMemOut2 : kMemOut;
+            if constexpr (kE4m3) {
+                const float inv = __fdiv_rn(kE4m3Max, top[r]);
+                uint32_t four[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float* const z = y[r] + 4 * j;
+                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+                        make_float2(__fmul_rn(z[0], inv), __fmul_rn(z[1], inv)), __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+                        make_float2(__fmul_rn(z[2], inv), __fmul_rn(z[3], inv)), __NV_SATFINITE, __NV_E4M3);
+                    four[j] = lo | hi << 16;
+                }
+                if constexpr (kVec && kInterleaved) {
+                    if (in_bounds(p.bounds, kind, out + at_a, 8))
+                        *reinterpret_cast<uint2*>(out + at_a) = make_uint2(four[0], four[1]);
+                } else {
+                    if (in_bounds(p.bounds, kind, out + at_a, 4)) *reinterpret_cast<uint32_t*>(out + at_a) = four[0];
+                    if (in_bounds(p.bounds, kind, out + at_b, 4)) *reinterpret_cast<uint32_t*>(out + at_b) = four[1];
+                }
+                if (lane == 0 && in_bounds(p.bounds, which ? kMemOutScale2 : kMemOutScale, out_scale, 4))
+                    *out_scale = __fmul_rn(top[r], 1.0f / kE4m3Max);
+                ++out_scale;
+            } else {
+                store8<X, kVec, kInterleaved>(p.bounds, kind, out + at_a, out + at_b, eight_of<X>(y[r]));
+            }
+            out += out_step;
         }
     }
 }
-
 }  // namespace fp8mqa

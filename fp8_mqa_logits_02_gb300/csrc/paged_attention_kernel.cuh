@@ -165,18 +165,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two floats as 16-bit halves, the first one low.
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi)
-{
-    uint32_t r;
-    if constexpr (kBf16)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Where piece c of row r lies in a stage.  A fragment read of K takes four pieces of two rows in
 // a phase, one of V two pieces of every second of eight rows.
 template <int kPieces>

@@ -196,6 +196,18 @@ __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
 
+// Two floats as 16-bit halves, the first one low.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (kBf16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // The larger of two, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b)
 {

@@ -43,29 +43,40 @@ bool pages_smem()
                                 int(3 * (kPagesMaxRows + 1) * sizeof(int32_t))) == cudaSuccess;
 }
 
-template <class X, int kDim, bool kE4m3>
+template <class X, int kDim, bool kE4m3, bool kInterleaved>
 cudaError_t rotate_launch(NormRotateParams& p, bool vec, int sm_count, cudaStream_t s)
 {
-    // Heads that a group of lanes takes: sine and cosine are made once for them, but there should be
-    // groups for every SM.
-    constexpr int64_t kGroups = kRotateThreads / (kDim / 8);
-    const int64_t rows = p.T * (int64_t(p.heads[0]) + p.heads[1]);
-    const int64_t most = std::max(p.heads[0], p.heads[1]);
-    p.per_unit = int32_t(std::clamp<int64_t>(rows / (kGroups * 4 * sm_count), 1, std::min<int64_t>(8, most)));
+    // As many heads to a group of lanes as there is room for, shared out evenly, since their factors are made once;
+    // fewer where that leaves SMs without work.
+    constexpr int kGroups = kRotateThreads / (kDim / 8);
+    const int most = std::max(p.heads[0], p.heads[1]);
+    int parts = (most + kRotateHeads<X> - 1) / kRotateHeads<X>;
+    auto units = [&] { return (int64_t(p.heads[0]) + p.per_unit - 1) / p.per_unit + (p.heads[1] + p.per_unit - 1) / p.per_unit; };
+    for (p.per_unit = (most + parts - 1) / parts; p.per_unit > 1 && p.T * units() < int64_t(kGroups) * 2 * sm_count;)
+        p.per_unit = (p.per_unit + 1) / 2;
     for (int i = 0; i < 2; ++i) p.units[i] = (p.heads[i] + p.per_unit - 1) / p.per_unit;
-    const int64_t units = int64_t(p.units[0]) + p.units[1];
-    p.by_units = FastDiv(uint32_t(units));
-    const dim3 grid(unsigned((p.T * units + kGroups - 1) / kGroups));
-    return vec ? launch_after(norm_rotate_kernel<X, kDim, kE4m3, true>, grid, kRotateThreads, 0, s, p)
-               : launch_after(norm_rotate_kernel<X, kDim, kE4m3, false>, grid, kRotateThreads, 0, s, p);
+    p.by_units = FastDiv(uint32_t(units()));
+    const size_t smem = size_t(rotate_smem<X>(p.per_unit));
+    const dim3 grid(unsigned((p.T * units() + kGroups - 1) / kGroups));
+    return vec ? launch_after(norm_rotate_kernel<X, kDim, kE4m3, true, kInterleaved>, grid, kRotateThreads, smem, s, p)
+               : launch_after(norm_rotate_kernel<X, kDim, kE4m3, false, kInterleaved>, grid, kRotateThreads, smem, s, p);
+}
+
+template <class X, int kDim>
+cudaError_t rotate_dim(NormRotateParams& p, bool interleaved, bool e4m3, bool vec, int sm_count, cudaStream_t s)
+{
+    if (interleaved)
+        return e4m3 ? rotate_launch<X, kDim, true, true>(p, vec, sm_count, s)
+                    : rotate_launch<X, kDim, false, true>(p, vec, sm_count, s);
+    return e4m3 ? rotate_launch<X, kDim, true, false>(p, vec, sm_count, s)
+                : rotate_launch<X, kDim, false, false>(p, vec, sm_count, s);
 }
 
 template <class X>
-cudaError_t rotate_type(NormRotateParams& p, int32_t dim, bool e4m3, bool vec, int sm_count, cudaStream_t s)
+cudaError_t rotate_type(NormRotateParams& p, int32_t dim, bool interleaved, bool e4m3, bool vec, int sm_count, cudaStream_t s)
 {
-    if (dim == 64)
-        return e4m3 ? rotate_launch<X, 64, true>(p, vec, sm_count, s) : rotate_launch<X, 64, false>(p, vec, sm_count, s);
-    return e4m3 ? rotate_launch<X, 128, true>(p, vec, sm_count, s) : rotate_launch<X, 128, false>(p, vec, sm_count, s);
+    return dim == 64 ? rotate_dim<X, 64>(p, interleaved, e4m3, vec, sm_count, s)
+                     : rotate_dim<X, 128>(p, interleaved, e4m3, vec, sm_count, s);
 }
 
 int check_heads(const fp8mqa_heads* h, int32_t x_type, int32_t out_type)
@@ -184,31 +195,31 @@ int fp8_mqa_norm_rotate(const fp8mqa_heads* q, const fp8mqa_heads* k, int32_t x_
         p.out_scale[i] = h->out_scale;
         p.heads[i] = h->heads;
         // strides of dimensions of one are never used
-        const uintptr_t four = uintptr_t(4 * e);
-        vec = vec && on(h->x, four) && (T == 1 || h->row_stride % 4 == 0) && (h->heads == 1 || h->head_stride % 4 == 0);
-        if (out_type != FP8MQA_E4M3)
-            vec = vec && on(h->out, four) && (T == 1 || h->out_row_stride % 4 == 0) &&
-                  (h->heads == 1 || h->out_head_stride % 4 == 0);
+        auto lies = [&](const void* at, int64_t row, int64_t head, int64_t size, uintptr_t bytes) {
+            return on(at, bytes) && (T == 1 || row * size % int64_t(bytes) == 0) &&
+                   (h->heads == 1 || head * size % int64_t(bytes) == 0);
+        };
+        vec = vec && on(h->weight, 16) && lies(h->x, h->row_stride, h->head_stride, e, 16) &&
+              lies(h->out, h->out_row_stride, h->out_head_stride, eo, out_type == FP8MQA_E4M3 ? 8 : 16);
         spans(p.bounds, kMemRows + i, h->x, extent(T, h->row_stride * e, h->heads, h->head_stride * e, 1, 0, dim * e));
         spans(p.bounds, i ? kMemOut2 : kMemOut, h->out,
               extent(T, h->out_row_stride * eo, h->heads, h->out_head_stride * eo, 1, 0, dim * eo));
         spans(p.bounds, i ? kMemOutScale2 : kMemOutScale, h->out_scale, 4 * T * h->heads);
         spans(p.bounds, kMemWeight + i, h->weight, dim * size_of(h->weight_type));
     }
-    p.T = T;
+    p.T = int32_t(T);
     p.positions = positions;
     p.wide_positions = position_bytes == 8;
     p.inv_freq = inv_freq;
     p.rotated = rotated;
-    p.interleaved = interleaved;
     p.eps = eps;
     spans(p.bounds, kMemPositions, positions, rotated > 0 ? T * position_bytes : 0);
     spans(p.bounds, kMemFreq, inv_freq, 4 * int64_t(rotated / 2));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool e4m3 = out_type == FP8MQA_E4M3;
-    return launched(x_type == FP8MQA_BF16  ? rotate_type<__nv_bfloat16>(p, dim, e4m3, vec, st->sm_count, s)
-                    : x_type == FP8MQA_F16 ? rotate_type<__half>(p, dim, e4m3, vec, st->sm_count, s)
-                                           : rotate_type<float>(p, dim, e4m3, vec, st->sm_count, s));
+    return launched(x_type == FP8MQA_BF16  ? rotate_type<__nv_bfloat16>(p, dim, interleaved, e4m3, vec, st->sm_count, s)
+                    : x_type == FP8MQA_F16 ? rotate_type<__half>(p, dim, interleaved, e4m3, vec, st->sm_count, s)
+                                           : rotate_type<float>(p, dim, interleaved, e4m3, vec, st->sm_count, s));
 }
 
 }  // extern "C"
