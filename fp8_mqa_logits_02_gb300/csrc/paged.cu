@@ -177,12 +177,13 @@ PagedView view_of(const fp8mqa_cache& c, const void* valid)
     return v;
 }
 
-// The units that a cache's rows are counted in; false if 32 bits do not hold them.
-bool row_units(const PagedView& v, RowUnits* u)
+// The units that something of a cache's rows is counted in, from the strides of its pages and rows and the
+// least unit; false if 32 bits do not hold them.
+bool row_units(const PagedView& v, int64_t page_stride, int64_t row_stride, int64_t least, RowUnits* u)
 {
     // strides of dimensions of one do not count; negative ones are not taken
-    const int64_t page = v.pages > 1 ? v.page_stride : 0, row = v.page_size > 1 ? v.row_stride : 0;
-    const int64_t unit = std::max<int64_t>(16, std::gcd(page, row));
+    const int64_t page = v.pages > 1 ? page_stride : 0, row = v.page_size > 1 ? row_stride : 0;
+    const int64_t unit = std::max<int64_t>(least, std::gcd(page, row));
     if (page < 0 || row < 0 || unit > INT32_MAX ||
         (v.pages * page + v.page_size * row) / unit >= int64_t(kNoRow))
         return false;
@@ -191,6 +192,9 @@ bool row_units(const PagedView& v, RowUnits* u)
     u->unit = uint32_t(unit);
     return true;
 }
+bool row_units(const PagedView& v, RowUnits* u) { return row_units(v, v.page_stride, v.row_stride, 16, u); }
+
+bool alike(const RowUnits& a, const RowUnits& b) { return a.page == b.page && a.row == b.row && a.unit == b.unit; }
 
 void spans(PagedBounds& b, int which, const PagedView& c, const fp8mqa_cache& arg)
 {
@@ -608,6 +612,19 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
     if (!row_units(p.k, &p.k_units) || !row_units(p.v, &p.v_units))
         return FP8MQA_ERR_UNSUPPORTED_SHAPE;
     p.same_rows = p.k_units.page == p.v_units.page && p.k_units.row == p.v_units.row;
+    if (k->type == FP8MQA_E2M1) {
+        auto units = [](const PagedView& c, RowUnits* group, RowUnits* scale) {
+            return row_units(c, c.group_page_stride, c.group_row_stride, 1, group) &&
+                   row_units(c, c.scale_page_stride, c.scale_row_stride, 1, scale);
+        };
+        if (!units(p.k, &p.k_group_units, &p.k_scale_units) || !units(p.v, &p.v_group_units, &p.v_scale_units))
+            return FP8MQA_ERR_UNSUPPORTED_SHAPE;
+        p.same_rows = alike(p.k_units, p.v_units) && alike(p.k_group_units, p.v_group_units) &&
+                      alike(p.k_scale_units, p.v_scale_units);
+        // (a step is 32 positions, and begins at a multiple of that)
+        p.whole_steps = n_indices < 0 && k->page_size % 32 == 0 &&
+                        p.k.row_stride < INT32_MAX / k->page_size && p.v.row_stride < INT32_MAX / k->page_size;
+    }
     p.table = {table, table_stride, table_cols, FastDiv(uint32_t(k->page_size))};
     p.lens = lens;
     p.indices = indices;

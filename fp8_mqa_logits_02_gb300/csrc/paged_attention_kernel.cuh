@@ -47,179 +47,352 @@
 // workspace, and a second kernel joins them, always in the same order.
 #pragma once
 
-#include <math_constants.h>
-
-#include "paged_common.cuh"
-#include "sm103_ptx.cuh"
+#include "paged_attention4.cuh"
+#include "paged_attention_common.cuh"
 
 namespace fp8mqa {
 
-constexpr int kAttnThreads = 128, kAttnWarps = kAttnThreads / 32;
-// Steps in a ring, for each warp that shares it, and CTAs of an SM: what fills the shared memory.  Three
-// steps and two CTAs take as long on the ragged batch and 5 % longer on selected positions.
-constexpr int kAttnStages = 2;
-constexpr int kAttnStages4 = 3;  // of E2M1 caches, whose steps are half as large
-constexpr int kAttnCtasPerSm = 3;
-constexpr int kAttnMaxCtas = 512;  // of one launch
-constexpr int64_t kAttnMaxPositions = INT32_MAX - 1024;  // of a row
-
-// Powers of two: how far the weights' reference may lag behind the largest score, and what the reference
-// counts for in f16 weights; together they keep to f16's range (2^15 < 65504).
-constexpr float kAttnLag = 8.0f;
-constexpr float kAttnLift = 7.0f;
-
-// What CTA `me` of a chunk (me > 0) says of the row that its share begins within: the row's parts
-// are those of CTAs first .. first + parts - 1.  parts = 0: its share begins with a row.
-struct AttnSplit {
-    int64_t row;
-    int32_t first, parts, first_slot, pad[3];
-};
-
-struct PagedAttentionParams {
-    const void* q;
-    int64_t q_row_stride, q_head_stride;  // elements
-    PagedView k, v;
-    RowUnits k_units, v_units;
-    int32_t same_rows;  // k_units and v_units are alike
-    int32_t hw;         // key heads that a CTA's warps take: 1 or 2
-    PageTable table;
-    const int32_t* lens;
-    const int32_t* indices;
-    int64_t indices_stride;
-    int32_t n_indices;  // -1: every position
-    int32_t q_heads;
-    int32_t q_bf16;
-    int64_t B;
-    float sm_scale;
-    void* out;
-    float* lse;
-    float* partial;  // [2 * CTAs][heads of a CTA][dim], then m and l [2 * CTAs][heads of a CTA][2]
-    AttnSplit* splits;  // [CTAs of a chunk]
-    PagedBounds bounds;
-};
-
-// kType: FP8MQA_E4M3, FP8MQA_BF16, FP8MQA_F16 or FP8MQA_E2M1 of the cache.  kNT: eights of heads of a warp.
-// kHq: warps that share a ring, for 8 kNT heads each of one key head.
-template <int kType, int kDim_, int kNT_, int kHq>
-struct AttnShape {
-    static constexpr bool kE4m3 = kType == 0, kBf16 = kType == 1, kE2m1 = kType == 4;
-    static constexpr bool kScaled = kE4m3 || kE2m1;    // rows have scales
-    static constexpr int kDim = kDim_, kNT = kNT_;
-    static constexpr int kHeads = 8 * kNT;             // heads of a warp
-    static constexpr int kStages = (kE2m1 ? kAttnStages4 : kAttnStages) * kHq;
-    static constexpr int kStep = kScaled ? 32 : 16;    // positions of a warp's step
-    static constexpr int kBlocks = kStep / 16;         // of 16 positions
-    static constexpr int kRowBytes = kE2m1 ? kDim / 2 : kDim * (kE4m3 ? 1 : 2);
-    static constexpr int kGroupBytes = kE2m1 ? kDim / kGroup : 0;  // of a row
-    static constexpr int kPieces = kRowBytes / 16;
-    static constexpr int kKRows = kStep / 8;           // rows of S^T a lane has
-    static constexpr int kVWords = kRowBytes / 32;     // words of a V row a lane has
-    static constexpr int kMT = kDim / 16;              // 16-blocks of dim
-    // a ring stage: K rows, V rows, their scales, their groups' scales, and which rows are there
-    static constexpr int kRows = kStep * kRowBytes;
-    static constexpr int kScales = 2 * kRows, kGroups = kScales + (kScaled ? 2 * kStep * 4 : 0);
-    static constexpr int kThere = kGroups + 2 * kStep * kGroupBytes;
-    static constexpr int kStage = (kThere + 16 + 127) / 128 * 128;
-    static constexpr int kRing = kStages * kStage;
-    static constexpr int kSmem = kAttnWarps / kHq * kRing;
-    // a warp's results take the place of its share of the rings
-    static constexpr int kResult = kRing / kHq;
-    static constexpr int kPitch = kDim + 4;            // floats from head to head: fewer bank conflicts
-    static_assert(kHeads * kPitch * 4 <= kResult && kResult % 16 == 0, "room for the results");
-};
-
-__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+// The steps over a 16-bit or E4M3 cache: a warp's tiles of a row, from its ring into sums.
+template <class S>
+__device__ __forceinline__ void attn_steps(const PagedAttentionParams& p, const AttnRows& rows, const AttnPart& part,
+                                           uint8_t* ring, AttnSums<S>& sums)
 {
-    uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
-}
+    constexpr int kDim = S::kDim, kNT = S::kNT, kHq = S::kHq;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int64_t b = part.b;
+    const int32_t lo = part.lo, hi = part.hi, tile = part.tile;
+    const int h0 = part.h0, n_heads = part.n_heads, kvh = part.kvh, hw = part.hw, side = hw * kHq;
+    const int32_t count = rows.count(b), len = rows.length(b);
+    const uint32_t ring_at = ptx::smem_addr(ring);
 
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ float log2_fast(float x)
-{
-    float r;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-template <bool kBf16>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    if constexpr (kBf16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Where piece c of row r lies in a stage.  A fragment read of K takes four pieces of two rows in
-// a phase, one of V two pieces of every second of eight rows.
-template <int kPieces>
-__device__ __forceinline__ int k_place(int r, int c)
-{
-    return r * kPieces + (kPieces >= 8 ? c ^ ((r & 1) << 2) : c);
-}
-template <int kPieces>
-__device__ __forceinline__ int v_place(int r, int c)
-{
-    return r * kPieces + (kPieces >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
-}
-// The same for E2M1 rows of 64 or 32 bytes, of which a lane takes 8 or 4 (a read of V takes them of every
-// second of eight rows): rows change places, so that those four rows fill the banks.
-template <int kPieces>
-__device__ __forceinline__ int v_place4(int r, int c)
-{
-    return kPieces == 4 ? ((r & ~3) | (r & 1) << 1 | (r >> 1 & 1)) * 4 + (c ^ (r >> 1 & 2))
-                        : ((r & ~7) | (r & 1) << 2 | (r >> 1 & 3)) * 2 + c;
-}
-
-// The rows' positions and tiles.
-struct AttnRows {
-    const PagedAttentionParams& p;
-    int64_t cap;
-    int32_t tile;  // positions
-    __device__ int32_t count(int64_t b) const
-    {
-        if (p.n_indices >= 0) return p.n_indices;
-        return length(b);
+    // ---- Q: the words of this lane's columns, two values each
+    uint32_t qf[kNT][S::kMT][2];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+        const int h = nt * 8 + g;
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.q_row_stride +
+                            int64_t(h0 + h) * p.q_head_stride;
+        // word w = 2 s + j (columns of fragment s) is word w % kRun of the run w / kRun of words that
+        // lie together, as in the cache's rows: 16 values of 64, or 8 of 32
+        constexpr int kRun = S::kE4m3 ? 8 : 4;
+#pragma unroll
+        for (int w = 0; w < 2 * S::kMT; w += 4) {
+            const int d = w / kRun * (8 * kRun) + t * (2 * kRun) + w % kRun * 2;
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (h < n_heads && in_bounds(p.bounds, kMemQ, q + d, 16))
+                x = *(reinterpret_cast<const uint4*>(q + d));
+            qf[nt][w / 2][0] = x.x;
+            qf[nt][w / 2][1] = x.y;
+            qf[nt][w / 2 + 1][0] = x.z;
+            qf[nt][w / 2 + 1][1] = x.w;
+        }
     }
-    __device__ int32_t length(int64_t b) const
-    {
-        const int64_t n = in_bounds(p.bounds, kMemLens, p.lens + b, 4) ? p.lens[b] : 0;
-        return int32_t(n < 0 ? 0 : n < cap ? n : cap);
-    }
-    // a row with nothing still has one tile, which writes its empty result
-    __device__ int32_t tiles(int64_t b) const { return max(1, (count(b) + tile - 1) / tile); }
-};
 
-// Writes float4 number i of a head's result, given the running maximum and sum.
-template <int kDim>
-__device__ __forceinline__ void attn_store(const PagedAttentionParams& p, int64_t head, int i,
-                                           float top, float sum, float4 v)
-{
-    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-    uint2 two;
-    if (p.q_bf16)
-        two = make_uint2(pack16<true>(v.x * inv, v.y * inv), pack16<true>(v.z * inv, v.w * inv));
-    else
-        two = make_uint2(pack16<false>(v.x * inv, v.y * inv), pack16<false>(v.z * inv, v.w * inv));
-    uint2* const to = static_cast<uint2*>(p.out) + head * (kDim / 4) + i;
-    if (in_bounds(p.bounds, kMemOut, to, 8)) *to = two;
-    if (p.lse && i == 0 && in_bounds(p.bounds, kMemOutScale, p.lse + head, 4))
-        p.lse[head] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * 0.6931471805599453f;
+    // ---- a step's rows: lane i finds position i of a step, a step ahead of its copies
+    const uint8_t* const k_base = p.k.data + kvh * p.k.head_stride;
+    const uint8_t* const v_base = p.v.data + kvh * p.v.head_stride;
+    const int32_t step_end = min(count, hi * tile);
+    const int mine = lane % S::kStep;
+    // (two steps ahead what `indices` says: its load, the table's and the rows' copies hang on
+    // one another, and nothing looks at what a load brings before the next one needs it)
+    int32_t page = -1, row = 0, listed = -1;
+    auto list = [&](int32_t i) {
+        listed = -1;
+        if (p.n_indices >= 0 && i + mine < step_end) {
+            const int32_t* const at = p.indices + b * p.indices_stride + i + mine;
+            if (in_bounds(p.bounds, kMemIndices, at, 4)) listed = *at;
+        }
+    };
+    auto find = [&](int32_t i) {  // i: the step's first place in the row's list
+        const int32_t n = p.n_indices >= 0 ? listed : i + mine;
+        page = -1;
+        if (i + mine < step_end && n >= 0 && n < len) {
+            const int32_t col = p.table.by_page.of(n);
+            row = n - col * p.k.page_size;
+            const int32_t* const at = p.table.ids + b * p.table.stride + col;
+            if (in_bounds(p.bounds, kMemTable, at, 4)) page = *at;
+        }
+        list(i + tile);
+    };
+    auto copy = [&](int stage) {  // the rows that find() found
+        const bool there = uint32_t(page) < uint32_t(p.k.pages);
+        const uint32_t k_at = there ? page * p.k_units.page + row * p.k_units.row : kNoRow;
+        const uint32_t v_at = there ? page * p.v_units.page + row * p.v_units.row : kNoRow;
+        const uint32_t to = ring_at + stage * S::kStage;
+        constexpr int kPer = 32 / S::kPieces;  // rows in one instruction
+        const int c = lane % S::kPieces;
+#pragma unroll
+        for (int j = 0; j < S::kStep / kPer / kHq; ++j) {
+            const int r = (j * kHq + warp % kHq) * kPer + lane / S::kPieces;
+            const uint32_t at = __shfl_sync(~0u, k_at, r);
+            const uint32_t at2 = p.same_rows ? at : __shfl_sync(~0u, v_at, r);
+            const bool ok = at != kNoRow;
+            auto k_from = [&] { return k_base + uint64_t(ok ? at : 0) * p.k_units.unit + 16 * c; };
+            auto v_from = [&] { return v_base + uint64_t(ok ? at2 : 0) * p.v_units.unit + 16 * c; };
+            copy16(to + 16 * k_place<S::kPieces>(r, c), k_from(),
+                   ok && in_bounds(p.bounds, kMemData, k_from(), 16));
+            copy16(to + S::kRows + 16 * v_place<S::kPieces>(r, c), v_from(),
+                   ok && in_bounds(p.bounds, kMemData2, v_from(), 16));
+        }
+        if (S::kE4m3 && warp % kHq == 0) {
+            const int64_t pg = there ? page : 0, rw = there ? row : 0;
+            const float* const k_from = p.k.scale + pg * p.k.scale_page_stride +
+                                        rw * p.k.scale_row_stride + kvh * p.k.scale_head_stride;
+            const float* const v_from = p.v.scale + pg * p.v.scale_page_stride +
+                                        rw * p.v.scale_row_stride + kvh * p.v.scale_head_stride;
+            copy4(to + S::kScales + 4 * lane, k_from, there && in_bounds(p.bounds, kMemScale, k_from, 4));
+            copy4(to + S::kScales + 4 * (S::kStep + lane), v_from,
+                  there && in_bounds(p.bounds, kMemScale2, v_from, 4));
+        }
+        const uint32_t here = __ballot_sync(~0u, there);
+        if (lane == 0 && warp % kHq == 0)
+            *reinterpret_cast<uint32_t*>(ring + stage * S::kStage + S::kThere) = here;
+    };
+
+    int32_t i0 = lo * tile + warp / side * S::kStep;  // the step being computed
+    int32_t ahead = i0;                               // the step that find() found
+    list(ahead);
+    find(ahead);
+#pragma unroll 1
+    for (int j = 0; j < S::kStages - 1; ++j) {
+        if (ahead < step_end) {
+            copy(j);
+            find(ahead += tile);
+        }
+        copy_commit();
+    }
+
+    // ---- Q as B fragments, and each head's factor of the scores (in powers of two)
+    float factor[kNT][2];
+    auto &m = sums.m, &l = sums.l, &w_top = sums.w_top;
+    auto& o = sums.o;
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+        float by = 1.0f;
+        if (S::kE4m3 && p.q_bf16) {
+            // bfloat16 -> f16: exact but for the range, so each head is brought to a largest
+            // magnitude of 2^12 .. 2^13 by a power of two (what then falls below f16's range
+            // is under 2^-36 of the largest)
+            float top = 0.0f;
+#pragma unroll
+            for (int s = 0; s < S::kMT; ++s)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    top = fmaxf(top, fabsf(__uint_as_float(qf[nt][s][j] << 16)));
+                    top = fmaxf(top, fabsf(__uint_as_float(qf[nt][s][j] & 0xFFFF0000u)));
+                }
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            const int e = min(max(int(__float_as_uint(top) >> 23), 20), 240) - 139;
+            const float down = __uint_as_float(uint32_t(127 - e) << 23);
+            by = __uint_as_float(uint32_t(127 + e) << 23);
+#pragma unroll
+            for (int s = 0; s < S::kMT; ++s)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    qf[nt][s][j] =
+                        pack16<false>(__uint_as_float(qf[nt][s][j] << 16) * down,
+                                      __uint_as_float(qf[nt][s][j] & 0xFFFF0000u) * down);
+        }
+        const float c = p.sm_scale * 1.4426950408889634f * by;
+        factor[nt][0] = __shfl_sync(~0u, c, 8 * t);
+        factor[nt][1] = __shfl_sync(~0u, c, 8 * t + 4);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            m[nt][j] = w_top[nt][j] = -CUDART_INF_F;
+            l[nt][j] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < S::kMT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
+    }
+
+    for (int stage = 0, t_left = hi - lo; t_left > 0;
+         --t_left, i0 += tile, stage = (stage + 1) % S::kStages) {
+        // a ring of one warp: the next copies go out first; a shared one: all its warps' copies
+        // are there, and all are done with the stage that the next ones fill
+        if (kHq > 1) copy_wait<S::kStages - 2>();
+        if (kHq > 1 || hw > 1) __syncthreads();  // (and the key heads' copies go out together)
+        if (ahead < step_end) {
+            copy((stage + S::kStages - 1) % S::kStages);
+            find(ahead += tile);
+        }
+        copy_commit();
+        if (i0 >= step_end || (kHq > 1 && n_heads <= 0)) continue;
+        if (kHq == 1) {
+            copy_wait<S::kStages - 1>();
+            __syncwarp();
+        }
+        const uint8_t* const at_k = ring + stage * S::kStage;
+        const uint8_t* const at_v = at_k + S::kRows;
+        const uint32_t here = *reinterpret_cast<const uint32_t*>(at_k + S::kThere);
+
+        // ---- scores
+        float x[kNT][S::kBlocks][4];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int mb = 0; mb < S::kBlocks; ++mb)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[nt][mb][j] = 0.0f;
+#pragma unroll
+        for (int mb = 0; mb < S::kBlocks; ++mb)
+#pragma unroll
+            for (int j = 0; j < S::kPieces / 4; ++j) {
+                const int r = 16 * mb + g;
+                const uint4 x0 = *reinterpret_cast<const uint4*>(
+                    at_k + 16 * k_place<S::kPieces>(r, 4 * j + t));
+                const uint4 x1 = *reinterpret_cast<const uint4*>(
+                    at_k + 16 * k_place<S::kPieces>(r + 8, 4 * j + t));
+                const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w};
+                const uint32_t w1[4] = {x1.x, x1.y, x1.z, x1.w};
+                constexpr int kSteps = S::kE4m3 ? 4 : 2;  // 16 columns of dim each
+#pragma unroll
+                for (int y = 0; y < kSteps; ++y) {
+                    const int s = j * kSteps + y;
+                    uint32_t a0, a1, a2, a3;
+                    if constexpr (S::kE4m3) {
+                        f16_of_e4m3(w0[y], &a0, &a2);
+                        f16_of_e4m3(w1[y], &a1, &a3);
+                    } else {
+                        a0 = w0[2 * y];
+                        a1 = w1[2 * y];
+                        a2 = w0[2 * y + 1];
+                        a3 = w1[2 * y + 1];
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < kNT; ++nt)
+                        mma16816<S::kBf16>(x[nt][mb], a0, a1, a2, a3, qf[nt][s][0], qf[nt][s][1]);
+                }
+            }
+
+        // ---- softmax: this lane has positions 8r + g, heads 2t and 2t + 1
+        float row_lv[S::kKRows];  // log2 of the rows' value scales
+        const float* const scales = reinterpret_cast<const float*>(at_k + S::kScales);
+        const bool negative = S::kE4m3 && __any_sync(~0u, scales[S::kStep + lane % S::kStep] < 0.0f);
+#pragma unroll
+        for (int r = 0; r < S::kKRows; ++r) {
+            const float row_ks = S::kE4m3 ? scales[r * 8 + g] : 1.0f;
+            row_lv[r] = S::kE4m3 ? log2_fast(fabsf(scales[S::kStep + r * 8 + g])) : 0.0f;
+            const bool ok = here >> (r * 8 + g) & 1u;
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float& y = x[nt][r / 2][r % 2 * 2 + j];
+                    y = ok ? y * (row_ks * factor[nt][j]) : -CUDART_INF_F;
+                }
+        }
+        bool moved = false;
+        float c[kNT][2];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // the largest score, and (E4M3) the largest score with the row's value scale in it
+                float top = m[nt][j], wide = w_top[nt][j];
+#pragma unroll
+                for (int r = 0; r < S::kKRows; ++r) {
+                    const float y = x[nt][r / 2][r % 2 * 2 + j];
+                    top = fmaxf(top, y);
+                    if (S::kE4m3) wide = fmaxf(wide, y + row_lv[r]);
+                }
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) {
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                    if (S::kE4m3) wide = fmaxf(wide, __shfl_xor_sync(~0u, wide, o));
+                }
+                if (!S::kE4m3) wide = top;
+                // what the weights are relative to lags behind the largest score by kAttnLag at most
+                // (weights up to 2^8 are as good), which spares most steps the rescaling of O; not
+                // with bfloat16 weights, where a largest weight of 1 is one that is not rounded
+                // (16 rows of up to 16385: error 2.0e-3, 2.4e-3 with the lag)
+                if constexpr (!S::kBf16) {
+                    // (l has the reference of the weights where those are its own terms)
+                    if constexpr (!S::kE4m3) top -= kAttnLift;
+                    wide -= kAttnLift;
+                    if (!(top > m[nt][j] + kAttnLag)) top = m[nt][j];
+                    if (!(wide > w_top[nt][j] + kAttnLag)) wide = w_top[nt][j];
+                }
+                const float ref = top == -CUDART_INF_F ? 0.0f : top;
+                const float w_ref = wide == -CUDART_INF_F ? 0.0f : wide;
+                float sum = l[nt][j] * exp2_fast(m[nt][j] - ref);
+                moved |= wide > w_top[nt][j];
+                c[nt][j] = exp2_fast(w_top[nt][j] - w_ref);
+                m[nt][j] = top;
+                w_top[nt][j] = wide;
+#pragma unroll
+                for (int r = 0; r < S::kKRows; ++r) {
+                    float& y = x[nt][r / 2][r % 2 * 2 + j];
+                    const float e = exp2_fast(y - ref);
+                    sum += e;
+                    y = S::kE4m3 ? exp2_fast(y + row_lv[r] - w_ref) : e;
+                    if (S::kE4m3 && negative)
+                        y = __uint_as_float(__float_as_uint(y) ^
+                                            (__float_as_uint(scales[S::kStep + r * 8 + g]) & 0x80000000u));
+                }
+                l[nt][j] = sum;
+            }
+        if (__any_sync(~0u, moved)) {
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int i = 0; i < S::kMT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[nt][i][j] *= c[nt][j % 2];
+        }
+
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int mb = 0; mb < S::kBlocks; ++mb) {
+            uint32_t pf[kNT][2];
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+                pf[nt][0] = transpose8(pack16<S::kBf16>(x[nt][mb][0], x[nt][mb][1]));
+                pf[nt][1] = transpose8(pack16<S::kBf16>(x[nt][mb][2], x[nt][mb][3]));
+            }
+            uint32_t w[4][S::kVWords];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int key = 16 * mb + r / 2 * 8 + 2 * t + r % 2;
+                if constexpr (S::kVWords == 2) {
+                    const uint2 y = *reinterpret_cast<const uint2*>(
+                        at_v + 16 * v_place<S::kPieces>(key, g / 2) + g % 2 * 8);
+                    w[r][0] = y.x;
+                    w[r][1] = y.y;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < S::kVWords / 4; ++j) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(
+                            at_v + 16 * v_place<S::kPieces>(key, 8 * j + g));
+                        w[r][4 * j] = y.x;
+                        w[r][4 * j + 1] = y.y;
+                        w[r][4 * j + 2] = y.z;
+                        w[r][4 * j + 3] = y.w;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < S::kMT; ++i) {
+                uint32_t a0, a1, a2, a3;
+                if constexpr (S::kE4m3) {
+                    const uint32_t sel = i % 2 ? 0x7362 : 0x5140;
+                    f16_of_e4m3(__byte_perm(w[0][i / 2], w[1][i / 2], sel), &a0, &a1);
+                    f16_of_e4m3(__byte_perm(w[2][i / 2], w[3][i / 2], sel), &a2, &a3);
+                } else {
+                    a0 = __byte_perm(w[0][i], w[1][i], 0x5410);
+                    a1 = __byte_perm(w[0][i], w[1][i], 0x7632);
+                    a2 = __byte_perm(w[2][i], w[3][i], 0x5410);
+                    a3 = __byte_perm(w[2][i], w[3][i], 0x7632);
+                }
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+                    mma16816<S::kBf16>(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            }
+        }
+        if (kHq == 1) __syncwarp();  // the stage may be filled again
+    }
 }
 
 template <int kType, int kDim, int kNT, int kHq>
@@ -247,7 +420,6 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     const int all_heads = side * S::kHeads;                  // of the CTA, with the empty ones
     const int tile = S::kStep * (kAttnWarps / side);         // positions
     uint8_t* const ring = smem + warp / kHq * S::kRing;
-    const uint32_t ring_at = ptx::smem_addr(ring);
     const AttnRows rows{p, int64_t(p.table.cols) * p.k.page_size, tile};
 
     asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this kernel's end
@@ -317,432 +489,10 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         // ---- one segment: tiles [lo, hi) of row b
         const int32_t count = rows.count(b), n_tiles = rows.tiles(b);
         const int32_t lo = at - row_start, hi = min(n_tiles, end - row_start);
-        const int h0 = kvh * group + h_first;
-        const int32_t len = rows.length(b);
-
-        // ---- Q: the words of this lane's columns, two values each
-        uint32_t qf[kNT][S::kMT][2];
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-            const int h = nt * 8 + g;
-            const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.q_row_stride +
-                                int64_t(h0 + h) * p.q_head_stride;
-            // word w = 2 s + j (columns of fragment s) is word w % kRun of the run w / kRun of words that
-            // lie together, as in the cache's rows: 16 values of 64, or 8 of 32
-            // (E2M1: all of a lane's values, 32 or 16)
-            constexpr int kRun = S::kE2m1 ? kDim / 8 : S::kE4m3 ? 8 : 4;
-#pragma unroll
-            for (int w = 0; w < 2 * S::kMT; w += 4) {
-                const int d = w / kRun * (8 * kRun) + t * (2 * kRun) + w % kRun * 2;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (h < n_heads && in_bounds(p.bounds, kMemQ, q + d, 16))
-                    x = *(reinterpret_cast<const uint4*>(q + d));
-                qf[nt][w / 2][0] = x.x;
-                qf[nt][w / 2][1] = x.y;
-                qf[nt][w / 2 + 1][0] = x.z;
-                qf[nt][w / 2 + 1][1] = x.w;
-            }
-        }
-
-        // ---- a step's rows: lane i finds position i of a step, a step ahead of its copies
-        const uint8_t* const k_base = p.k.data + kvh * p.k.head_stride;
-        const uint8_t* const v_base = p.v.data + kvh * p.v.head_stride;
-        const int32_t step_end = min(count, hi * tile);
-        const int mine = lane % S::kStep;
-        // (two steps ahead what `indices` says: its load, the table's and the rows' copies hang on
-        // one another, and nothing looks at what a load brings before the next one needs it)
-        int32_t page = -1, row = 0, listed = -1;
-        auto list = [&](int32_t i) {
-            listed = -1;
-            if (p.n_indices >= 0 && i + mine < step_end) {
-                const int32_t* const at = p.indices + b * p.indices_stride + i + mine;
-                if (in_bounds(p.bounds, kMemIndices, at, 4)) listed = *at;
-            }
-        };
-        auto find = [&](int32_t i) {  // i: the step's first place in the row's list
-            const int32_t n = p.n_indices >= 0 ? listed : i + mine;
-            page = -1;
-            if (i + mine < step_end && n >= 0 && n < len) {
-                const int32_t col = p.table.by_page.of(n);
-                row = n - col * p.k.page_size;
-                const int32_t* const at = p.table.ids + b * p.table.stride + col;
-                if (in_bounds(p.bounds, kMemTable, at, 4)) page = *at;
-            }
-            list(i + tile);
-        };
-        auto copy = [&](int stage) {  // the rows that find() found
-            const bool there = uint32_t(page) < uint32_t(p.k.pages);
-            const uint32_t k_at = there ? page * p.k_units.page + row * p.k_units.row : kNoRow;
-            const uint32_t v_at = there ? page * p.v_units.page + row * p.v_units.row : kNoRow;
-            const uint32_t to = ring_at + stage * S::kStage;
-            constexpr int kPer = 32 / S::kPieces;  // rows in one instruction
-            const int c = lane % S::kPieces;
-#pragma unroll
-            for (int j = 0; j < S::kStep / kPer / kHq; ++j) {
-                const int r = (j * kHq + warp % kHq) * kPer + lane / S::kPieces;
-                const uint32_t at = __shfl_sync(~0u, k_at, r);
-                const uint32_t at2 = p.same_rows ? at : __shfl_sync(~0u, v_at, r);
-                const bool ok = at != kNoRow;
-                auto k_from = [&] { return k_base + uint64_t(ok ? at : 0) * p.k_units.unit + 16 * c; };
-                auto v_from = [&] { return v_base + uint64_t(ok ? at2 : 0) * p.v_units.unit + 16 * c; };
-                copy16(to + 16 * k_place<S::kPieces>(r, c), k_from(),
-                       ok && in_bounds(p.bounds, kMemData, k_from(), 16));
-                const int v_to = S::kE2m1 ? v_place4<S::kPieces>(r, c) : v_place<S::kPieces>(r, c);
-                copy16(to + S::kRows + 16 * v_to, v_from(),
-                       ok && in_bounds(p.bounds, kMemData2, v_from(), 16));
-            }
-            if (S::kScaled && warp % kHq == 0) {
-                const int64_t pg = there ? page : 0, rw = there ? row : 0;
-                if constexpr (S::kE2m1) {
-                    const uint8_t* const k_group = p.k.groups + pg * p.k.group_page_stride +
-                                                   rw * p.k.group_row_stride + kvh * p.k.group_head_stride;
-                    const uint8_t* const v_group = p.v.groups + pg * p.v.group_page_stride +
-                                                   rw * p.v.group_row_stride + kvh * p.v.group_head_stride;
-                    auto copy_groups = [&](uint32_t at, const uint8_t* from, bool ok) {
-                        if constexpr (S::kGroupBytes == 8) copy8(at, from, ok);
-                        else copy4(at, from, ok);
-                    };
-                    copy_groups(to + S::kGroups + S::kGroupBytes * lane, k_group,
-                                there && in_bounds(p.bounds, kMemGroups, k_group, S::kGroupBytes));
-                    copy_groups(to + S::kGroups + S::kGroupBytes * (S::kStep + lane), v_group,
-                                there && in_bounds(p.bounds, kMemGroups2, v_group, S::kGroupBytes));
-                }
-                const float* const k_from = p.k.scale + pg * p.k.scale_page_stride +
-                                            rw * p.k.scale_row_stride + kvh * p.k.scale_head_stride;
-                const float* const v_from = p.v.scale + pg * p.v.scale_page_stride +
-                                            rw * p.v.scale_row_stride + kvh * p.v.scale_head_stride;
-                copy4(to + S::kScales + 4 * lane, k_from, there && in_bounds(p.bounds, kMemScale, k_from, 4));
-                copy4(to + S::kScales + 4 * (S::kStep + lane), v_from,
-                      there && in_bounds(p.bounds, kMemScale2, v_from, 4));
-            }
-            const uint32_t here = __ballot_sync(~0u, there);
-            if (lane == 0 && warp % kHq == 0)
-                *reinterpret_cast<uint32_t*>(ring + stage * S::kStage + S::kThere) = here;
-        };
-
-        int32_t i0 = lo * tile + warp / side * S::kStep;  // the step being computed
-        int32_t ahead = i0;                               // the step that find() found
-        list(ahead);
-        find(ahead);
-#pragma unroll 1
-        for (int j = 0; j < S::kStages - 1; ++j) {
-            if (ahead < step_end) {
-                copy(j);
-                find(ahead += tile);
-            }
-            copy_commit();
-        }
-
-        // ---- Q as B fragments, and each head's factor of the scores (in powers of two)
-        float factor[kNT][2], m[kNT][2], l[kNT][2], w_top[kNT][2], o[kNT][S::kMT][4];
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-            float by = 1.0f;
-            if (S::kScaled && p.q_bf16) {
-                // bfloat16 -> f16: exact but for the range, so each head is brought to a largest
-                // magnitude of 2^12 .. 2^13 by a power of two (what then falls below f16's range
-                // is under 2^-36 of the largest)
-                float top = 0.0f;
-#pragma unroll
-                for (int s = 0; s < S::kMT; ++s)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        top = fmaxf(top, fabsf(__uint_as_float(qf[nt][s][j] << 16)));
-                        top = fmaxf(top, fabsf(__uint_as_float(qf[nt][s][j] & 0xFFFF0000u)));
-                    }
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                const int e = min(max(int(__float_as_uint(top) >> 23), 20), 240) - 139;
-                const float down = __uint_as_float(uint32_t(127 - e) << 23);
-                by = __uint_as_float(uint32_t(127 + e) << 23);
-#pragma unroll
-                for (int s = 0; s < S::kMT; ++s)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        qf[nt][s][j] =
-                            pack16<false>(__uint_as_float(qf[nt][s][j] << 16) * down,
-                                          __uint_as_float(qf[nt][s][j] & 0xFFFF0000u) * down);
-            }
-            const float c = p.sm_scale * 1.4426950408889634f * by;
-            factor[nt][0] = __shfl_sync(~0u, c, 8 * t);
-            factor[nt][1] = __shfl_sync(~0u, c, 8 * t + 4);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                m[nt][j] = w_top[nt][j] = -CUDART_INF_F;
-                l[nt][j] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < S::kMT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
-        }
-
-        for (int stage = 0, t_left = hi - lo; t_left > 0;
-             --t_left, i0 += tile, stage = (stage + 1) % S::kStages) {
-            // a ring of one warp: the next copies go out first; a shared one: all its warps' copies
-            // are there, and all are done with the stage that the next ones fill
-            if (kHq > 1) copy_wait<S::kStages - 2>();
-            if (kHq > 1 || hw > 1) __syncthreads();  // (and the key heads' copies go out together)
-            if (ahead < step_end) {
-                copy((stage + S::kStages - 1) % S::kStages);
-                find(ahead += tile);
-            }
-            copy_commit();
-            if (i0 >= step_end || (kHq > 1 && n_heads <= 0)) continue;
-            if (kHq == 1) {
-                copy_wait<S::kStages - 1>();
-                __syncwarp();
-            }
-            const uint8_t* const at_k = ring + stage * S::kStage;
-            const uint8_t* const at_v = at_k + S::kRows;
-            const uint32_t here = *reinterpret_cast<const uint32_t*>(at_k + S::kThere);
-
-            // ---- scores
-            float x[kNT][S::kBlocks][4];
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                for (int mb = 0; mb < S::kBlocks; ++mb)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[nt][mb][j] = 0.0f;
-            if constexpr (S::kE2m1) {
-                // a lane's values of a row are one or two whole groups: kWords words of eight
-                constexpr int kWords = S::kRowBytes / 16;
-                const uint8_t* const k_groups = at_k + S::kGroups;
-#pragma unroll
-                for (int mb = 0; mb < S::kBlocks; ++mb) {
-                    uint32_t w[2][kWords], by[2][kWords];  // of rows g and g + 8
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = 16 * mb + 8 * i + g;
-                        if constexpr (kWords == 4) {
-                            const uint4 y = *reinterpret_cast<const uint4*>(at_k + 16 * k_place<S::kPieces>(r, t));
-                            w[i][0] = y.x;
-                            w[i][1] = y.y;
-                            w[i][2] = y.z;
-                            w[i][3] = y.w;
-                            const uint32_t two =
-                                f16x2_of_e4m3x2(*reinterpret_cast<const uint16_t*>(k_groups + r * 8 + 2 * t));
-                            by[i][0] = by[i][1] = __byte_perm(two, two, 0x1010);
-                            by[i][2] = by[i][3] = __byte_perm(two, two, 0x3232);
-                        } else {
-                            const uint2 y = *reinterpret_cast<const uint2*>(at_k + r * 32 + 8 * t);
-                            w[i][0] = y.x;
-                            w[i][1] = y.y;
-                            by[i][0] = by[i][1] = f16x2_of_e4m3x2(k_groups[r * 4 + t] * 0x101u);
-                        }
-                    }
-#pragma unroll
-                    for (int y = 0; y < kWords; ++y) {
-                        uint32_t a[2][4];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            f16_of_e2m1(w[i][y], a[i]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) a[i][j] = mul_f16x2(a[i][j], by[i][y]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int nt = 0; nt < kNT; ++nt)
-                                mma16816<false>(x[nt][mb], a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1],
-                                                qf[nt][2 * y + j][0], qf[nt][2 * y + j][1]);
-                    }
-                }
-            } else {
-#pragma unroll
-            for (int mb = 0; mb < S::kBlocks; ++mb)
-#pragma unroll
-                for (int j = 0; j < S::kPieces / 4; ++j) {
-                    const int r = 16 * mb + g;
-                    const uint4 x0 = *reinterpret_cast<const uint4*>(
-                        at_k + 16 * k_place<S::kPieces>(r, 4 * j + t));
-                    const uint4 x1 = *reinterpret_cast<const uint4*>(
-                        at_k + 16 * k_place<S::kPieces>(r + 8, 4 * j + t));
-                    const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w};
-                    const uint32_t w1[4] = {x1.x, x1.y, x1.z, x1.w};
-                    constexpr int kSteps = S::kE4m3 ? 4 : 2;  // 16 columns of dim each
-#pragma unroll
-                    for (int y = 0; y < kSteps; ++y) {
-                        const int s = j * kSteps + y;
-                        uint32_t a0, a1, a2, a3;
-                        if constexpr (S::kE4m3) {
-                            f16_of_e4m3(w0[y], &a0, &a2);
-                            f16_of_e4m3(w1[y], &a1, &a3);
-                        } else {
-                            a0 = w0[2 * y];
-                            a1 = w1[2 * y];
-                            a2 = w0[2 * y + 1];
-                            a3 = w1[2 * y + 1];
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt)
-                            mma16816<S::kBf16>(x[nt][mb], a0, a1, a2, a3, qf[nt][s][0], qf[nt][s][1]);
-                    }
-                }
-            }
-
-            // ---- softmax: this lane has positions 8r + g, heads 2t and 2t + 1
-            float row_lv[S::kKRows];  // log2 of the rows' value scales
-            const float* const scales = reinterpret_cast<const float*>(at_k + S::kScales);
-            const bool negative = S::kScaled && __any_sync(~0u, scales[S::kStep + lane % S::kStep] < 0.0f);
-#pragma unroll
-            for (int r = 0; r < S::kKRows; ++r) {
-                const float row_ks = S::kScaled ? scales[r * 8 + g] : 1.0f;
-                row_lv[r] = S::kScaled ? log2_fast(fabsf(scales[S::kStep + r * 8 + g])) : 0.0f;
-                const bool ok = here >> (r * 8 + g) & 1u;
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float& y = x[nt][r / 2][r % 2 * 2 + j];
-                        y = ok ? y * (row_ks * factor[nt][j]) : -CUDART_INF_F;
-                    }
-            }
-            bool moved = false;
-            float c[kNT][2];
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    // the largest score, and (E4M3) the largest score with the row's value scale in it
-                    float top = m[nt][j], wide = w_top[nt][j];
-#pragma unroll
-                    for (int r = 0; r < S::kKRows; ++r) {
-                        const float y = x[nt][r / 2][r % 2 * 2 + j];
-                        top = fmaxf(top, y);
-                        if (S::kScaled) wide = fmaxf(wide, y + row_lv[r]);
-                    }
-#pragma unroll
-                    for (int o = 4; o < 32; o *= 2) {
-                        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-                        if (S::kScaled) wide = fmaxf(wide, __shfl_xor_sync(~0u, wide, o));
-                    }
-                    if (!S::kScaled) wide = top;
-                    // what the weights are relative to lags behind the largest score by kAttnLag at most
-                    // (weights up to 2^8 are as good), which spares most steps the rescaling of O; not
-                    // with bfloat16 weights, where a largest weight of 1 is one that is not rounded
-                    // (16 rows of up to 16385: error 2.0e-3, 2.4e-3 with the lag)
-                    if constexpr (!S::kBf16) {
-                        // (l has the reference of the weights where those are its own terms)
-                        if constexpr (!S::kScaled) top -= kAttnLift;
-                        wide -= kAttnLift;
-                        if (!(top > m[nt][j] + kAttnLag)) top = m[nt][j];
-                        if (!(wide > w_top[nt][j] + kAttnLag)) wide = w_top[nt][j];
-                    }
-                    const float ref = top == -CUDART_INF_F ? 0.0f : top;
-                    const float w_ref = wide == -CUDART_INF_F ? 0.0f : wide;
-                    float sum = l[nt][j] * exp2_fast(m[nt][j] - ref);
-                    moved |= wide > w_top[nt][j];
-                    c[nt][j] = exp2_fast(w_top[nt][j] - w_ref);
-                    m[nt][j] = top;
-                    w_top[nt][j] = wide;
-#pragma unroll
-                    for (int r = 0; r < S::kKRows; ++r) {
-                        float& y = x[nt][r / 2][r % 2 * 2 + j];
-                        const float e = exp2_fast(y - ref);
-                        sum += e;
-                        y = S::kScaled ? exp2_fast(y + row_lv[r] - w_ref) : e;
-                        if (S::kScaled && negative)
-                            y = __uint_as_float(__float_as_uint(y) ^
-                                                (__float_as_uint(scales[S::kStep + r * 8 + g]) & 0x80000000u));
-                    }
-                    l[nt][j] = sum;
-                }
-            if (__any_sync(~0u, moved)) {
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < S::kMT; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) o[nt][i][j] *= c[nt][j % 2];
-            }
-
-            // ---- O^T += V^T P^T
-#pragma unroll
-            for (int mb = 0; mb < S::kBlocks; ++mb) {
-                uint32_t pf[kNT][2];
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) {
-                    pf[nt][0] = transpose8(pack16<S::kBf16>(x[nt][mb][0], x[nt][mb][1]));
-                    pf[nt][1] = transpose8(pack16<S::kBf16>(x[nt][mb][2], x[nt][mb][3]));
-                }
-                uint32_t w[4][S::kVWords];
-                uint32_t group[4];  // E2M1: the scale of the lane's columns, an E4M3 code
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int key = 16 * mb + r / 2 * 8 + 2 * t + r % 2;
-                    if constexpr (S::kE2m1) {
-                        if constexpr (S::kVWords == 2) {
-                            const uint2 y = *reinterpret_cast<const uint2*>(
-                                at_v + 16 * v_place4<S::kPieces>(key, g / 2) + g % 2 * 8);
-                            w[r][0] = y.x;
-                            w[r][1] = y.y;
-                        } else {
-                            w[r][0] = *reinterpret_cast<const uint32_t*>(
-                                at_v + 16 * v_place4<S::kPieces>(key, g / 4) + g % 4 * 4);
-                        }
-                        group[r] = at_k[S::kGroups + (S::kStep + key) * S::kGroupBytes + g * S::kGroupBytes / 8];
-                    } else if constexpr (S::kVWords == 2) {
-                        const uint2 y = *reinterpret_cast<const uint2*>(
-                            at_v + 16 * v_place<S::kPieces>(key, g / 2) + g % 2 * 8);
-                        w[r][0] = y.x;
-                        w[r][1] = y.y;
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < S::kVWords / 4; ++j) {
-                            const uint4 y = *reinterpret_cast<const uint4*>(
-                                at_v + 16 * v_place<S::kPieces>(key, 8 * j + g));
-                            w[r][4 * j] = y.x;
-                            w[r][4 * j + 1] = y.y;
-                            w[r][4 * j + 2] = y.z;
-                            w[r][4 * j + 3] = y.w;
-                        }
-                    }
-                }
-                if constexpr (S::kE2m1) {
-                    const uint32_t by01 = f16x2_of_e4m3x2(group[0] | group[1] << 8);
-                    const uint32_t by23 = f16x2_of_e4m3x2(group[2] | group[3] << 8);
-#pragma unroll
-                    for (int y = 0; y < S::kVWords; ++y) {
-                        // bytes of one column of two rows: columns 0, 2, 4 and 6 of a word's, then 1, 3, 5 and 7
-                        constexpr uint32_t kLow = 0x0F0F0F0Fu;
-                        uint32_t a[4][4];
-                        f16_of_e2m1((w[0][y] & kLow) | (w[1][y] << 4 & ~kLow), a[0]);
-                        f16_of_e2m1((w[0][y] >> 4 & kLow) | (w[1][y] & ~kLow), a[1]);
-                        f16_of_e2m1((w[2][y] & kLow) | (w[3][y] << 4 & ~kLow), a[2]);
-                        f16_of_e2m1((w[2][y] >> 4 & kLow) | (w[3][y] & ~kLow), a[3]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t a0 = mul_f16x2(a[0][j], by01), a1 = mul_f16x2(a[1][j], by01);
-                            const uint32_t a2 = mul_f16x2(a[2][j], by23), a3 = mul_f16x2(a[3][j], by23);
-#pragma unroll
-                            for (int nt = 0; nt < kNT; ++nt)
-                                mma16816<false>(o[nt][4 * y + j], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                for (int i = 0; i < S::kMT; ++i) {
-                    uint32_t a0, a1, a2, a3;
-                    if constexpr (S::kE4m3) {
-                        const uint32_t sel = i % 2 ? 0x7362 : 0x5140;
-                        f16_of_e4m3(__byte_perm(w[0][i / 2], w[1][i / 2], sel), &a0, &a1);
-                        f16_of_e4m3(__byte_perm(w[2][i / 2], w[3][i / 2], sel), &a2, &a3);
-                    } else {
-                        a0 = __byte_perm(w[0][i], w[1][i], 0x5410);
-                        a1 = __byte_perm(w[0][i], w[1][i], 0x7632);
-                        a2 = __byte_perm(w[2][i], w[3][i], 0x5410);
-                        a3 = __byte_perm(w[2][i], w[3][i], 0x7632);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt)
-                        mma16816<S::kBf16>(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                }
-                }
-            }
-            if (kHq == 1) __syncwarp();  // the stage may be filled again
-        }
+        AttnSums<S> r;
+        const AttnPart part{b, lo, hi, kvh * group + h_first, n_heads, kvh, hw, tile};
+        if constexpr (S::kE2m1) attn_steps4<S>(p, rows, part, ring, r);
+        else attn_steps<S>(p, rows, part, ring, r);
 
         // ---- the warps' results, joined in shared memory
         // [heads][dim], where the rings were
@@ -754,14 +504,14 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             for (int j = 0; j < 2; ++j) {
                 // O is counted in 2^w_top, m and l in 2^m
                 const float v_back =
-                    !S::kScaled ? 1.0f : w_top[nt][j] == -CUDART_INF_F ? 0.0f : exp2_fast(w_top[nt][j] - m[nt][j]);
-                float sum = l[nt][j];
+                    !S::kScaled ? 1.0f : r.w_top[nt][j] == -CUDART_INF_F ? 0.0f : exp2_fast(r.w_top[nt][j] - r.m[nt][j]);
+                float sum = r.l[nt][j];
                 sum += __shfl_xor_sync(~0u, sum, 4);
                 sum += __shfl_xor_sync(~0u, sum, 8);
                 sum += __shfl_xor_sync(~0u, sum, 16);
                 const int h = nt * 8 + 2 * t + j;
                 if (g == 0) {
-                    s_ml[warp][h][0] = m[nt][j];
+                    s_ml[warp][h][0] = r.m[nt][j];
                     s_ml[warp][h][1] = sum;
                 }
                 // four columns of a head at a time: those of fragments i and i + 1 lie together
@@ -770,8 +520,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
                     const int d = S::kScaled ? g * (kDim / 8) + 2 * i
                                            : i / 4 * 64 + g * 8 + 2 * i % 8;
                     *reinterpret_cast<float4*>(s_o + h * S::kPitch + d) =
-                        make_float4(o[nt][i][j] * v_back, o[nt][i][2 + j] * v_back,
-                                    o[nt][i + 1][j] * v_back, o[nt][i + 1][2 + j] * v_back);
+                        make_float4(r.o[nt][i][j] * v_back, r.o[nt][i][2 + j] * v_back,
+                                    r.o[nt][i + 1][j] * v_back, r.o[nt][i + 1][2 + j] * v_back);
                 }
             }
         __syncthreads();

@@ -293,7 +293,8 @@ FP8MQA_API int fp8_mqa_topk_ex(const float* logits, int64_t M, int64_t N, int64_
  * their strides a multiple of dim / 16 bytes;
  * pages * page_size < 2^31; strides are not negative.  Byte offsets are 64-bit throughout;
  * fp8_mqa_attention_paged counts a cache's rows in units of the greatest common divisor of its
- * page and row strides, of which a cache may span up to 2^32 - 2 (64 GB even at 16 bytes).
+ * page and row strides, of which a cache may span up to 2^32 - 2 (64 GB even at 16 bytes); for E2M1
+ * caches the groups and the scales too, whose strides are not negative either.
  * ------------------------------------------------------------------------------------------ */
 
 /* Element types. */

@@ -181,7 +181,7 @@ def close(got, lse, want, wlse, size, dots, dtype):
 
 
 def check_attention(rng, lens, q_heads, heads, dim, page, dtype=torch.bfloat16, layout="plain", select=None, holes=False,
-                    fused=False, shared=False, sharp=1.0, spread=None, cols=None, negative=False):
+                    fused=False, shared=False, sharp=1.0, spread=None, cols=None, negative=False, sm=None):
     lens = np.asarray(lens, np.int32)
     B = len(lens)
     table, pages = tables(rng, lens[:1] if shared else lens, page, cols=cols)
@@ -202,7 +202,7 @@ def check_attention(rng, lens, q_heads, heads, dim, page, dtype=torch.bfloat16, 
             n = rng.permutation(max(0, int(lens[b])))[:select]
             indices[b, rng.permutation(select)[:len(n)]] = n
             indices[b, select:] = [lens[b], -2 ** 31, 2 ** 31 - 1]  # out of range: ignored
-    sm = dim ** -0.5
+    sm = dim ** -0.5 if sm is None else sm
     tab = gpu(table).expand(B, -1) if shared else gpu(table)
     got, lse = fm.attention_paged(q, k[0].view(F4), v[0].view(F4), tab, gpu(lens), sm, k_scale=k[2], v_scale=v[2],
                                   indices=None if indices is None else gpu(indices), return_lse=True, k_groups=k[1],
@@ -267,6 +267,33 @@ def test_attention_sharp_scores_and_wide_scales():
         check_attention(rng, [400, 1000], 8, 2, 128, 64, dtype, sharp=30.0)
         check_attention(rng, [400, 1000], 8, 2, 128, 64, dtype, spread=4.0)
         check_attention(rng, [400, 1000], 8, 2, 64, 64, dtype, negative=True)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attention_scales_of_the_scores(dtype):
+    rng = np.random.default_rng(14)
+    for sm in (0.0, -0.05, -dim_root(64), 1e-30, 3.0):
+        check_attention(rng, [200, 0, 65], 8, 2, 64, 32, dtype, sm=sm)
+        check_attention(rng, [300], 4, 1, 128, 64, dtype, sm=sm, holes=True)
+
+
+def dim_root(dim):
+    return float(np.float32(dim ** -0.5))
+
+
+def test_attention_scores_that_rise_and_fall():
+    # keys grow from page to page and shrink again, so that the references move step after step, and stay far behind
+    for dtype in TYPES:
+        for power in (1.0, -1.0):
+            rng = np.random.default_rng(15)
+            table, pages = tables(rng, [900], 64)
+            k, v = cache(rng, pages, 64, 2, 128), cache(rng, pages, 64, 2, 128)
+            at = torch.arange(15, device="cuda", dtype=torch.float32)
+            k[2][torch.from_numpy(table[0].astype(np.int64)).cuda()] = (0.0002 * 1.5 ** (power * (at - 7)))[:, None, None]
+            q = torch.from_numpy(np.abs(rng.standard_normal((1, 8, 128)))).to(dtype).cuda()
+            got, lse = fm.attention_paged(q, k[0].view(F4), v[0].view(F4), gpu(table), gpu(np.array([900], np.int32)),
+                                          k_scale=k[2], v_scale=v[2], k_groups=k[1], v_groups=v[1], return_lse=True)
+            close(got, lse, *plain.attention(f64(q), as_rows(k), as_rows(v), table, [900], 128 ** -0.5), dtype)
 
 
 def test_attention_of_nan_and_zero_rows():
