@@ -177,6 +177,14 @@ PagedView view_of(const fp8mqa_cache& c, const void* valid)
     return v;
 }
 
+bool same_strides(const PagedView& a, const PagedView& b)
+{
+    return a.page_stride == b.page_stride && a.row_stride == b.row_stride && a.head_stride == b.head_stride &&
+           a.scale_page_stride == b.scale_page_stride && a.scale_row_stride == b.scale_row_stride &&
+           a.scale_head_stride == b.scale_head_stride && a.group_page_stride == b.group_page_stride &&
+           a.group_row_stride == b.group_row_stride && a.group_head_stride == b.group_head_stride;
+}
+
 // The units that something of a cache's rows is counted in, from the strides of its pages and rows and the
 // least unit; false if 32 bits do not hold them.
 bool row_units(const PagedView& v, int64_t page_stride, int64_t row_stride, int64_t least, RowUnits* u)
@@ -214,16 +222,17 @@ void spans(PagedBounds& b, const PageTable& t, int64_t B)
     spans(b, kMemTable, t.ids, extent(B, 4 * t.stride, t.cols, 4, 1, 0, 4));
 }
 
-// Rows of x that start on 16 bytes are read 16 bytes at a time, others value by value.
+// Rows of x that start on 16 bytes (32 for E2M1 caches) are read as many bytes at a time, others value by value.
 template <class X, int kDim, int kTensors>
 cudaError_t write_tensors(const CacheWriteParams& p, bool four, cudaStream_t s)
 {
     const int64_t rows = p.T * p.heads, per = kCacheThreads / (kDim / 16);
     const unsigned blocks = unsigned((rows + per - 1) / per);
+    const int64_t wide = four ? 32 : 16;
     bool vec = true;
     for (int i = 0; i < kTensors; ++i)
-        vec = vec && on(p.x[i], 16) && p.row_stride[i] * int64_t(sizeof(X)) % 16 == 0 &&
-              p.head_stride[i] * int64_t(sizeof(X)) % 16 == 0;
+        vec = vec && on(p.x[i], uintptr_t(wide)) && p.row_stride[i] * int64_t(sizeof(X)) % wide == 0 &&
+              p.head_stride[i] * int64_t(sizeof(X)) % wide == 0;
     if (four)
         return vec
                    ? launch_after(cache_write4_kernel<X, kDim, true, kTensors>, dim3(blocks), kCacheThreads, 0, s, p)
@@ -242,13 +251,13 @@ cudaError_t write_rows(const CacheWriteParams& p, int32_t dim, int tensors, bool
 // A block packs about kReadTurns x kReadPieces pieces a thread (finding the rows costs a block its
 // start: 66 thousand rows of 8 heads as stored take 25.3 us so and 28.6 in one turn), but no more
 // than leaves two blocks an SM.
-constexpr int64_t kReadTurns = 4;
+constexpr int64_t kReadTurns = 4, kReadTurns4 = 8;
 template <class Out>
 cudaError_t read_rows(CacheReadParams& p, int32_t dim, bool four, int sm_count, cudaStream_t s)
 {
     const int64_t row_pieces = four ? int64_t(p.cache.heads) * dim / kGroup
                                     : int64_t(p.cache.heads) * dim * int64_t(sizeof(Out)) / 16;
-    const int64_t rows = std::min(kReadTurns * kReadPieces * kCacheThreads / row_pieces,
+    const int64_t rows = std::min((four ? kReadTurns4 * kReadPieces4 : kReadTurns * kReadPieces) * kCacheThreads / row_pieces,
                                   p.total / (2 * sm_count));
     p.block_rows = int32_t(std::max<int64_t>(1, std::min<int64_t>(kReadRows, rows)));
     const unsigned blocks = unsigned((p.total + p.block_rows - 1) / p.block_rows);
@@ -441,6 +450,7 @@ int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const v
     p.head_stride[1] = x2_head_stride;
     p.cache[0] = view_of(*cache, x);
     p.cache[1] = view_of(cache2 ? *cache2 : *cache, x);
+    p.alike = same_strides(p.cache[0], p.cache[1]);
     p.bounds = bounds_for(*st);
     spans(p.bounds, kMemSlots, slots, 4 * T);
     for (int i = 0; i < (x2 ? 2 : 1); ++i) {
@@ -487,6 +497,7 @@ int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t 
     p.by_heads = FastDiv(uint32_t(cache->heads));
     p.out = out;
     p.out_scale = out_scale;
+    p.aligned32 = on(out, 32);
     p.bounds = bounds_for(*st);
     spans(p.bounds, 0, p.cache, *cache);
     spans(p.bounds, p.table, B);

@@ -31,7 +31,8 @@ struct Entries {
     decltype(&fp8_mqa_norm_rotate) norm_rotate = nullptr;
 } g_entry;
 
-PyObject* g_error = nullptr;  // Fp8MqaError
+PyObject* g_error = nullptr;     // Fp8MqaError
+PyTypeObject* g_step = nullptr;  // PagesStep, a tuple of five
 
 constexpr int64_t kHeads = 32, kDim = 128;
 
@@ -175,6 +176,16 @@ fp8mqa_cache cache_of(PyObject* data_o, PyObject* scale_o, PyObject* groups_o, c
 at::Tensor empty(c10::IntArrayRef sizes, at::ScalarType type, const c10::Device& device)
 {
     return at::empty(sizes, at::TensorOptions().dtype(type).device(device));
+}
+
+// n elements of a one-dimensional tensor, from `from` on.
+at::Tensor part_of(const at::Tensor& base, int64_t from, int64_t n)
+{
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(base.storage()),
+                                                            base.key_set(), base.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(from);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    return t;
 }
 
 void* current_stream(const c10::Device& device)
@@ -420,11 +431,17 @@ PyObject* pages_update(PyObject* const* a, Py_ssize_t n)
     if (total < 0) bad(PyExc_ValueError, "total must not be negative");
     if (B > 1 && table.stride(0) < cols) bad(PyExc_ValueError, "the rows of table must not overlap: they are written");
     const c10::cuda::CUDAGuard guard(device);
-    at::Tensor out[5] = {empty({total}, at::kInt, device), empty({total}, at::kInt, device),
-                         empty({total}, at::kInt, device), empty({B + 1}, at::kInt, device),
-                         empty({B}, at::kInt, device)};
+    // one allocation for the five results, each on 16 bytes: five of them took half of the call
+    const int64_t size[5] = {total, total, total, B + 1, B};
+    int64_t at[6] = {0};
+    for (int i = 0; i < 5; ++i) at[i + 1] = at[i] + (size[i] + 3) / 4 * 4;
+    const at::Tensor base = empty({at[5]}, at::kInt, device);
+    at::Tensor out[5];
     int32_t* to[5];
-    for (int i = 0; i < 5; ++i) to[i] = static_cast<int32_t*>(out[i].data_ptr());
+    for (int i = 0; i < 5; ++i) {
+        out[i] = part_of(base, at[i], size[i]);
+        to[i] = static_cast<int32_t*>(base.data_ptr()) + at[i];
+    }
     auto *ids = static_cast<int32_t*>(table.data_ptr()), *len = static_cast<int32_t*>(lens.data_ptr());
     auto *stack = static_cast<int32_t*>(pool.data_ptr()), *height = static_cast<int32_t*>(n_free.data_ptr());
     const auto* by = static_cast<const int32_t*>(change.data_ptr());
@@ -435,9 +452,10 @@ PyObject* pages_update(PyObject* const* a, Py_ssize_t n)
                                          total, to[0], to[1], to[2], to[3], to[4], stream);
          }),
          "fp8_mqa_pages_update");
-    return Py_BuildValue("(NNNNN)", THPVariable_Wrap(std::move(out[0])), THPVariable_Wrap(std::move(out[1])),
-                         THPVariable_Wrap(std::move(out[2])), THPVariable_Wrap(std::move(out[3])),
-                         THPVariable_Wrap(std::move(out[4])));
+    PyObject* const result = g_step->tp_alloc(g_step, 5);  // a kind of tuple
+    if (!result) throw Raised{};
+    for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(result, i, THPVariable_Wrap(std::move(out[i])));
+    return result;
 }
 
 // q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, q_out, k_out
@@ -554,10 +572,10 @@ PyObject* norm_rotate(PyObject* const* a, Py_ssize_t n)
 }
 
 // The entry points' addresses (cache_write, cache_read, logits_paged, workspace_bytes,
-// attention_paged, pages_update, norm_rotate) and the error class.
+// attention_paged, pages_update, norm_rotate), the error class and the type of a step's result.
 PyObject* bind(PyObject* const* a, Py_ssize_t n)
 {
-    if (n != 8) bad(PyExc_TypeError, "wrong number of arguments");
+    if (n != 9) bad(PyExc_TypeError, "wrong number of arguments");
     void* p[7];
     for (int i = 0; i < 7; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
@@ -569,6 +587,11 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n)
     Py_INCREF(a[7]);
     Py_XDECREF(g_error);
     g_error = a[7];
+    if (!PyType_Check(a[8]) || !PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(a[8]), &PyTuple_Type))
+        bad(PyExc_TypeError, "the step's type must be a kind of tuple");
+    Py_INCREF(a[8]);
+    Py_XDECREF(reinterpret_cast<PyObject*>(g_step));
+    g_step = reinterpret_cast<PyTypeObject*>(a[8]);
     g_entry.cache_write = reinterpret_cast<decltype(g_entry.cache_write)>(p[0]);
     g_entry.cache_read = reinterpret_cast<decltype(g_entry.cache_read)>(p[1]);
     g_entry.logits_paged = reinterpret_cast<decltype(g_entry.logits_paged)>(p[2]);

@@ -13,34 +13,44 @@
 namespace fp8mqa {
 namespace {
 
-// A cluster of 8 CTAs where there is enough to write, else one, which has no barrier to wait for.
-constexpr int kPagesCluster = 8;
-constexpr int64_t kPagesOneCta = 4096;  // tokens and requests
+size_t pages_smem_bytes(int32_t B) { return 4 * size_t(B + 1) * sizeof(int32_t); }
 
-cudaError_t pages_launch(const PagesParams& p, cudaStream_t s)
+// A cluster for what it has the threads for, else a CTA for each kPagesTokens tokens and then the lengths.
+constexpr int64_t kPagesTokens = 4 * kPagesThreads;
+constexpr unsigned kPagesCluster = 8;
+constexpr int64_t kPagesInCluster = 2 * kPagesCluster * kPagesTokens;
+
+cudaError_t pages_launch(PagesParams& p, int sm_count, cudaStream_t s)
 {
-    const unsigned ctas = int64_t(p.total) + p.B > kPagesOneCta ? kPagesCluster : 1;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kPagesThreads);
-    cfg.dynamicSmemBytes = 3 * size_t(p.B + 1) * sizeof(int32_t);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, pages_update_kernel, p);
+    const size_t smem = pages_smem_bytes(p.B);
+    p.state = p.total <= kPagesInCluster;
+    if (p.state) {
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = kPagesCluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kPagesCluster);
+        cfg.blockDim = dim3(kPagesThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, pages_update_kernel, p);
+    }
+    const int64_t ctas = std::min<int64_t>((p.total + kPagesTokens - 1) / kPagesTokens, 2 * sm_count);
+    const cudaError_t e = launch_after(pages_update_kernel, dim3(unsigned(ctas)), kPagesThreads, smem, s, p);
+    if (e != cudaSuccess) return e;
+    return launch_after(pages_state_kernel, dim3(1), 1024, 0, s, p);
 }
 
 // What a call that needs more shared memory than a kernel gets unasked sets up once for each device.
 bool pages_smem()
 {
     return cudaFuncSetAttribute(pages_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                int(3 * (kPagesMaxRows + 1) * sizeof(int32_t))) == cudaSuccess;
+                                int(pages_smem_bytes(kPagesMaxRows))) == cudaSuccess;
 }
 
 template <class X, int kDim, bool kE4m3, bool kInterleaved>
@@ -105,7 +115,7 @@ int fp8_mqa_pages_update(int32_t* table, int64_t table_stride, int32_t table_col
 {
     using namespace fp8mqa;
     if (B < 0 || table_cols < 0 || page_size < 1 || capacity < 0 || total < 0) return FP8MQA_ERR_INVALID_ARG;
-    if (B > kPagesMaxRows || int64_t(table_cols) * page_size > INT32_MAX || capacity > INT32_MAX || total > INT32_MAX)
+    if (B > kPagesMaxRows || int64_t(table_cols) * page_size > INT32_MAX || B * table_cols > INT32_MAX || capacity > INT32_MAX || total > INT32_MAX)
         return FP8MQA_ERR_UNSUPPORTED_SHAPE;
     if ((B > 0 && (!lens || !change || !changed)) || (B > 0 && table_cols > 0 && !table) || (capacity > 0 && !free_pages) ||
         !n_free || !starts || (total > 0 && (!slots || !positions || !rows)))
@@ -122,7 +132,7 @@ int fp8_mqa_pages_update(int32_t* table, int64_t table_stride, int32_t table_col
     const PagedDevice* st = paged_device(&err);
     if (!st) return err;
     // (what a kernel gets unasked is 48 KB)
-    if (3 * (B + 1) * 4 > 47 * 1024 && !pages_smem()) return launched(cudaErrorInvalidValue);
+    if (pages_smem_bytes(int32_t(B)) > 47 * 1024 && !pages_smem()) return launched(cudaErrorInvalidValue);
     PagesParams p;
     p.table = table;
     p.table_stride = table_stride;
@@ -141,6 +151,7 @@ int fp8_mqa_pages_update(int32_t* table, int64_t table_stride, int32_t table_col
     p.rows = rows;
     p.starts = starts;
     p.changed = changed;
+    p.aligned = on(slots, 16) && on(positions, 16) && on(rows, 16);
     p.bounds = bounds_for(*st);
     spans(p.bounds, kMemTable, table, extent(B, 4 * table_stride, table_cols, 4, 1, 0, 4));
     spans(p.bounds, kMemLens, lens, 4 * B);
@@ -152,7 +163,7 @@ int fp8_mqa_pages_update(int32_t* table, int64_t table_stride, int32_t table_col
     spans(p.bounds, kMemRows, rows, 4 * total);
     spans(p.bounds, kMemStarts, starts, 4 * (B + 1));
     spans(p.bounds, kMemOut, changed, 4 * B);
-    return launched(pages_launch(p, static_cast<cudaStream_t>(stream)));
+    return launched(pages_launch(p, st->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 int fp8_mqa_norm_rotate(const fp8mqa_heads* q, const fp8mqa_heads* k, int32_t x_type, int32_t out_type, int64_t T,

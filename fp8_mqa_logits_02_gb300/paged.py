@@ -54,7 +54,7 @@ def _binding():
             spec = importlib.util.spec_from_file_location("_paged_binding", nvcc_build.BINDING)
             _compiled = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(_compiled)
-        _compiled.bind(*entries, Fp8MqaError)
+        _compiled.bind(*entries, Fp8MqaError, PagesStep)
         _bound = _package._debug
     return _compiled
 
@@ -181,8 +181,8 @@ def pages_update(table: torch.Tensor, lens: torch.Tensor, change: torch.Tensor, 
     call = _binding().pages_update
     if stream is not None:
         with _on(stream, table):
-            return PagesStep(*call(table, lens, change, free, n_free, page_size, total))
-    return PagesStep(*call(table, lens, change, free, n_free, page_size, total))
+            return call(table, lens, change, free, n_free, page_size, total)
+    return call(table, lens, change, free, n_free, page_size, total)
 
 
 def norm_rotate(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,

@@ -470,7 +470,8 @@ FP8MQA_API uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int
  *   starts      DEVICE int32 [B + 1]: request b's new tokens are rows starts[b] .. starts[b + 1] - 1 (sums
  *               stop at 2^31 - 1).
  *   changed     DEVICE int32 [B]: by how much the length changed (0 for a request that does not fit).
- * Limits: B <= 8192 (FP8MQA_ERR_UNSUPPORTED_SHAPE), table_cols * page_size < 2^31.  Arrays do not overlap.
+ * Limits: B <= 8192, table_cols * page_size < 2^31, B * table_cols < 2^31 (FP8MQA_ERR_UNSUPPORTED_SHAPE).
+ * Arrays do not overlap.
  * The result is always the same for the same arguments.  No workspace, no allocation; may be captured
  * into a graph.
  */
