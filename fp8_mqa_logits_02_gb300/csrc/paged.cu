@@ -418,7 +418,8 @@ int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_type, const v
                         const fp8mqa_cache* cache2, void* stream)
 {
     using namespace fp8mqa;
-    if (T < 0 || (x2 == nullptr) != (cache2 == nullptr)) return FP8MQA_ERR_INVALID_ARG;
+    // (an empty tensor has no memory)
+    if (T < 0 || (x2 && !cache2) || (T > 0 && cache2 && !x2)) return FP8MQA_ERR_INVALID_ARG;
     if (x_type != FP8MQA_BF16 && x_type != FP8MQA_F16 && x_type != FP8MQA_F32)
         return FP8MQA_ERR_INVALID_ARG;
     int rc = check_cache(cache);

@@ -91,7 +91,6 @@ cudaError_t rotate_type(NormRotateParams& p, int32_t dim, bool interleaved, bool
 
 int check_heads(const fp8mqa_heads* h, int32_t x_type, int32_t out_type)
 {
-    if (!h || h->heads < 0) return FP8MQA_ERR_INVALID_ARG;
     if (h->heads == 0) return FP8MQA_OK;
     if (!h->x || !h->out || (out_type == FP8MQA_E4M3) != (h->out_scale != nullptr)) return FP8MQA_ERR_INVALID_ARG;
     if (h->weight && h->weight_type != x_type && h->weight_type != FP8MQA_F32) return FP8MQA_ERR_INVALID_ARG;
@@ -177,12 +176,14 @@ int fp8_mqa_norm_rotate(const fp8mqa_heads* q, const fp8mqa_heads* k, int32_t x_
         (out_type != x_type && out_type != FP8MQA_E4M3))
         return FP8MQA_ERR_INVALID_ARG;
     if ((dim != 64 && dim != 128) || rotated > dim || rotated % 16 != 0) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
+    if (!q || q->heads < 0 || (k && k->heads < 0)) return FP8MQA_ERR_INVALID_ARG;
+    if (T == 0) return FP8MQA_OK;  // (empty tensors have no memory)
     int rc = check_heads(q, x_type, out_type);
     if (rc == FP8MQA_OK && k) rc = check_heads(k, x_type, out_type);
     if (rc != FP8MQA_OK) return rc;
     const int64_t heads = int64_t(q->heads) + (k ? k->heads : 0);
     if (T >= int64_t(1) << 31 || T * heads >= int64_t(1) << 31) return FP8MQA_ERR_UNSUPPORTED_SHAPE;
-    if (T == 0 || heads == 0) return FP8MQA_OK;
+    if (heads == 0) return FP8MQA_OK;
     if (rotated > 0 && (!positions || !inv_freq)) return FP8MQA_ERR_INVALID_ARG;
     if (!on(positions, uintptr_t(position_bytes)) || !on(inv_freq, 4)) return FP8MQA_ERR_MISALIGNED;
     int err = FP8MQA_OK;

@@ -107,6 +107,17 @@ def test_far_positions(wide):
     check(x, got[0], None, pos, f)
 
 
+def test_no_tokens_and_no_heads():
+    x, pos = torch.empty(0, 3, 64, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")
+    q, k = fm.norm_rotate(x, x[:, :1], pos, freq(64))
+    assert q.shape == (0, 3, 64) and k.shape == (0, 1, 64)
+    (q, by), _ = fm.norm_rotate(x, None, pos, freq(64), dtype=F8)
+    assert q.shape == (0, 3, 64) and by.shape == (0, 3)
+    one = torch.ones(2, 1, 64, device="cuda")
+    q, k = fm.norm_rotate(one[:, :0], one, torch.zeros(2, dtype=torch.int32, device="cuda"), freq(64))
+    assert q.shape == (2, 0, 64) and torch.equal(k, one)
+
+
 def test_norm_without_rotation_and_rotation_without_norm():
     rng = np.random.default_rng(2)
     x = rows(rng, 9, 3, 128, torch.bfloat16)

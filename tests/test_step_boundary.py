@@ -68,6 +68,14 @@ def test_caches_in_4_bits_go_with_their_own(lib):
     assert write(P, 0, BF16, P, 128, 128, ctypes.create_string_buffer(short, len(short)), None, 0, 0, None, None) == OK
 
 
+def test_no_rows_of_a_pair(lib):
+    # empty tensors have no memory: there is nothing to do, in either type of cache
+    for c in (cache(), e4m3()):
+        assert lib.fp8_mqa_cache_write(None, 0, BF16, None, 128, 128, c, None, 128, 128, c, None) == OK
+        assert lib.fp8_mqa_cache_write(P, 3, BF16, P, 128, 128, c, None, 128, 128, c, None) == INVALID
+        assert lib.fp8_mqa_cache_write(None, 0, BF16, None, 128, 128, c, P, 128, 128, None, None) == INVALID
+
+
 def test_pages_refusals(lib):
     def f(table=P, stride=4, cols=4, page=64, lens=P, change=P, B=2, free=P, cap=9, n=P, total=5, slots=P, pos=P, rows=P,
           starts=P, changed=P):
@@ -89,6 +97,7 @@ def heads(x=P, weight=P, out=P, scale=None, row=1024, head=128, out_row=1024, ou
 def test_norm_rotate_refusals(lib):
     def f(q=None, k=None, x=BF16, to=BF16, T=3, dim=128, pos=P, wide=4, freq=P, rotated=64, inter=0, **kw):
         return lib.fp8_mqa_norm_rotate(q or heads(**kw), k, x, to, T, dim, pos, wide, freq, rotated, inter, 1e-6, None)
+    assert f(T=0, q=heads(x=None, out=None), pos=None) == OK               # empty tensors have no memory
     assert f(T=0) == f(n=0) == f(n=0, x=F16, to=F16) == OK
     assert lib.fp8_mqa_norm_rotate(None, None, BF16, BF16, 3, 128, P, 4, P, 64, 0, 1e-6, None) == INVALID
     assert f(T=-1) == f(rotated=-16) == f(inter=2) == f(wide=2) == f(n=-1) == INVALID
