@@ -1,7 +1,7 @@
 """One sparse-attention layer of a small serving loop, on the library's operators.
 
-Three requests are served from paged e4m3 caches.  The prompt's rows are quantised into the pages
-(``cache_write``), packed back and scored as a prompt chunk (``cache_read``, ``fp8_mqa_logits``);
+Three requests are served from paged e4m3 caches.  ``pages_update`` hands out pages as they grow; the
+prompt's rows are quantised into the pages (``cache_write``), packed back and scored as a prompt chunk (``cache_read``, ``fp8_mqa_logits``);
 then, token by token, a step writes the new rows, scores every cached position for the newest token
 (``logits_paged``), selects the best (``topk``) and attends to those alone (``attention_paged``).
 Run it on a GB300:
@@ -21,7 +21,7 @@ F8 = torch.float8_e4m3fn
 
 
 class Layer:
-    """The caches of one layer and their page tables.  ``pages`` are handed out as requests grow."""
+    """The caches of one layer and their page tables."""
 
     def __init__(self, requests: int, longest: int, device):
         self.cols = -(-longest // PAGE)
@@ -33,19 +33,13 @@ class Layer:
         self.index_scale = torch.zeros((pages, PAGE, 1), device=device)
         self.table = torch.full((requests, self.cols), -1, dtype=torch.int32, device=device)
         self.lens = torch.zeros(requests, dtype=torch.int32, device=device)
-        self.free = torch.randperm(pages).tolist()
+        self.free = torch.randperm(pages).to(device=device, dtype=torch.int32)
+        self.n_free = torch.full((1,), pages, dtype=torch.int32, device=device)
 
     def slots(self, new: list[int]) -> torch.Tensor:
         """Slots for ``new[b]`` further tokens of each request, one request after the other."""
-        out = []
-        for b, n in enumerate(new):
-            have = int(self.lens[b])
-            for at in range(have, have + n):
-                if at % PAGE == 0:
-                    self.table[b, at // PAGE] = self.free.pop()
-                out.append(int(self.table[b, at // PAGE]) * PAGE + at % PAGE)
-        self.lens += torch.tensor(new, dtype=torch.int32, device=self.lens.device)
-        return torch.tensor(out, dtype=torch.int32, device=self.lens.device)
+        change = torch.tensor(new, dtype=torch.int32, device=self.lens.device)
+        return fm.pages_update(self.table, self.lens, change, self.free, self.n_free, PAGE, sum(new)).slots
 
     def write(self, slots, k, v, index_keys):
         fm.cache_write(slots, k, self.k, self.k_scale, v, self.v, self.v_scale)

@@ -280,16 +280,16 @@ __global__ void __launch_bounds__(kRotateThreads, 4) norm_rotate_kernel(const __
                     nu = fmaf(-v, sv[j], nu);
                     nv = fmaf(u, su[j], nv);
                 }
-                u = nu * by[r];
-                v = nv * by[r];
+                u = kE4m3 ? nu : nu * by[r];
+                v = kE4m3 ? nv : nv * by[r];
             }
         }
-        if constexpr (kE4m3) {
+        if constexpr (kE4m3) {  // (the row's factor joins the scale's)
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                top[r] = kTinyMax;
+                top[r] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) top[r] = max_nan(top[r], fabsf(y[r][j]));
+                for (int j = 0; j < 8; j += 2) top[r] = max_nan(top[r], fabsf(y[r][j]), fabsf(y[r][j + 1]));
             }
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o /= 2)
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kRotateThreads, 4) norm_rotate_kernel(const __
             if (i + r >= n) break;
             const int kind = which ? kMemOut2 : kMemOut;
             if constexpr (kE4m3) {
-                const float inv = __fdiv_rn(kE4m3Max, top[r]);
+                const float a = max_nan(top[r] * by[r], kTinyMax), inv = by[r] * __fdiv_rn(kE4m3Max, a);
                 uint32_t four[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kRotateThreads, 4) norm_rotate_kernel(const __
                     if (in_bounds(p.bounds, kind, out + at_b, 4)) *reinterpret_cast<uint32_t*>(out + at_b) = four[1];
                 }
                 if (lane == 0 && in_bounds(p.bounds, which ? kMemOutScale2 : kMemOutScale, out_scale, 4))
-                    *out_scale = __fmul_rn(top[r], 1.0f / kE4m3Max);
+                    *out_scale = __fmul_rn(a, 1.0f / kE4m3Max);
                 ++out_scale;
             } else {
                 store8<X, kVec, kInterleaved>(p.bounds, kind, out + at_a, out + at_b, eight_of<X>(y[r]));

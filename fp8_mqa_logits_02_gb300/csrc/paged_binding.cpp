@@ -138,6 +138,10 @@ fp8mqa_cache cache_of(PyObject* data_o, PyObject* scale_o, PyObject* groups_o, c
     c.scale_page_stride = c.scale_row_stride = c.scale_head_stride = 0;
     c.groups = nullptr;
     c.group_page_stride = c.group_row_stride = c.group_head_stride = 0;
+    if (!four && dtype != at::kFloat8_e4m3fn && dtype != other)
+        bad(PyExc_TypeError, what + " data must be " + name_of(at::kFloat8_e4m3fn) +
+                                 (groups_o ? ", torch.float4_e2m1fn_x2" : "") +
+                                 (other == at::kFloat8_e4m3fn ? "" : " or " + name_of(other)) + ", got " + name_of(dtype));
     if (!four && groups_o && groups_o != Py_None)
         bad(PyExc_ValueError, what + " groups go with float4_e2m1fn_x2 data only");
     if (four) {
@@ -163,10 +167,6 @@ fp8mqa_cache cache_of(PyObject* data_o, PyObject* scale_o, PyObject* groups_o, c
         c.scale_row_stride = scale.stride(1);
         c.scale_head_stride = scale.stride(2);
     } else {
-        if (dtype != other)
-            bad(PyExc_TypeError, what + " data must be " + name_of(at::kFloat8_e4m3fn) +
-                                     (groups_o ? ", torch.float4_e2m1fn_x2" : "") + (other == at::kFloat8_e4m3fn ? "" : " or " + name_of(other)) + ", got " +
-                                     name_of(dtype));
         if (scale_o != Py_None) bad(PyExc_ValueError, what + " scale goes with float8_e4m3fn" +
                                                    std::string(groups_o ? " or float4_e2m1fn_x2" : "") + " data only");
     }

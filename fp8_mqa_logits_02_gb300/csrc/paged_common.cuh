@@ -216,6 +216,14 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// The largest of three, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Asynchronous copies into shared memory; what is not there is filled with zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
 {
