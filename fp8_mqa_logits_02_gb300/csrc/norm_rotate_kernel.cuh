@@ -14,14 +14,10 @@
 // shared memory at once, and keeps the sines' and cosines' products with the weights in registers; a block's
 // tokens share a table of sines and cosines, made by all of its threads while the rows are on their way.
 //
-// Measured: 16384 tokens x 40 heads of 128 in bfloat16 (336 MB) 53.7 us, 6.2 TB/s of 6.8; with rows loaded straight
-// into registers 82, heads of both tensors in one group 64.  8192 tokens x 32 heads to E4M3 (102 MB) 25.9 us, where
-// the instructions decide (72 % of the issue slots).
-//
-// Far positions: a product position * inv_freq of 10^5 has no correct digit past the fifth in 32 bits.
-// The frequency is taken as a 64-bit fraction of a turn, so that its product with an integer position wraps
-// around by itself; what is left is under half a turn, exact to 32 bits of it.  (In integers: the fp64 units
-// are few, and made 16384 tokens x 40 heads take 107 us with one product, floor and conversion a pair.)
+// Measured: 16384 tokens x 40 heads of 128 in bfloat16 (336 MB) 53.4 us, 6.3 TB/s of 6.8; with rows loaded straight
+// into registers 82, heads of both tensors in one group 64.  8192 tokens x 32 heads to E4M3 (102 MB) 25.1 us, where
+// the instructions decide (74 % of the issue slots); twice as many values a lane, with a third fewer instructions, took
+// 25.6, since the registers leave fewer warps.
 #pragma once
 
 #include <type_traits>
@@ -31,10 +27,10 @@
 
 namespace fp8mqa {
 
-constexpr int kRotateThreads = 256;
+constexpr int kRotateThreads = 128;
 
-// Heads of a group of lanes, at most, and the shared memory for `rows` of each: with the table, what a kernel gets
-// unasked (48 KB).
+// Heads of a group of lanes, at most, and the shared memory for `rows` of each: eight blocks of an SM have room for
+// 10 of 16 bits (16 take 59 us where 10 take 53, 4 take 63).
 template <class X>
 constexpr int kRotateHeads = 20 / int(sizeof(X));
 template <class X>
@@ -143,7 +139,7 @@ __device__ __forceinline__ void store8(const PagedBounds& bounds, int kind, X* a
 // X: x's type.  kE4m3: the result is E4M3 with scales, else of x's type.  kVec: x, its weights and the result lie on
 // 16 bytes (E4M3: on 8).  kInterleaved: how values pair, side by side or apart.
 template <class X, int kDim, bool kE4m3, bool kVec, bool kInterleaved>
-__global__ void __launch_bounds__(kRotateThreads, 4) norm_rotate_kernel(const __grid_constant__ NormRotateParams p)
+__global__ void __launch_bounds__(kRotateThreads, 8) norm_rotate_kernel(const __grid_constant__ NormRotateParams p)
 {
     constexpr int kLanes = kDim / 8, kGroups = kRotateThreads / kLanes;
     constexpr int kRows = 2;  // worked on at once

@@ -458,6 +458,12 @@ PyObject* pages_update(PyObject* const* a, Py_ssize_t n)
     return result;
 }
 
+// Whether n0 blocks of n1 rows of `dim` values, at strides s0 and s1, follow one another without overlapping.
+bool apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t dim)
+{
+    return (n1 <= 1 || s1 >= dim) && (n0 <= 1 || s0 >= (n1 > 0 ? (n1 - 1) * s1 : 0) + dim);
+}
+
 // q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, q_out, k_out
 PyObject* norm_rotate(PyObject* const* a, Py_ssize_t n)
 {
@@ -528,8 +534,8 @@ PyObject* norm_rotate(PyObject* const* a, Py_ssize_t n)
                 o.stride(2) != 1)
                 bad(PyExc_ValueError, name + "_out must be " + name_of(type) + " " + list(x.sizes()) +
                                           ", contiguous in its last dimension");
-            // written: nothing of it may overlap
-            if ((T > 1 && o.stride(0) < dim) || (x.size(1) > 1 && o.stride(1) < dim))
+            // written: no two rows may overlap
+            if (!apart(T, o.stride(0), x.size(1), o.stride(1), dim) && !apart(x.size(1), o.stride(1), T, o.stride(0), dim))
                 bad(PyExc_ValueError, name + "_out must not overlap");
             given[i] = a[9 + i];
             h.out = o.data_ptr();

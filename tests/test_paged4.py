@@ -4,6 +4,8 @@ cache_write and cache_read are exact: every step is defined in fp32.  attention_
 caches (test_paged.py): a value's data * group is exact in the 16 bits that are multiplied, so it is the
 scores' fp32 sums, the weights' 11 bits and the result's rounding again.
 """
+import struct
+
 import numpy as np
 import pytest
 import torch
@@ -75,6 +77,13 @@ def test_write_pair_is_exact(T, heads, dim, page, dtype):
     slots = rng.permutation(pages * page)[:T].astype(np.int32)
     slots[::5] = [-1, pages * page, -2 ** 31, 2 ** 31 - 1][T % 4]  # padding and slots out of range
     check_write(qkv[:, 1:1 + heads], slots, caches, qkv[:, 2 + heads:2 + 2 * heads])
+
+
+def test_write_pair_into_caches_of_two_layouts():
+    rng = np.random.default_rng(21)
+    x = torch.from_numpy(rng.standard_normal((50, 8, 128))).to(torch.float16).cuda()
+    caches = [cache(rng, 5, 24, 4, 128, layout="heads"), cache(rng, 5, 24, 4, 128, layout="joint")]
+    check_write(x[:, :4], rng.permutation(120)[:50].astype(np.int32), caches, x[:, 4:])
 
 
 @pytest.mark.parametrize("layout", ["joint", "heads"])
@@ -164,6 +173,27 @@ def test_read_is_exact(lens, heads, dim, page, layout, dtype):
     assert torch.equal(got.cpu(), torch.from_numpy(want * by[..., None]).to(dtype))
 
 
+@pytest.mark.parametrize("kind,dtype", [(1, torch.bfloat16), (2, torch.float16), (3, torch.float32)])
+def test_read_to_16_bytes(kind, dtype):
+    # through the C entry, whose results lie on 16 bytes and need not on 32
+    rng = np.random.default_rng(22)
+    table, pages = tables(rng, [70, 9], 16)
+    c = cache(rng, pages, 16, 2, 64)
+    starts = gpu(np.array([0, 70, 79], np.int32))
+    want = fm.cache_read(c[0].view(F4), c[2], gpu(table), starts, 79, dtype=dtype, groups=c[1])
+    to = torch.full((79 * 128 + 64,), 5.0, dtype=dtype, device="cuda")
+    at = 16 // to.element_size()
+    st = [s for t in (c[0], c[2]) for s in t.stride()[:3]]
+    struct_ = struct.pack("@PPqiiiiqqqqqqPqqq", c[0].data_ptr(), c[2].data_ptr(), pages, 16, 2, 64, 4, *st, c[1].data_ptr(),
+                          *c[1].stride()[:3])
+    t = gpu(table)
+    assert fm.lib().fp8_mqa_cache_read(struct_, t.data_ptr(), t.stride(0), t.shape[1], starts.data_ptr(), 2, 79, kind,
+                                       to.data_ptr() + 16, None, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(to[at:at + 79 * 128].view(79, 2, 64), want)
+    assert (to[:at] == 5).all() and (to[at + 79 * 128:] == 5).all()
+
+
 # ------------------------------------------------------------------------------------ attention
 
 def close(got, lse, want, wlse, size, dots, dtype):
@@ -181,14 +211,14 @@ def close(got, lse, want, wlse, size, dots, dtype):
 
 
 def check_attention(rng, lens, q_heads, heads, dim, page, dtype=torch.bfloat16, layout="plain", select=None, holes=False,
-                    fused=False, shared=False, sharp=1.0, spread=None, cols=None, negative=False, sm=None):
+                    fused=False, shared=False, sharp=1.0, spread=None, cols=None, negative=False, sm=None, v_layout=None):
     lens = np.asarray(lens, np.int32)
     B = len(lens)
     table, pages = tables(rng, lens[:1] if shared else lens, page, cols=cols)
     if holes:
         table[0, -1] = -7
         table[-1, 0] = pages
-    k, v = (cache(rng, pages, page, heads, dim, layout) for _ in range(2))
+    k, v = cache(rng, pages, page, heads, dim, layout), cache(rng, pages, page, heads, dim, v_layout or layout)
     if spread is not None:
         v[2].mul_(torch.from_numpy(np.exp(spread * rng.standard_normal(tuple(v[2].shape))).astype(np.float32)).cuda())
     if negative:
@@ -251,6 +281,50 @@ def test_attention_layouts_holes_and_selected(dim, dtype):
     check_attention(rng, [300, 129, 10], 8, 4, dim, 32, dtype, layout="heads", holes=True, select=64)
     check_attention(rng, [900] * 5, 8, 2, dim, 48, dtype, select=513, shared=True)
     check_attention(rng, [500, 0, 3], 4, 1, dim, 16, dtype, select=1)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_keys_and_values_of_two_layouts(dim, page):
+    rng = np.random.default_rng(23)
+    check_attention(rng, [300, 129, 10], 8, 4, dim, page, layout="heads", v_layout="plain")
+    check_attention(rng, [300, 129, 10], 8, 4, dim, page, layout="joint", v_layout="heads", select=64, holes=True)
+    check_attention(rng, [3000], 32, 1, dim, page, layout="plain", v_layout="joint")
+
+
+def test_attention_without_pages_or_columns():
+    f = lambda *n: torch.zeros(n, dtype=torch.uint8, device="cuda")  # noqa: E731
+    q = torch.ones(2, 4, 128, device="cuda").bfloat16()
+    lens = gpu(np.array([5, 0], np.int32))
+    for pages, cols in ((0, 3), (2, 0)):
+        data, groups, scale = f(pages, 32, 2, 64).view(F4), f(pages, 32, 2, 8).view(F8), torch.ones(pages, 32, 2, device="cuda")
+        for indices in (None, torch.zeros(2, 9, dtype=torch.int32, device="cuda")):
+            out, lse = fm.attention_paged(q, data, data, torch.zeros(2, cols, dtype=torch.int32, device="cuda"), lens, k_scale=scale,
+                                          v_scale=scale, k_groups=groups, v_groups=groups, indices=indices, return_lse=True)
+            assert (out == 0).all() and lse.isneginf().all()
+        rows = fm.cache_read(data, scale, torch.zeros(2, cols, dtype=torch.int32, device="cuda"),
+                             torch.tensor([0, 5, 5], dtype=torch.int32, device="cuda"), 5, dtype=torch.float32, groups=groups)
+        assert (rows == 0).all()
+        fm.cache_write(torch.zeros(3, dtype=torch.int32, device="cuda") + 64, torch.ones(3, 2, 128, device="cuda"), data, scale,
+                       k_groups=groups)
+
+
+def test_attention_captured_and_replayed():
+    rng = np.random.default_rng(24)
+    table, pages = tables(rng, [500, 64, 1], 64)
+    k, v = cache(rng, pages, 64, 2, 128), cache(rng, pages, 64, 2, 128)
+    q, t, lens = torch.zeros(3, 8, 128, device="cuda").bfloat16(), gpu(table), gpu(np.array([1, 1, 1], np.int32))
+    call = lambda: fm.attention_paged(q, k[0].view(F4), v[0].view(F4), t, lens, k_scale=k[2], v_scale=v[2],  # noqa: E731
+                                      k_groups=k[1], v_groups=v[1], return_lse=True)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for n in ([500, 64, 1], [0, 33, 1], [499, 0, 0]):
+        lens.copy_(gpu(np.array(n, np.int32)))
+        q.copy_(torch.from_numpy(rng.standard_normal((3, 8, 128))))
+        graph.replay()
+        close(*got, *plain.attention(f64(q), as_rows(k), as_rows(v), table, n, 128 ** -0.5), q.dtype)
 
 
 def test_attention_split_and_joined():

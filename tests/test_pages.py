@@ -152,6 +152,25 @@ def test_captured_and_replayed():
         assert np.array_equal(both.gpu[1].cpu().numpy(), n) and np.array_equal(both.gpu[2].cpu().numpy(), free)
 
 
+def test_a_large_step_captured_and_replayed():
+    # many CTAs for the tokens, and the lengths by a kernel of their own
+    rng = np.random.default_rng(7)
+    both = Both(*state(rng, [0, 100, 31], 32, 900, 2500), 32)
+    change = gpu([0, 0, 0])
+    fm.pages_update(*both.gpu[:2], change, *both.gpu[2:], 32, 20000)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fm.pages_update(*both.gpu[:2], change, *both.gpu[2:], 32, 20000)
+    for new in ([9000, 7000, 1], [1, 1, 1], [-9001, 3000, -33], [20000, 20000, 30000], [0, 0, 0]):
+        change.copy_(gpu(new))
+        graph.replay()
+        t, n, free, n_free = both.plain
+        both.plain[3], *want = plain.pages(t, n, new, free, n_free, 32, 20000)
+        assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, want))
+        assert both.gpu[3].item() == both.plain[3] and np.array_equal(both.gpu[0].cpu().numpy(), t)
+        assert np.array_equal(both.gpu[1].cpu().numpy(), n) and np.array_equal(both.gpu[2].cpu().numpy(), free)
+
+
 def test_on_another_stream():
     rng = np.random.default_rng(6)
     both = Both(*state(rng, [100] * 40, 16, 30, 300), 16)

@@ -82,6 +82,9 @@ def test_norm_rotate_refusals():
     raises(ValueError, "does not go with", lambda: f(dtype=F8, q_out=x.clone()))
     raises(ValueError, "q_out must be", lambda: f(q_out=x.float()))
     raises(ValueError, "overlap", lambda: f(q_out=x[:1].expand(3, 2, 128)))
+    raises(ValueError, "overlap", lambda: f(q_out=torch.zeros(1024, device="cuda").bfloat16().as_strided((3, 2, 128), (128, 128, 1))))
+    by_heads = torch.zeros(2, 3, 128, device="cuda", dtype=torch.bfloat16).transpose(0, 1)
+    assert torch.equal(f(q_out=by_heads)[0], f()[0])
     raises(ValueError, "CUDA", lambda: f(q=x.cpu()))
     raises(ValueError, "CUDA", lambda: f(freq=torch.zeros(64)))
 
