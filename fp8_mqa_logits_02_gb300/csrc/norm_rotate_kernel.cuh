@@ -259,12 +259,11 @@ __global__ void __launch_bounds__(kRotateThreads, 8) norm_rotate_kernel(const __
                 by[r] = fmaf(y[r][j], y[r][j], by[r]);
             }
         }
-        if (norm) {
+        // (without a weight too: a warp's groups may be of both tensors, and all its lanes exchange)
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o /= 2)
+        for (int o = kLanes / 2; o > 0; o /= 2)
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) by[r] += __shfl_xor_sync(~0u, by[r], o);
-        }
+            for (int r = 0; r < kRows; ++r) by[r] += __shfl_xor_sync(~0u, by[r], o);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
             by[r] = norm ? rsqrtf(fmaf(by[r], 1.0f / kDim, p.eps)) : 1.0f;

@@ -92,6 +92,21 @@ def test_many_heads_a_group(dtype):
         check(x[:, 18:], got[1], None, pos, freq(64), dtype=out)
 
 
+@pytest.mark.parametrize("out", [None, F8])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,hq,hk,dim", [(1, 1, 1, 64), (1, 1, 1, 128), (5, 3, 2, 64), (5, 2, 1, 128), (1500, 17, 3, 64)])
+def test_a_norm_of_one_tensor(T, hq, hk, dim, dtype, out):
+    # groups of lanes of one warp, of which some norm their heads and others do not
+    rng = np.random.default_rng(T + dim)
+    q, k = rows(rng, T, hq, dim, dtype), rows(rng, T, hk, dim, dtype)
+    pos = torch.from_numpy(rng.integers(0, 200000, T).astype(np.int32)).cuda()
+    w = torch.from_numpy(rng.standard_normal(dim)).to(dtype).cuda()
+    for wq, wk in ((w, None), (None, w)):
+        got = fm.norm_rotate(q, k, pos, freq(dim), wq, wk, dtype=out)
+        check(q, got[0], wq, pos, freq(dim), dtype=out)
+        check(k, got[1], wk, pos, freq(dim), dtype=out)
+
+
 @pytest.mark.parametrize("wide", [torch.int32, torch.int64])
 def test_far_positions(wide):
     rng = np.random.default_rng(1)
