@@ -185,13 +185,13 @@ __global__ void __launch_bounds__(kPagesThreads) pages_update_kernel(const __gri
         const int32_t i = int32_t(i0), b = i0 < all ? last_at_most(s_tokens, p.B, i) : 0;
         const int32_t at = i0 < all ? s_len[b] + (i - s_tokens[b]) : 0;  // (one that does not fit: below 0, or not looked at)
         const int32_t col = p.by_page.of(max(at, 0)), in_page = at - col * p.page_size;
-        if (i0 + 4 <= all && i0 + 4 <= s_tokens[b + 1] && s_len[b] >= 0 && in_page + 4 <= p.page_size) {
-            const int32_t page = page_of(b, col);
-            const int64_t x = int64_t(page) * p.page_size + in_page;
-            const bool ok = page >= 0 && x + 3 <= INT32_MAX;
+        if (i0 + 4 <= all && i0 + 4 <= s_tokens[b + 1] && s_len[b] >= 0 && p.page_size >= 4) {
+            // of one request, on one page or two
+            const int32_t page = page_of(b, col), left = p.page_size - in_page;  // tokens on the first page
+            const int32_t next = left < 4 ? page_of(b, col + 1) : page;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                slot[k] = ok ? int32_t(x) + k : slot_of(page, in_page + k);
+                slot[k] = k < left ? slot_of(page, in_page + k) : slot_of(next, k - left);
                 position[k] = at + k;
                 row[k] = b;
             }
