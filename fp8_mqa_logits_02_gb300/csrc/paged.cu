@@ -634,8 +634,7 @@ int fp8_mqa_attention_paged(const void* q, int32_t q_type, int64_t B, int32_t q_
         p.same_rows = alike(p.k_units, p.v_units) && alike(p.k_group_units, p.v_group_units) &&
                       alike(p.k_scale_units, p.v_scale_units);
         // (a step is 32 positions, and begins at a multiple of that)
-        p.whole_steps = n_indices < 0 && k->page_size % 32 == 0 &&
-                        p.k.row_stride < INT32_MAX / k->page_size && p.v.row_stride < INT32_MAX / k->page_size;
+        p.whole_steps = n_indices < 0 && k->page_size % 32 == 0 && p.same_rows;
     }
     p.table = {table, table_stride, table_cols, FastDiv(uint32_t(k->page_size))};
     p.lens = lens;

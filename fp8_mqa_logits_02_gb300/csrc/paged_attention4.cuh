@@ -7,8 +7,9 @@
 //               two values, 256 a step.  K's lanes have 32 (16) values of a row side by side, whole groups;
 //               V's have a group's columns of four rows, whose halves of a byte change places so that one
 //               conversion gives a column of two rows.
-//   copies      a step whose positions share a page (pages of 32, 64, ... rows, every position) has its
-//               addresses by additions to the lane's own; the others find each row, as E4M3 steps do.
+//   copies      where a step's positions share a page (pages of 32, 64, ... rows, every position) the pages of 32
+//               steps are looked up at once and a row is some units on from the step's first; the others find each
+//               row, as E4M3 steps do.  (Both ways in one loop cost 9 us of 149: the registers of each.)
 //   softmax     the weights are computed with the references as they are, which may lag behind the largest
 //               score by 2^kAttnLag and more; only where one comes out too large for f16 does the warp look for
 //               the largest score, and computes them again.
@@ -36,7 +37,14 @@ __device__ __forceinline__ uint32_t twice(uint32_t x)
     return r;
 }
 
+// Whether a warp looks up the pages of 32 steps at once where their positions share them.  Not for 16 heads, whose
+// registers are short (of 131072 positions 23.4 us with it, 22.5 without; of a batch with 8 heads a warp 149 and 154).
 template <class S>
+constexpr bool kWholeSteps = S::kNT == 1;
+
+// kWhole: the positions of a step share a page (pages of 32, 64, ... rows, no list of positions), and K's and V's
+// strides are alike.
+template <bool kWhole, class S>
 __device__ __forceinline__ void attn_steps4(const PagedAttentionParams& p, const AttnRows& rows, const AttnPart& part,
                                             uint8_t* ring, AttnSums<S>& sums)
 {
@@ -72,9 +80,8 @@ __device__ __forceinline__ void attn_steps4(const PagedAttentionParams& p, const
         }
     }
 
-    // ---- finding a step's rows.  Lane i has position i of it; without a list of positions and with whole steps a
-    // page, lane 0's page is everyone's.  (A list is read two steps ahead: its load, the table's and the rows' copies
-    // hang on one another.)
+    // ---- finding a step's rows: lane i has its i-th position.  (A list is read two steps ahead: its load, the table's
+    // and the rows' copies hang on one another.)
     const int32_t* const table = p.table.ids + part.b * p.table.stride;
     const int32_t* const listed_at = p.indices + part.b * p.indices_stride;
     int32_t page = -1, row = 0, listed = -1;
@@ -94,15 +101,19 @@ __device__ __forceinline__ void attn_steps4(const PagedAttentionParams& p, const
         if (p.n_indices >= 0) list(i + tile);
     };
 
-    // ---- copying what find() found into a stage.  A lane's own part of the addresses: row lane / kPieces and piece
+    // ---- copying a step's rows into a stage.  A lane's own part of the addresses: row lane / kPieces and piece
     // lane % kPieces of the data, row `lane` of the scales
     const int piece = lane % S::kPieces, first = warp % kHq * kPer + lane / S::kPieces;
     const uint8_t* const k_lane = p.k.data + kvh * p.k.head_stride + 16 * piece;
+    const uint8_t* const v_lane = p.v.data + kvh * p.v.head_stride + 16 * piece;
     const uint8_t* const k_groups = p.k.groups + kvh * p.k.group_head_stride;
+    const uint8_t* const v_groups = p.v.groups + kvh * p.v.group_head_stride;
     const float* const k_scales = p.k.scale + kvh * p.k.scale_head_stride;
-    const int64_t v_lane = p.v.data + kvh * p.v.head_stride + 16 * piece - k_lane;  // from K's to V's
-    const int64_t v_groups = p.v.groups + kvh * p.v.group_head_stride - k_groups;
-    const int64_t v_scales = p.v.scale + kvh * p.v.scale_head_stride - k_scales;
+    const float* const v_scales = p.v.scale + kvh * p.v.scale_head_stride;
+    auto far = [&](const RowUnits& u, uint32_t at) { return uint64_t(at) * u.unit; };
+    // (of steps that keep to a page, where V's addresses are K's and the way from one to the other)
+    const uint8_t* const k_own = k_lane + far(p.k_units, first * p.k_units.row);
+    const int64_t v_data_on = v_lane - k_lane, v_groups_on = v_groups - k_groups, v_scales_on = v_scales - k_scales;
     auto data = [&](uint32_t to, int r, const uint8_t* k, const uint8_t* v, bool ok) {
         copy16(to + 16 * k_place<S::kPieces>(r, piece), k, ok && in_bounds(p.bounds, kMemData, k, 16));
         copy16(to + S::kRows + 16 * v_place4<S::kPieces>(r, piece), v, ok && in_bounds(p.bounds, kMemData2, v, 16));
@@ -117,52 +128,103 @@ __device__ __forceinline__ void attn_steps4(const PagedAttentionParams& p, const
         copy4(to + S::kScales + 8 * lane, ks, ok && in_bounds(p.bounds, kMemScale, ks, 4));  // side by side
         copy4(to + S::kScales + 8 * lane + 4, vs, ok && in_bounds(p.bounds, kMemScale2, vs, 4));
     };
-    auto copy = [&](int stage) {
+    auto copy = [&](int stage) {  // what find() found
         const bool there = uint32_t(page) < uint32_t(p.k.pages);
         const uint32_t here = __ballot_sync(~0u, there);
         const uint32_t to = ring_at + stage * S::kStage;
         const uint32_t pg = there ? page : 0, rw = there ? row : 0;
         auto at = [&](const RowUnits& u) { return pg * u.page + rw * u.row; };
-        auto far = [&](const RowUnits& u, uint32_t at) { return uint64_t(at) * u.unit; };
-        const uint32_t k_at = at(p.k_units);
-        if (p.whole_steps && p.same_rows && here == ~0u) {
-            const uint32_t pitch = p.k_units.row * p.k_units.unit, step = kPer * kHq * pitch;  // (a page is under 2^31)
-            const uint8_t* k = k_lane + far(p.k_units, __shfl_sync(~0u, k_at, 0)) + first * pitch;
+        const uint32_t k_at = at(p.k_units), v_at = at(p.v_units);
+        if (!kWholeSteps<S> && p.whole_steps && here == ~0u) {
+            const uint64_t step = far(p.k_units, kPer * kHq * p.k_units.row);
+            const uint8_t* k = k_own + far(p.k_units, __shfl_sync(~0u, k_at, 0));
 #pragma unroll
-            for (int j = 0; j < S::kStep / kPer / kHq; ++j, k += step) data(to, first + j * kHq * kPer, k, k + v_lane, true);
+            for (int j = 0; j < S::kStep / kPer / kHq; ++j, k += step) data(to, first + j * kHq * kPer, k, k + v_data_on, true);
         } else {
-            const uint32_t v_at = at(p.v_units);
 #pragma unroll
             for (int j = 0; j < S::kStep / kPer / kHq; ++j) {
                 const int r = first + j * kHq * kPer;
                 const uint32_t k_row = __shfl_sync(~0u, k_at, r), v_row = __shfl_sync(~0u, v_at, r);
-                data(to, r, k_lane + far(p.k_units, k_row), k_lane + v_lane + far(p.v_units, v_row), here >> r & 1u);
+                data(to, r, k_lane + far(p.k_units, k_row), v_lane + far(p.v_units, v_row), here >> r & 1u);
             }
         }
         if (warp % kHq == 0) {
-            const uint8_t* const kg = k_groups + far(p.k_group_units, at(p.k_group_units));
-            const float* const ks = k_scales + far(p.k_scale_units, at(p.k_scale_units));
-            if (p.same_rows)
-                scales(to, kg, kg + v_groups, ks, ks + v_scales, there);
-            else
-                scales(to, kg, k_groups + v_groups + far(p.v_group_units, at(p.v_group_units)), ks,
-                       k_scales + v_scales + far(p.v_scale_units, at(p.v_scale_units)), there);
+            auto of = [&](auto* from, const RowUnits& u) { return from + far(u, at(u)); };
+            scales(to, of(k_groups, p.k_group_units), of(v_groups, p.v_group_units), of(k_scales, p.k_scale_units),
+                   of(v_scales, p.v_scale_units), there);
+            if (lane == 0) *reinterpret_cast<uint32_t*>(ring + stage * S::kStage + S::kThere) = here;
+        }
+    };
+
+    // ---- both where steps keep to a page: lane i has the page of the warp's i-th next step, 32 steps ahead, and where
+    // the step's first row lies
+    const uint8_t* const groups_own = k_groups + far(p.k_group_units, lane * p.k_group_units.row);
+    const float* const scales_own = k_scales + far(p.k_scale_units, lane * p.k_scale_units.row);
+    uint32_t at_data = 0, at_group = 0, at_scale = 0, valid = 0;
+    int turn = 0;
+    auto look = [&](int32_t i) {
+        const uint32_t n = uint32_t(i) + uint32_t(lane * tile);  // (past 2^31 perhaps)
+        page = -1;
+        if (n < uint32_t(step_end)) {
+            const int32_t* const from = table + p.table.by_page.of(int32_t(n));
+            if (in_bounds(p.bounds, kMemTable, from, 4)) page = *from;
+        }
+    };
+    auto find_whole = [&](int32_t i) {
+        const bool there = uint32_t(page) < uint32_t(p.k.pages);
+        const uint32_t n = min(uint32_t(i) + uint32_t(lane * tile), uint32_t(step_end));
+        const uint32_t pg = there ? page : 0, rw = there ? n - p.table.by_page.of(int32_t(n)) * p.k.page_size : 0;
+        auto at = [&](const RowUnits& u) { return pg * u.page + rw * u.row; };
+        at_data = at(p.k_units);
+        at_group = at(p.k_group_units);
+        at_scale = at(p.k_scale_units);
+        valid = __ballot_sync(~0u, there);
+        turn = 0;
+        look(i + 32 * tile);
+    };
+    auto copy_whole = [&](int stage, int32_t i) {
+        const uint32_t to = ring_at + stage * S::kStage;
+        const uint32_t left = uint32_t(step_end - i);
+        const uint32_t here = !(valid >> turn & 1u) ? 0u : left < 32u ? ~(~0u << left) : ~0u;
+        uint32_t row_at = __shfl_sync(~0u, at_data, turn);
+#pragma unroll
+        for (int j = 0; j < S::kStep / kPer / kHq; ++j, row_at += kPer * kHq * p.k_units.row) {
+            const int r = first + j * kHq * kPer;
+            const uint8_t* const k = k_own + far(p.k_units, row_at);
+            data(to, r, k, k + v_data_on, here >> r & 1u);
+        }
+        if (warp % kHq == 0) {
+            const uint8_t* const group = groups_own + far(p.k_group_units, __shfl_sync(~0u, at_group, turn));
+            const float* const scale = scales_own + far(p.k_scale_units, __shfl_sync(~0u, at_scale, turn));
+            scales(to, group, group + v_groups_on, scale, scale + v_scales_on, here >> lane & 1u);
             if (lane == 0) *reinterpret_cast<uint32_t*>(ring + stage * S::kStage + S::kThere) = here;
         }
     };
 
     int32_t i0 = part.lo * tile + warp / side * S::kStep;  // the step being computed
     int32_t ahead = i0;                                    // the step that find() found
-    if (p.n_indices >= 0) list(ahead);
-    find(ahead);
-#pragma unroll 1
-    for (int j = 0; j < S::kStages - 1; ++j) {
+    if constexpr (kWhole) {
+        look(ahead);
+        find_whole(ahead);
+    } else {
+        if (p.n_indices >= 0) list(ahead);
+        find(ahead);
+    }
+    auto fill = [&](int stage) {
         if (ahead < step_end) {
-            copy(j);
-            find(ahead += tile);
+            if constexpr (kWhole) {
+                copy_whole(stage, ahead);
+                ahead += tile;
+                if (++turn == 32) find_whole(ahead);
+            } else {
+                copy(stage);
+                find(ahead += tile);
+            }
         }
         copy_commit();
-    }
+    };
+#pragma unroll 1
+    for (int j = 0; j < S::kStages - 1; ++j) fill(j);
 
     // ---- Q as f16 B fragments, each head brought to a largest magnitude of 2^12 .. 2^13 by a power of two (what then
     // falls below f16's range is under 2^-36 of the largest), and each head's factor of the scores, in powers of two
@@ -221,11 +283,7 @@ __device__ __forceinline__ void attn_steps4(const PagedAttentionParams& p, const
         // are there, and all are done with the stage that the next ones fill
         if (kHq > 1) copy_wait<S::kStages - 2>();
         if (kHq > 1) __syncthreads();  // (two key heads side by side need none: 166 us with it, 155 without)
-        if (ahead < step_end) {
-            copy((stage + S::kStages - 1) % S::kStages);
-            find(ahead += tile);
-        }
-        copy_commit();
+        fill((stage + S::kStages - 1) % S::kStages);
         if (i0 >= step_end || (kHq > 1 && part.n_heads <= 0)) continue;
         if (kHq == 1) {
             copy_wait<S::kStages - 1>();

@@ -35,7 +35,7 @@ struct PagedAttentionParams {
     PagedView k, v;
     RowUnits k_units, v_units;
     int32_t same_rows;  // k_units and v_units are alike (E2M1: those of groups and scales too)
-    // E2M1: of the groups' and the rows' scales, and whether a step's positions always share a page
+    // E2M1: of the groups' and the rows' scales, and whether a step's positions always share a page (with same_rows)
     RowUnits k_group_units, v_group_units, k_scale_units, v_scale_units;
     int32_t whole_steps;
     int32_t hw;         // key heads that a CTA's warps take: 1 or 2

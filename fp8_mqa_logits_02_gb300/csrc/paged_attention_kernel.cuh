@@ -491,8 +491,9 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         const int32_t lo = at - row_start, hi = min(n_tiles, end - row_start);
         AttnSums<S> r;
         const AttnPart part{b, lo, hi, kvh * group + h_first, n_heads, kvh, hw, tile};
-        if constexpr (S::kE2m1) attn_steps4<S>(p, rows, part, ring, r);
-        else attn_steps<S>(p, rows, part, ring, r);
+        if constexpr (!S::kE2m1) attn_steps<S>(p, rows, part, ring, r);
+        else if (kWholeSteps<S> && p.whole_steps) attn_steps4<kWholeSteps<S>>(p, rows, part, ring, r);
+        else attn_steps4<false>(p, rows, part, ring, r);
 
         // ---- the warps' results, joined in shared memory
         // [heads][dim], where the rings were

@@ -218,6 +218,9 @@ def check_attention(rng, lens, q_heads, heads, dim, page, dtype=torch.bfloat16, 
     if holes:
         table[0, -1] = -7
         table[-1, 0] = pages
+    if holes == "many":
+        at = rng.permutation(table.shape[1])[:table.shape[1] // 5]
+        table[:, at] = rng.choice([-1, pages, 2 ** 31 - 1], len(at))
     k, v = cache(rng, pages, page, heads, dim, layout), cache(rng, pages, page, heads, dim, v_layout or layout)
     if spread is not None:
         v[2].mul_(torch.from_numpy(np.exp(spread * rng.standard_normal(tuple(v[2].shape))).astype(np.float32)).cuda())
@@ -333,6 +336,14 @@ def test_attention_split_and_joined():
     check_attention(rng, [40000, 1, 20001], 32, 2, 64, 128)
     check_attention(rng, [9001, 3, 0, 5000], 16, 4, 128, 100)
     check_attention(rng, list(rng.integers(0, 300, 500)), 4, 2, 128, 16)
+
+
+@pytest.mark.parametrize("holes", [False, "many"])
+@pytest.mark.parametrize("page", [32, 64, 160])
+def test_attention_of_many_steps_a_warp(page, holes):
+    # a warp looks up the pages of 32 steps at once: twice or more here (rows share their pages)
+    lens = np.r_[np.full(60, 26000), 25999, 25001, 0, 33]
+    check_attention(np.random.default_rng(page), lens, 2, 2, 64, page, shared=True, holes=holes)
 
 
 def test_attention_sharp_scores_and_wide_scales():
