@@ -428,7 +428,7 @@ PyObject* pages_update(PyObject* const* a, Py_ssize_t n)
     const long long total = PyLong_AsLongLong(a[6]);
     if (total == -1 && PyErr_Occurred()) throw Raised{};
     if (page < 1 || page > INT32_MAX) bad(PyExc_ValueError, "page_size must be 1 or more");
-    if (total < 0) bad(PyExc_ValueError, "total must not be negative");
+    if (total < 0 || total > INT32_MAX) bad(PyExc_ValueError, "total must be 0 or more, and under 2^31");
     if (B > 1 && table.stride(0) < cols) bad(PyExc_ValueError, "the rows of table must not overlap: they are written");
     const c10::cuda::CUDAGuard guard(device);
     // one allocation for the five results, each on 16 bytes: five of them took half of the call

@@ -32,6 +32,15 @@ def ints(*shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("total", [2 ** 31, 2 ** 61, 2 ** 62, 2 ** 63 - 1])
+def test_more_new_tokens_than_are_counted_are_refused_before_anything_is_allocated(total):
+    fm.build()
+    held = torch.cuda.memory_reserved()
+    raises(ValueError, "total", lambda: fm.pages_update(ints(2, 4), ints(2), ints(2), ints(9), ints(1), 64, total))
+    assert torch.cuda.memory_reserved() - held < 1 << 30
+
+
+@pytest.mark.gpu
 def test_pages_update_refusals():
     fm.build()
 
