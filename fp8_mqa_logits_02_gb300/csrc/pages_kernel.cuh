@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_update_kernel(const __gri
         }
     }
     if (p.state) {
+        __syncwarp();  // the lanes had different numbers of tokens and pages
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (blockIdx.x == gridDim.x - 1) {
             for (int32_t b = b0; b < b1; ++b) {
