@@ -162,8 +162,8 @@ __device__ __forceinline__ void attn_steps4(const PagedAttentionParams& p, const
     const float* const scales_own = k_scales + far(p.k_scale_units, lane * p.k_scale_units.row);
     uint32_t at_data = 0, at_group = 0, at_scale = 0, valid = 0;
     int turn = 0;
-    auto look = [&](int32_t i) {
-        const uint32_t n = uint32_t(i) + uint32_t(lane * tile);  // (past 2^31 perhaps)
+    auto look = [&](uint32_t i) {
+        const uint32_t n = i + uint32_t(lane * tile);  // (past 2^31 perhaps)
         page = -1;
         if (n < uint32_t(step_end)) {
             const int32_t* const from = table + p.table.by_page.of(int32_t(n));
@@ -180,7 +180,7 @@ __device__ __forceinline__ void attn_steps4(const PagedAttentionParams& p, const
         at_scale = at(p.k_scale_units);
         valid = __ballot_sync(~0u, there);
         turn = 0;
-        look(i + 32 * tile);
+        look(uint32_t(i) + uint32_t(32 * tile));
     };
     auto copy_whole = [&](int stage, int32_t i) {
         const uint32_t to = ring_at + stage * S::kStage;
