@@ -278,12 +278,12 @@ __device__ __forceinline__ void attn_steps4(const PagedAttentionParams& p, const
 
 #pragma unroll 1
     for (int stage = 0, t_left = part.hi - part.lo; t_left > 0;
-         --t_left, i0 += tile, stage = (stage + 1) % S::kStages) {
+         --t_left, i0 += tile, stage = stage + 1 < S::kStages ? stage + 1 : 0) {
         // a ring of one warp: the next copies go out first; a shared one: all its warps' copies
         // are there, and all are done with the stage that the next ones fill
         if (kHq > 1) copy_wait<S::kStages - 2>();
         if (kHq > 1) __syncthreads();  // (two key heads side by side need none: 166 us with it, 155 without)
-        fill((stage + S::kStages - 1) % S::kStages);
+        fill(stage > 0 ? stage - 1 : S::kStages - 1);
         if (i0 >= step_end || (kHq > 1 && part.n_heads <= 0)) continue;
         if (kHq == 1) {
             copy_wait<S::kStages - 1>();

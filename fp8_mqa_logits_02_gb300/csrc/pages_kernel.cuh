@@ -12,7 +12,7 @@
 //
 // The requests are few (8192 at most), so each CTA makes the running sums by itself, in shared memory, and
 // the tokens, pages and requests are shared out to all threads: no workspace, no atomics.  A thread finds four
-// tokens side by side with one search and, mostly, one page.  A call is one cluster, whose barrier the lengths
+// tokens side by side with one search and one page, or two.  A call is one cluster, whose barrier the lengths
 // and the height wait for (everyone arrives there early, after the sums); a large one is as many CTAs as its
 // tokens want, and then a small kernel for the lengths and the height.
 //
