@@ -14,10 +14,10 @@
 // shared memory at once, and keeps the sines' and cosines' products with the weights in registers; a block's
 // tokens share a table of sines and cosines, made by all of its threads while the rows are on their way.
 //
-// Measured: 16384 tokens x 40 heads of 128 in bfloat16 (336 MB) 53.4 us, 6.3 TB/s of 6.8; with rows loaded straight
-// into registers 82, heads of both tensors in one group 64.  8192 tokens x 32 heads to E4M3 (102 MB) 25.1 us, where
+// Measured: 16384 tokens x 40 heads of 128 in bfloat16 (336 MB) 53.0 us, 6.3 TB/s of 6.8; with rows loaded straight
+// into registers 82, heads of both tensors in one group 64.  8192 tokens x 32 heads to E4M3 (102 MB) 24.2 us, where
 // the instructions decide (74 % of the issue slots); twice as many values a lane, with a third fewer instructions, took
-// 25.6, since the registers leave fewer warps.
+// 25.6 for 25.1, since the registers leave fewer warps.
 #pragma once
 
 #include <type_traits>
