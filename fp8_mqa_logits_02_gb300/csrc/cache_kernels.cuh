@@ -215,6 +215,12 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write4_kernel(const __gri
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o /= 2) a = max_nan(a, __shfl_xor_sync(~0u, a, o));
         const PagedView& cache = p.cache[i];
+        // (before the look at the page: the second cache may have pages that the first has not)
+        if (i == 0 || !p.alike) {
+            at_data = page * cache.page_stride + r * cache.row_stride + h * cache.head_stride + c * 8;
+            at_group = page * cache.group_page_stride + r * cache.group_row_stride + h * cache.group_head_stride + c;
+            at_scale = page * cache.scale_page_stride + r * cache.scale_row_stride + h * cache.scale_head_stride;
+        }
         if (slot < 0 || page >= cache.pages) continue;
         // 2^-e of a in [2^e, 2^(e + 1)); the largest ones, and what is not finite, take 2^-126
         const float down = __uint_as_float((254u - min(__float_as_uint(a) >> 23, 253u)) << 23);
@@ -229,11 +235,6 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write4_kernel(const __gri
             v[j] = to_float(raw[i].v[j]);
             v[j + 1] = to_float(raw[i].v[j + 1]);
             quotients(v[j], v[j + 1], by2, b2, y2);
-        }
-        if (i == 0 || !p.alike) {
-            at_data = page * cache.page_stride + r * cache.row_stride + h * cache.head_stride + c * 8;
-            at_group = page * cache.group_page_stride + r * cache.group_row_stride + h * cache.group_head_stride + c;
-            at_scale = page * cache.scale_page_stride + r * cache.scale_row_stride + h * cache.scale_head_stride;
         }
         uint8_t* const to = cache.data + at_data;
         if (in_bounds(p.bounds, kMemData + i, to, 8))
