@@ -53,7 +53,7 @@ bool pages_smem()
                                 int(pages_smem_bytes(kPagesMaxRows))) == cudaSuccess;
 }
 
-template <class X, int kDim, bool kE4m3, bool kInterleaved>
+template <class X, int kDim, bool kE4m3, bool kInterleaved, bool kSmallEps = false>
 cudaError_t rotate_launch(NormRotateParams& p, bool vec, int sm_count, cudaStream_t s)
 {
     // As many heads to a group of lanes as there is room for, shared out evenly, since their factors are made once;
@@ -68,18 +68,23 @@ cudaError_t rotate_launch(NormRotateParams& p, bool vec, int sm_count, cudaStrea
     p.by_units = FastDiv(uint32_t(units()));
     const size_t smem = size_t(rotate_smem<X>(p.per_unit));
     const dim3 grid(unsigned((p.T * units() + kGroups - 1) / kGroups));
-    return vec ? launch_after(norm_rotate_kernel<X, kDim, kE4m3, true, kInterleaved>, grid, kRotateThreads, smem, s, p)
-               : launch_after(norm_rotate_kernel<X, kDim, kE4m3, false, kInterleaved>, grid, kRotateThreads, smem, s, p);
+    return vec ? launch_after(norm_rotate_kernel<X, kDim, kE4m3, true, kInterleaved, kSmallEps>, grid, kRotateThreads, smem, s, p)
+               : launch_after(norm_rotate_kernel<X, kDim, kE4m3, false, kInterleaved, kSmallEps>, grid, kRotateThreads, smem, s, p);
+}
+
+template <class X, int kDim, bool kInterleaved>
+cudaError_t rotate_to(NormRotateParams& p, bool e4m3, bool vec, int sm_count, cudaStream_t s)
+{
+    if (!e4m3) return rotate_launch<X, kDim, false, kInterleaved>(p, vec, sm_count, s);
+    return p.eps >= kRotateEps ? rotate_launch<X, kDim, true, kInterleaved>(p, vec, sm_count, s)
+                               : rotate_launch<X, kDim, true, kInterleaved, true>(p, vec, sm_count, s);
 }
 
 template <class X, int kDim>
 cudaError_t rotate_dim(NormRotateParams& p, bool interleaved, bool e4m3, bool vec, int sm_count, cudaStream_t s)
 {
-    if (interleaved)
-        return e4m3 ? rotate_launch<X, kDim, true, true>(p, vec, sm_count, s)
-                    : rotate_launch<X, kDim, false, true>(p, vec, sm_count, s);
-    return e4m3 ? rotate_launch<X, kDim, true, false>(p, vec, sm_count, s)
-                : rotate_launch<X, kDim, false, false>(p, vec, sm_count, s);
+    return interleaved ? rotate_to<X, kDim, true>(p, e4m3, vec, sm_count, s)
+                       : rotate_to<X, kDim, false>(p, e4m3, vec, sm_count, s);
 }
 
 template <class X>
