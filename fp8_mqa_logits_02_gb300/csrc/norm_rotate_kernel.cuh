@@ -206,11 +206,11 @@ __global__ void __launch_bounds__(kRotateThreads, 8) norm_rotate_kernel(const __
             if (in_bounds(p.bounds, kMemPositions, at, 4)) pos = *at;
         }
         const float* const at = p.inv_freq + pair;
-        const uint64_t turn = in_bounds(p.bounds, kMemFreq, at, 4) ? turn_of(*at) : 0;
+        const float f = in_bounds(p.bounds, kMemFreq, at, 4) ? *at : 0.0f;
         // in halves of a turn, [-1, 1)
-        const float half = float(int32_t((turn * uint64_t(pos)) >> 32)) * 0x1p-31f;
+        const float half = float(int32_t((turn_of(f) * uint64_t(pos)) >> 32)) * 0x1p-31f;
         float2 sc;
-        sincospif(half, &sc.x, &sc.y);
+        sincospif(half + (f - f), &sc.x, &sc.y);  // (f - f: NaN of a frequency that is not finite)
         s_turns[token][pair] = sc;
     }
     __syncthreads();

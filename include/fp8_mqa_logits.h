@@ -511,7 +511,7 @@ typedef struct fp8mqa_heads {
  *   x_type      FP8MQA_BF16, FP8MQA_F16 or FP8MQA_F32, of both.  out_type: x_type or FP8MQA_E4M3.
  *   dim         64 or 128.  rotated: a multiple of 16, at most dim; 0 only norms.
  *   positions   DEVICE int32 or int64 [T] (position_bytes 4 or 8); any value, negative ones too.
- *   inv_freq    DEVICE float32 [rotated / 2], radians a position.
+ *   inv_freq    DEVICE float32 [rotated / 2], radians a position; where one is not finite its pair is NaN.
  * T * (all heads) < 2^31.  No workspace, no allocation; may be captured into a graph.
  */
 FP8MQA_API int fp8_mqa_norm_rotate(const fp8mqa_heads* q, const fp8mqa_heads* k, int32_t x_type,

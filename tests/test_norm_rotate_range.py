@@ -54,3 +54,22 @@ def test_rows_without_weight_to_e4m3(eps):
     got, _ = fm.norm_rotate(x, None, pos, freq(64), w, eps=eps, dtype=F8)
     check(x, got, w, pos, freq(64), eps, False, F8)
     assert (back(got) == 0).all() and torch.isfinite(got[1]).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("at", [0, 5, 31])
+def test_a_frequency_that_is_not_finite_is_nan(at, interleaved, bad):
+    rng = np.random.default_rng(2)
+    x = rows(rng, 4, 2, 128, torch.float32)
+    pos = torch.tensor([0, 1, -7, 99], dtype=torch.int32, device="cuda")
+    f = freq(64)
+    want, _ = fm.norm_rotate(x, None, pos, f, interleaved=interleaved)
+    f[at] = bad
+    got, _ = fm.norm_rotate(x, None, pos, f, interleaved=interleaved)
+    pair = [2 * at, 2 * at + 1] if interleaved else [at, at + 32]
+    rest = [d for d in range(128) if d not in pair]
+    assert got[..., pair].isnan().all()
+    assert torch.equal(got[..., rest], want[..., rest])
+    v, s = fm.norm_rotate(x, None, pos, f, interleaved=interleaved, dtype=F8)[0]
+    assert s.isnan().all() and v.float().isnan().all()
