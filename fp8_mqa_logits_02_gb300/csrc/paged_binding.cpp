@@ -16,6 +16,7 @@
 #include <string>
 
 #include "../../include/fp8_mqa_logits.h"
+#include "overlap.h"
 
 namespace {
 
@@ -458,11 +459,13 @@ PyObject* pages_update(PyObject* const* a, Py_ssize_t n)
     return result;
 }
 
-// Whether n0 blocks of n1 rows of `dim` values, at strides s0 and s1, follow one another without overlapping.
-bool apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t dim)
+// The bytes of rows [T, heads, dim], and of a contiguous tensor.
+fp8mqa::Places rows_of(const at::Tensor& t)
 {
-    return (n1 <= 1 || s1 >= dim) && (n0 <= 1 || s0 >= (n1 > 0 ? (n1 - 1) * s1 : 0) + dim);
+    const int64_t e = t.element_size();
+    return {t.data_ptr(), t.size(0), t.stride(0) * e, t.size(1), t.stride(1) * e, t.size(2) * e};
 }
+fp8mqa::Places all_of(const at::Tensor& t) { return fp8mqa::bytes_at(t.data_ptr(), int64_t(t.nbytes())); }
 
 // q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, q_out, k_out
 PyObject* norm_rotate(PyObject* const* a, Py_ssize_t n)
@@ -535,8 +538,7 @@ PyObject* norm_rotate(PyObject* const* a, Py_ssize_t n)
                 bad(PyExc_ValueError, name + "_out must be " + name_of(type) + " " + list(x.sizes()) +
                                           ", contiguous in its last dimension");
             // written: no two rows may overlap
-            if (!apart(T, o.stride(0), x.size(1), o.stride(1), dim) && !apart(x.size(1), o.stride(1), T, o.stride(0), dim))
-                bad(PyExc_ValueError, name + "_out must not overlap");
+            if (!fp8mqa::apart(rows_of(o))) bad(PyExc_ValueError, name + "_out must not overlap");
             given[i] = a[9 + i];
             h.out = o.data_ptr();
             h.out_row_stride = o.stride(0);
@@ -551,6 +553,24 @@ PyObject* norm_rotate(PyObject* const* a, Py_ssize_t n)
                 h.out_scale = static_cast<float*>(scale[i].data_ptr());
             }
         }
+    }
+    // written: a result may take the place of its own rows, and else overlaps nothing of the call
+    for (int i = 0; i < 2; ++i) {
+        if (!given[i]) continue;
+        const fp8mqa::Places to = rows_of(THPVariable_Unpack(given[i]));
+        auto with = [&](bool overlaps, const char* what) {
+            if (overlaps) bad(PyExc_ValueError, std::string(i ? "k" : "q") + "_out must not overlap " + what);
+        };
+        for (int j = 0; j < 2; ++j) {
+            if (j && a[1] == Py_None) continue;
+            const fp8mqa::Places x = rows_of(THPVariable_Unpack(a[j]));
+            with(!(i == j && fp8mqa::same_places(to, x)) && fp8mqa::meet(to, x),
+                 i != j ? (j ? "k" : "q") : i ? "k unless it is k" : "q unless it is q");
+            if (a[4 + j] != Py_None) with(fp8mqa::meet(to, all_of(THPVariable_Unpack(a[4 + j]))), j ? "k_weight" : "q_weight");
+        }
+        if (i && given[0]) with(fp8mqa::meet(to, rows_of(THPVariable_Unpack(given[0]))), "q_out");
+        with(fp8mqa::meet(to, all_of(positions)), "positions");
+        with(fp8mqa::meet(to, all_of(freq)), "inv_freq");
     }
     const void* pos = positions.data_ptr();
     const auto* f = static_cast<const float*>(freq.data_ptr());

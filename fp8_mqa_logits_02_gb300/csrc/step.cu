@@ -7,6 +7,7 @@
 
 #include "../../include/fp8_mqa_logits.h"
 #include "norm_rotate_kernel.cuh"
+#include "overlap.h"
 #include "pages_kernel.cuh"
 #include "paged_launch.cuh"
 
@@ -107,6 +108,34 @@ int check_heads(const fp8mqa_heads* h, int32_t x_type, int32_t out_type)
     return on(h->out, 4) && h->out_row_stride % 4 == 0 && h->out_head_stride % 4 == 0 ? FP8MQA_OK : FP8MQA_ERR_MISALIGNED;
 }
 
+// Whether each result lies apart from itself and from everything else, but for one that takes the place of its own rows:
+// those are read by the lanes that write it, before they do.
+bool results_apart(const fp8mqa_heads* const (&h)[2], int64_t T, int32_t dim, int64_t e, int64_t eo, const Places& positions,
+                   const Places& inv_freq)
+{
+    Ascending read[6] = {positions, inv_freq}, written[4];  // then rows and a weight of each; results and scales
+    bool in_place[2] = {false, false};
+    int n = 0;
+    for (; n < 2 && h[n]; ++n) {
+        const fp8mqa_heads& t = *h[n];
+        const Places x = {t.x, T, t.row_stride * e, t.heads, t.head_stride * e, dim * e};
+        const Places out = {t.out, T, t.out_row_stride * eo, t.heads, t.out_head_stride * eo, dim * eo};
+        if (!apart(out)) return false;
+        in_place[n] = e == eo && same_places(x, out);
+        read[2 + 2 * n] = x;
+        read[3 + 2 * n] = bytes_at(t.weight, t.heads > 0 ? dim * size_of(t.weight_type) : 0);
+        written[2 * n] = out;
+        written[2 * n + 1] = bytes_at(t.out_scale, 4 * T * t.heads);
+    }
+    for (int i = 0; i < 2 * n; ++i) {
+        for (int j = 0; j < 2 + 2 * n; ++j)
+            if (meet(written[i], read[j]) && !(j == i + 2 && i % 2 == 0 && in_place[i / 2])) return false;
+        for (int j = 0; j < i; ++j)
+            if (meet(written[i], written[j])) return false;
+    }
+    return true;
+}
+
 }  // namespace
 }  // namespace fp8mqa
 
@@ -191,6 +220,9 @@ int fp8_mqa_norm_rotate(const fp8mqa_heads* q, const fp8mqa_heads* k, int32_t x_
     if (heads == 0) return FP8MQA_OK;
     if (rotated > 0 && (!positions || !inv_freq)) return FP8MQA_ERR_INVALID_ARG;
     if (!on(positions, uintptr_t(position_bytes)) || !on(inv_freq, 4)) return FP8MQA_ERR_MISALIGNED;
+    if (!results_apart({q, k}, T, dim, size_of(x_type), size_of(out_type), bytes_at(positions, rotated > 0 ? T * position_bytes : 0),
+                       bytes_at(inv_freq, 2 * int64_t(rotated))))
+        return FP8MQA_ERR_INVALID_ARG;
     int err = FP8MQA_OK;
     const PagedDevice* st = paged_device(&err);
     if (!st) return err;

@@ -52,7 +52,8 @@ def torch_dir() -> str:
 
 def binding_deps() -> list:
     """What the binding is compiled from; another torch has other headers and needs a new one."""
-    return [BINDING_SOURCE, os.path.join(ROOT, "include", "fp8_mqa_logits.h"), os.path.abspath(__file__),
+    return [BINDING_SOURCE, os.path.join(CSRC, "overlap.h"), os.path.join(ROOT, "include", "fp8_mqa_logits.h"),
+            os.path.abspath(__file__),
             os.path.join(torch_dir(), "version.py")]
 
 

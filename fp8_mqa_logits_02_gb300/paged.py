@@ -196,7 +196,8 @@ def norm_rotate(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor
     position for each pair of the first ``2 * len(inv_freq)`` values (a multiple of 16), pairs (i, i +
     len(inv_freq)) or, ``interleaved``, (2 i, 2 i + 1).  q_weight, k_weight: [dim] of the tensors' type
     or float32; a tensor without one is rotated only.  Returns (q, k) in the inputs' type, in new
-    tensors or in q_out and k_out (which may be q and k themselves); with ``dtype`` float8_e4m3fn each is
+    tensors or in q_out and k_out (which may be q and k themselves, and else share no memory with any
+    argument or with one another); with ``dtype`` float8_e4m3fn each is
     (values, scales float32 [T, heads]), the q of fp8_mqa_logits and logits_paged, whose scales go into w.
     """
     call = _binding().norm_rotate

@@ -487,7 +487,8 @@ typedef struct fp8mqa_heads {
     const void* x;        /* DEVICE, aligned to its type */
     const void* weight;   /* DEVICE [dim], or NULL: rows are not normed */
     void* out;            /* DEVICE, aligned to its type (E4M3: to 4 bytes, strides too); may be x itself,
-                             with x's strides, where the type is x's */
+                             with x's strides, where the type is x's, and else shares no memory with
+                             anything that the call reads or writes */
     float* out_scale;     /* DEVICE [T, heads] for E4M3 results, else NULL */
     int64_t row_stride, head_stride;
     int64_t out_row_stride, out_head_stride;
@@ -512,7 +513,10 @@ typedef struct fp8mqa_heads {
  *   dim         64 or 128.  rotated: a multiple of 16, at most dim; 0 only norms.
  *   positions   DEVICE int32 or int64 [T] (position_bytes 4 or 8); any value, negative ones too.
  *   inv_freq    DEVICE float32 [rotated / 2], radians a position; where one is not finite its pair is NaN.
- * T * (all heads) < 2^31.  No workspace, no allocation; may be captured into a graph.
+ * T * (all heads) < 2^31.  Results that share memory with one another or with an argument, but for x
+ * itself, are refused (FP8MQA_ERR_INVALID_ARG; slices of one tensor do not share it, but many rows that lie
+ * between one another's at different strides are refused too).  No workspace, no allocation; may be captured
+ * into a graph.
  */
 FP8MQA_API int fp8_mqa_norm_rotate(const fp8mqa_heads* q, const fp8mqa_heads* k, int32_t x_type,
                                    int32_t out_type, int64_t T, int32_t dim,

@@ -1,0 +1,152 @@
+"""The host code of page tables and of norms with rotation against a stand-in for the CUDA runtime (no GPU, no kernel
+runs): which calls it refuses, and what it launches for the others."""
+import ctypes
+import os
+import shutil
+import struct
+import subprocess
+
+import numpy as np
+import pytest
+
+import fp8_mqa_logits_02_gb300 as fm
+from fp8_mqa_logits_02_gb300 import nvcc_build
+from test_paged_host import CALLS
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+OK, INVALID = 0, -1
+E4M3, BF16, F32 = 0, 1, 3
+LOOK = """
+#include "overlap.h"
+extern "C" int places_meet(const int64_t* a, const int64_t* b)
+{
+    const auto of = [](const int64_t* p) {
+        return fp8mqa::Places{reinterpret_cast<const void*>(p[0]), p[1], p[2], p[3], p[4], p[5]};
+    };
+    return fp8mqa::meet(of(a), of(b));
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def built(tmp_path_factory):
+    nvcc = nvcc_build.nvcc_path()
+    d = tmp_path_factory.mktemp("host")
+    (d / "look.cpp").write_text(LOOK)
+    common = [nvcc, "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(nvcc_build.ROOT, "include"),
+              "-I", nvcc_build.CSRC, "-c"]
+    sources = [os.path.join(nvcc_build.CSRC, "step.cu"), os.path.join(nvcc_build.CSRC, "paged.cu"),
+               os.path.join(HERE, "fake_runtime.cpp"), str(d / "look.cpp")]
+    objects = [str(d / (os.path.basename(s) + ".o")) for s in sources]
+    # the kernels are not assembled
+    virtual = ["-gencode", "arch=compute_103a,code=compute_103a"]
+    running = [subprocess.Popen(common + (virtual if s.endswith(".cu") else []) + ["-o", o, s], stdout=subprocess.PIPE,
+                                stderr=subprocess.STDOUT, text=True) for s, o in zip(sources, objects)]
+    for p in running:
+        out, _ = p.communicate()
+        assert p.returncode == 0, out
+    wraps = [x for c in CALLS for x in ("-Xlinker", f"--wrap={c}")]
+    subprocess.run([nvcc, "-shared", "-o", str(d / "host.so"), *objects, *wraps], check=True)
+    return str(d / "host.so")
+
+
+@pytest.fixture
+def lib(built, tmp_path):
+    """A library of its own, with the state of a fresh process."""
+    path = str(tmp_path / "host.so")
+    shutil.copy(built, path)
+    handle = ctypes.CDLL(path)
+    for name, (res, args) in fm.SIGNATURES.items():
+        fn = getattr(handle, name, None)
+        if fn is not None:
+            fn.restype, fn.argtypes = res, args
+    handle.fake_set(0, 0, 0)
+    return handle
+
+
+# ------------------------------------------------------------------------------------ memory that is shared
+
+def test_pieces_meet_where_their_bytes_do(lib):
+    rng = np.random.default_rng(1)
+    hits = 0
+    for _ in range(4000):
+        steps = rng.integers(-40, 41, (2, 2))
+        steps[1] = np.where(rng.random(2) < 0.5, steps[0], steps[1])     # half of them alike
+        places, bytes_ = [], []
+        for s in steps:
+            n0, n1 = rng.integers(0, 6, 2)
+            p = np.array([10000 + rng.integers(0, 120), n0, s[0], n1, s[1], rng.integers(0, 20)], np.int64)
+            places.append(p)
+            bytes_.append({int(p[0] + i * p[2] + j * p[4] + k) for i in range(n0) for j in range(n1) for k in range(p[5])})
+        want = bool(bytes_[0] & bytes_[1])
+        hits += want
+        at = [p.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)) for p in places]
+        assert lib.places_meet(at[0], at[1]) == lib.places_meet(at[1], at[0]) == want, places
+    assert 500 < hits < 3500
+
+
+BASE, T, DIM = 1 << 20, 50, 128
+
+
+def heads(x, n=4, row=9 * DIM, head=DIM, out=None, out_row=None, out_head=None, weight=0, scale=0, weight_type=F32):
+    return struct.pack("@PPPPqqqqii", x, weight, x if out is None else out, scale, row, head, row if out_row is None else out_row,
+                       head if out_head is None else out_head, n, weight_type)
+
+
+def rotate(lib, q, k=None, to=BF16, pos=8 << 20, freq=9 << 20, T=T, rotated=64):
+    launched = lib.fake_launches()
+    rc = lib.fp8_mqa_norm_rotate(q, k, BF16, to, T, DIM, pos, 4, freq, rotated, 0, 1e-6, None)
+    assert (lib.fake_launches() - launched == 1) == (rc == OK)
+    return rc
+
+
+def at(h, t=0):     # bfloat16 [T, 9, 128] from BASE on
+    return BASE + 2 * DIM * (h + 9 * t)
+
+
+def test_results_in_place_or_apart_are_taken(lib):
+    far = 4 << 20
+    assert rotate(lib, heads(at(0)), heads(at(5), n=2)) == OK                             # both in place
+    assert rotate(lib, heads(at(0), out=far), heads(at(5), n=2, out=far + 8 * DIM)) == OK   # slices of another tensor
+    assert rotate(lib, heads(at(0), out=at(5)), heads(at(4), n=1)) == OK                  # into heads that nobody reads
+    # heads side by side: q, k and v of each in turn
+    assert rotate(lib, heads(at(0), n=3, head=3 * DIM), heads(at(1), n=3, head=3 * DIM)) == OK
+    assert rotate(lib, heads(at(0), n=3, head=3 * DIM, out=at(2)), heads(at(1), n=3, head=3 * DIM)) == OK
+    # heads before tokens, in place
+    assert rotate(lib, heads(BASE, row=DIM, head=T * DIM), heads(BASE + 8 * T * DIM, row=DIM, head=T * DIM)) == OK
+    # strides of dimensions of one are never used
+    assert rotate(lib, heads(at(0), n=1, head=DIM, out_head=7)) == OK
+    assert rotate(lib, heads(at(0), row=5, out_row=77), heads(at(4)), T=1) == OK
+    # no heads, no rotation: what is not read does not count
+    assert rotate(lib, heads(at(0), n=0), heads(at(0))) == OK
+    assert rotate(lib, heads(at(0)), pos=at(1), freq=at(2), rotated=0) == OK
+    # to E4M3, beside one another
+    assert rotate(lib, heads(at(0), out=far, out_row=512, out_head=128, scale=far + 1024 * T),
+                  heads(at(4), out=far + (1 << 19), out_row=512, out_head=128, scale=far + 1024 * T + 16 * T), to=E4M3) == OK
+
+
+@pytest.mark.parametrize("name,q,k,kw", [
+    ("each into the other's place", heads(at(0), out=at(4)), heads(at(4), out=at(0)), {}),
+    ("q into k", heads(at(0), out=at(4)), heads(at(4), out=4 << 20), {}),
+    ("k into q", heads(at(0), out=4 << 20), heads(at(4), out=at(0)), {}),
+    ("q over a shared tensor's k", heads(at(0)), heads(at(3), out=4 << 20), {}),
+    ("one head on", heads(at(0), out=at(1)), None, {}),
+    ("one token on", heads(at(0), out=at(0, 1)), None, {}),
+    ("one value on", heads(at(0), out=at(0) + 16), None, {}),
+    ("another stride", heads(at(0), n=3, out_head=2 * DIM), None, {}),
+    ("both results in one place", heads(at(0), out=4 << 20), heads(at(4), out=4 << 20), {}),
+    ("the last head", heads(at(0), out=4 << 20), heads(at(4), out=(4 << 20) + 6 * DIM), {}),
+    ("rows on one another", heads(at(0), out=4 << 20, out_row=3 * DIM), None, {}),
+    ("heads on one another", heads(at(0), out=4 << 20, out_head=0), None, {}),
+    ("in turn, a head on", heads(at(0), n=3, head=3 * DIM, out=at(1)), heads(at(1), n=3, head=3 * DIM, out=4 << 20), {}),
+    ("a weight", heads(at(0), weight=at(3)), None, {}),
+    ("the other's weight", heads(at(0)), heads(at(5), out=4 << 20, weight=at(3)), {}),
+    ("the last position", heads(at(0)), None, dict(pos=at(3, T - 1) + 2 * DIM - 4)),
+    ("the frequencies", heads(at(0)), None, dict(freq=at(2, 7))),
+    ("in place, to E4M3", heads(at(0), scale=4 << 20), None, dict(to=E4M3)),
+    ("a scale", heads(at(0), out=4 << 20, out_row=512, scale=at(1)), None, dict(to=E4M3)),
+    ("a scale and its values", heads(at(0), out=4 << 20, out_row=512, scale=(4 << 20) + 512 * T - 128), None, dict(to=E4M3)),
+    ("one scale for both", heads(at(0), out=4 << 20, out_row=512, scale=5 << 20),
+     heads(at(4), out=6 << 20, out_row=512, scale=5 << 20), dict(to=E4M3))])
+def test_results_that_share_memory_are_refused(lib, name, q, k, kw):
+    assert rotate(lib, q, k, **kw) == INVALID
