@@ -161,6 +161,20 @@ int fp8_mqa_pages_update(int32_t* table, int64_t table_stride, int32_t table_col
                           static_cast<const void*>(rows), static_cast<const void*>(starts),
                           static_cast<const void*>(changed)})
         if (!on(p, 4)) return FP8MQA_ERR_MISALIGNED;
+    // what is written lies apart from everything else (`change` alone is not)
+    const Ascending arrays[10] = {bytes_at(change, 4 * B),
+                                  Places{table, B, 4 * table_stride, 1, 0, 4 * int64_t(table_cols)},
+                                  bytes_at(lens, 4 * B),
+                                  bytes_at(free_pages, 4 * capacity),
+                                  bytes_at(n_free, 4),
+                                  bytes_at(slots, 4 * total),
+                                  bytes_at(positions, 4 * total),
+                                  bytes_at(rows, 4 * total),
+                                  bytes_at(starts, 4 * (B + 1)),
+                                  bytes_at(changed, 4 * B)};
+    for (int i = 1; i < 10; ++i)
+        for (int j = 0; j < i; ++j)
+            if (meet(arrays[i], arrays[j])) return FP8MQA_ERR_INVALID_ARG;
     int err = FP8MQA_OK;
     const PagedDevice* st = paged_device(&err);
     if (!st) return err;

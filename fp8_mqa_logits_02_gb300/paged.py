@@ -170,7 +170,8 @@ def pages_update(table: torch.Tensor, lens: torch.Tensor, change: torch.Tensor, 
     """Change the requests' lengths, give and take their pages, and find their new tokens' slots.
 
     table: int32 [B, columns] page ids; lens: int32 [B]; free: int32 [n], a stack of the pages that
-    nobody holds, of which the first ``n_free`` (int32 [1]) are there: all four are updated in place.
+    nobody holds, of which the first ``n_free`` (int32 [1]) are there: all four are updated in place, and
+    none shares memory with another argument.
     change: int32 [B], tokens that each request gets (1 for a decode step), or gives up (its whole
     length when it ends).  Shrinking requests give their pages back first, then growing ones take
     theirs, both in order; a request that the table or the stack has no room for keeps its length

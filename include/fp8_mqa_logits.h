@@ -471,7 +471,7 @@ FP8MQA_API uint64_t fp8_mqa_attention_paged_workspace_bytes(int32_t q_heads, int
  *               stop at 2^31 - 1).
  *   changed     DEVICE int32 [B]: by how much the length changed (0 for a request that does not fit).
  * Limits: B <= 8192, table_cols * page_size < 2^31, B * table_cols < 2^31 (FP8MQA_ERR_UNSUPPORTED_SHAPE).
- * Arrays do not overlap.
+ * Arrays that overlap are refused (FP8MQA_ERR_INVALID_ARG).
  * The result is always the same for the same arguments.  No workspace, no allocation; may be captured
  * into a graph.
  */

@@ -38,8 +38,8 @@ def built(tmp_path_factory):
     sources = [os.path.join(nvcc_build.CSRC, "step.cu"), os.path.join(nvcc_build.CSRC, "paged.cu"),
                os.path.join(HERE, "fake_runtime.cpp"), str(d / "look.cpp")]
     objects = [str(d / (os.path.basename(s) + ".o")) for s in sources]
-    # the kernels are not assembled
-    virtual = ["-gencode", "arch=compute_103a,code=compute_103a"]
+    # the kernels are not assembled, nor optimised
+    virtual = ["-gencode", "arch=compute_103a,code=compute_103a", "-Xcicc", "-O0"]
     running = [subprocess.Popen(common + (virtual if s.endswith(".cu") else []) + ["-o", o, s], stdout=subprocess.PIPE,
                                 stderr=subprocess.STDOUT, text=True) for s, o in zip(sources, objects)]
     for p in running:
@@ -150,3 +150,43 @@ def test_results_in_place_or_apart_are_taken(lib):
      heads(at(4), out=6 << 20, out_row=512, scale=5 << 20), dict(to=E4M3))])
 def test_results_that_share_memory_are_refused(lib, name, q, k, kw):
     assert rotate(lib, q, k, **kw) == INVALID
+
+
+ARRAYS = {"table": 4 * 20 * 9, "lens": 4 * 20, "change": 4 * 20, "free": 4 * 33, "n_free": 4, "slots": 4 * 50, "positions": 4 * 50,
+          "rows": 4 * 50, "starts": 4 * 21, "changed": 4 * 20}      # bytes (20 requests, rows of 7 pages 9 apart)
+
+
+def update(lib, B=20, cols=7, pitch=9, capacity=33, total=50, **at):
+    where = {name: (i + 1) << 20 for i, name in enumerate(ARRAYS)} | at
+    launched = lib.fake_launches()
+    rc = lib.fp8_mqa_pages_update(where["table"], pitch, cols, 64, where["lens"], where["change"], B, where["free"], capacity,
+                                  where["n_free"], total, where["slots"], where["positions"], where["rows"], where["starts"],
+                                  where["changed"], None)
+    assert (lib.fake_launches() > launched) == (rc == OK)
+    return rc
+
+
+def test_page_tables_arrays_beside_one_another_are_taken(lib):
+    ends, at = {}, 1 << 16
+    for name, size in ARRAYS.items():
+        ends[name] = at
+        at += size
+    assert update(lib) == update(lib, **ends) == OK
+    # between the rows of a table that lie further apart than they are long
+    assert update(lib, n_free=(1 << 20) + 4 * 8, table=1 << 20) == OK
+    # what is empty is nowhere
+    assert update(lib, total=0, slots=1 << 20, positions=1 << 20, rows=1 << 20) == OK
+    assert update(lib, B=0, table=9 << 20, lens=9 << 20, changed=9 << 20, change=9 << 20) == OK
+    assert update(lib, capacity=0, free=1 << 20) == OK
+
+
+@pytest.mark.parametrize("i", range(1, 10))
+def test_page_tables_arrays_that_overlap_are_refused(lib, i):
+    names = list(ARRAYS)
+    for j in range(i):
+        a, b = names[i], names[j]
+        assert update(lib, **{a: 32 << 20, b: 32 << 20}) == INVALID
+        # the last entry of one (of a table: past its last row there is nothing) is the first of the other
+        last = ARRAYS[b] - (12 if b == "table" else 4)
+        assert update(lib, **{b: 32 << 20, a: (32 << 20) + last}) == INVALID
+        assert update(lib, **{b: 32 << 20, a: (32 << 20) + last + 4}) == OK
