@@ -19,6 +19,7 @@ struct PagedDevice {
     int sm_count = 0;
     int32_t* status = nullptr;  // status word of the paged logits
     std::atomic<bool> ready{false};
+    std::atomic<bool> wide_pages{false};  // the page tables' kernel may take all the shared memory that it wants
 };
 
 // The current device's state, set up by the first call that succeeds in it: what fails once (no memory

@@ -47,11 +47,16 @@ cudaError_t pages_launch(PagesParams& p, int sm_count, cudaStream_t s)
     return launch_after(pages_state_kernel, dim3(1), 1024, 0, s, p);
 }
 
-// What a call that needs more shared memory than a kernel gets unasked sets up once for each device.
-bool pages_smem()
+// What a call that needs more shared memory than a kernel gets unasked sets up once for each device (calls at the same
+// time perhaps once each).
+bool pages_smem(PagedDevice& st)
 {
-    return cudaFuncSetAttribute(pages_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                int(pages_smem_bytes(kPagesMaxRows))) == cudaSuccess;
+    if (st.wide_pages.load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(pages_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(pages_smem_bytes(kPagesMaxRows))) != cudaSuccess)
+        return false;
+    st.wide_pages.store(true, std::memory_order_release);
+    return true;
 }
 
 template <class X, int kDim, bool kE4m3, bool kInterleaved, bool kSmallEps = false>
@@ -176,10 +181,10 @@ int fp8_mqa_pages_update(int32_t* table, int64_t table_stride, int32_t table_col
         for (int j = 0; j < i; ++j)
             if (meet(arrays[i], arrays[j])) return FP8MQA_ERR_INVALID_ARG;
     int err = FP8MQA_OK;
-    const PagedDevice* st = paged_device(&err);
+    PagedDevice* st = paged_device(&err);
     if (!st) return err;
     // (what a kernel gets unasked is 48 KB)
-    if (pages_smem_bytes(int32_t(B)) > 47 * 1024 && !pages_smem()) return launched(cudaErrorInvalidValue);
+    if (pages_smem_bytes(int32_t(B)) > 47 * 1024 && !pages_smem(*st)) return launched(cudaErrorInvalidValue);
     PagesParams p;
     p.table = table;
     p.table_stride = table_stride;

@@ -14,10 +14,26 @@ from fp8_mqa_logits_02_gb300 import nvcc_build
 from test_paged_host import CALLS
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-OK, INVALID = 0, -1
+OK, INVALID, LAUNCH = 0, -1, -5
 E4M3, BF16, F32 = 0, 1, 3
 LOOK = """
 #include "overlap.h"
+#include <cuda_runtime.h>
+namespace {
+int g_attributes, g_fail;
+}
+// In the place of the stand-in's own: counts, and fails where it is told to.
+extern "C" cudaError_t __wrap_cudaFuncSetAttribute(const void*, cudaFuncAttribute, int)
+{
+    return ++g_attributes == g_fail ? cudaErrorInvalidValue : cudaSuccess;
+}
+extern "C" int attributes_set(int fail)
+{
+    const int n = g_attributes;
+    g_attributes = 0;
+    g_fail = fail;
+    return n;
+}
 extern "C" int places_meet(const int64_t* a, const int64_t* b)
 {
     const auto of = [](const int64_t* p) {
@@ -40,7 +56,8 @@ def built(tmp_path_factory):
     objects = [str(d / (os.path.basename(s) + ".o")) for s in sources]
     # the kernels are not assembled, nor optimised
     virtual = ["-gencode", "arch=compute_103a,code=compute_103a", "-Xcicc", "-O0"]
-    running = [subprocess.Popen(common + (virtual if s.endswith(".cu") else []) + ["-o", o, s], stdout=subprocess.PIPE,
+    more = {"step.cu": virtual, "paged.cu": virtual, "fake_runtime.cpp": ["-D__wrap_cudaFuncSetAttribute=not_this_one"]}
+    running = [subprocess.Popen(common + more.get(os.path.basename(s), []) + ["-o", o, s], stdout=subprocess.PIPE,
                                 stderr=subprocess.STDOUT, text=True) for s, o in zip(sources, objects)]
     for p in running:
         out, _ = p.communicate()
@@ -190,3 +207,12 @@ def test_page_tables_arrays_that_overlap_are_refused(lib, i):
         last = ARRAYS[b] - (12 if b == "table" else 4)
         assert update(lib, **{b: 32 << 20, a: (32 << 20) + last}) == INVALID
         assert update(lib, **{b: 32 << 20, a: (32 << 20) + last + 4}) == OK
+
+
+def test_shared_memory_for_many_requests_is_set_up_once(lib):
+    def many():
+        return update(lib, B=8192, total=0, table=1 << 30, lens=1 << 25, change=2 << 25, starts=3 << 25, changed=4 << 25)
+    assert update(lib) == OK and lib.attributes_set(1) > 0      # (that of the paged operators' kernels)
+    assert many() == LAUNCH and lib.attributes_set(0) == 1      # it fails, and is tried again
+    assert many() == OK and lib.attributes_set(0) == 1
+    assert many() == many() == update(lib) == OK and lib.attributes_set(0) == 0
