@@ -478,7 +478,9 @@ int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table, int64_t 
     if (!scaled(cache->type) || B < 0 || total < 0 || table_cols < 0 || out_type < (four ? FP8MQA_BF16 : 0) ||
         out_type > FP8MQA_F32)
         return FP8MQA_ERR_INVALID_ARG;
-    if (total * cache->heads >= int64_t(1) << 31 || B >= int64_t(1) << 31)
+    // (a block counts the 16-byte pieces of its output in 32 bits, a few turns of the block past the last one)
+    if (total * cache->heads >= int64_t(1) << 31 || B >= int64_t(1) << 31 ||
+        cache->heads * int64_t(cache->dim) * size_of(out_type) > int64_t(1) << 34)
         return FP8MQA_ERR_UNSUPPORTED_SHAPE;
     if (total == 0) return FP8MQA_OK;
     if (!starts || !out || (table_cols > 0 && B > 0 && !table) ||

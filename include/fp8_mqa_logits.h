@@ -360,6 +360,8 @@ FP8MQA_API int fp8_mqa_cache_write(const int32_t* slots, int64_t T, int32_t x_ty
  *              BF16, F16 or F32: data * scale in fp32, rounded to the type (out_scale is NULL);
  *              the only ones for an E2M1 cache (data * group, which is exact, then * scale).
  * Positions on pages that are not there, or past the table, are zero (and their scale).
+ * total * heads < 2^31, and a token's row of `out`, all its heads, is 2^34 bytes at most
+ * (FP8MQA_ERR_UNSUPPORTED_SHAPE).
  */
 FP8MQA_API int fp8_mqa_cache_read(const fp8mqa_cache* cache, const int32_t* table,
                                   int64_t table_stride, int32_t table_cols, const int32_t* starts,

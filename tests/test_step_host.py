@@ -14,8 +14,8 @@ from fp8_mqa_logits_02_gb300 import nvcc_build
 from test_paged_host import CALLS
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-OK, INVALID, LAUNCH = 0, -1, -5
-E4M3, BF16, F32 = 0, 1, 3
+OK, INVALID, UNSUPPORTED, LAUNCH = 0, -1, -2, -5
+E4M3, BF16, F32, E2M1 = 0, 1, 3, 4
 LOOK = """
 #include "overlap.h"
 #include <cuda_runtime.h>
@@ -216,3 +216,27 @@ def test_shared_memory_for_many_requests_is_set_up_once(lib):
     assert many() == LAUNCH and lib.attributes_set(0) == 1      # it fails, and is tried again
     assert many() == OK and lib.attributes_set(0) == 1
     assert many() == many() == update(lib) == OK and lib.attributes_set(0) == 0
+
+
+# ------------------------------------------------------------------------------------ many heads
+
+def cache(heads, dim, type, row):
+    """One token of many heads."""
+    return struct.pack("@PPqiiiiqqqqqqPqqq", BASE, BASE, 1, 1, heads, dim, type, heads * row, heads * row, row, heads, heads, 1,
+                       BASE if type == E2M1 else 0, heads * dim // 16, heads * dim // 16, dim // 16)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("type,to,size", [(E4M3, E4M3, 1), (E4M3, BF16, 2), (E4M3, F32, 4), (E2M1, BF16, 2), (E2M1, F32, 4)])
+def test_reads_of_more_heads_than_a_block_counts_are_refused(lib, type, to, size, dim):
+    # a block counts the 16-byte pieces of a row of its output in 32 bits
+    most = 2 ** 34 // (dim * size)
+
+    def read(heads):
+        launched = lib.fake_launches()
+        c = cache(heads, dim, type, dim if type == E4M3 else dim // 2)
+        rc = lib.fp8_mqa_cache_read(c, BASE, 1, 1, BASE, 1, 1, to, BASE, BASE if to == E4M3 else None, None)
+        assert (lib.fake_launches() > launched) == (rc == OK)
+        return rc
+    assert read(most) == OK
+    assert read(most + 1) == read(2 * most) == read(2 ** 31 - 1) == UNSUPPORTED
