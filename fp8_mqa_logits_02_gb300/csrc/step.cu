@@ -65,15 +65,16 @@ cudaError_t rotate_launch(NormRotateParams& p, bool vec, int sm_count, cudaStrea
     // As many heads to a group of lanes as there is room for, shared out evenly, since their factors are made once;
     // fewer where that leaves SMs without work.
     constexpr int kGroups = kRotateThreads / (kDim / 8);
-    const int most = std::max(p.heads[0], p.heads[1]);
-    int parts = (most + kRotateHeads<X> - 1) / kRotateHeads<X>;
-    auto units = [&] { return (int64_t(p.heads[0]) + p.per_unit - 1) / p.per_unit + (p.heads[1] + p.per_unit - 1) / p.per_unit; };
-    for (p.per_unit = (most + parts - 1) / parts; p.per_unit > 1 && p.T * units() < int64_t(kGroups) * 2 * sm_count;)
+    const int64_t most = std::max(p.heads[0], p.heads[1]);  // (up to 2^31 - 1)
+    const int64_t parts = (most + kRotateHeads<X> - 1) / kRotateHeads<X>;
+    auto units = [&](int i) { return (int64_t(p.heads[i]) + p.per_unit - 1) / p.per_unit; };
+    auto all_units = [&] { return units(0) + units(1); };
+    for (p.per_unit = int32_t((most + parts - 1) / parts); p.per_unit > 1 && p.T * all_units() < int64_t(kGroups) * 2 * sm_count;)
         p.per_unit = (p.per_unit + 1) / 2;
-    for (int i = 0; i < 2; ++i) p.units[i] = (p.heads[i] + p.per_unit - 1) / p.per_unit;
-    p.by_units = FastDiv(uint32_t(units()));
+    for (int i = 0; i < 2; ++i) p.units[i] = int32_t(units(i));
+    p.by_units = FastDiv(uint32_t(all_units()));
     const size_t smem = size_t(rotate_smem<X>(p.per_unit));
-    const dim3 grid(unsigned((p.T * units() + kGroups - 1) / kGroups));
+    const dim3 grid(unsigned((p.T * all_units() + kGroups - 1) / kGroups));
     return vec ? launch_after(norm_rotate_kernel<X, kDim, kE4m3, true, kInterleaved, kSmallEps>, grid, kRotateThreads, smem, s, p)
                : launch_after(norm_rotate_kernel<X, kDim, kE4m3, false, kInterleaved, kSmallEps>, grid, kRotateThreads, smem, s, p);
 }

@@ -240,3 +240,17 @@ def test_reads_of_more_heads_than_a_block_counts_are_refused(lib, type, to, size
         return rc
     assert read(most) == OK
     assert read(most + 1) == read(2 * most) == read(2 ** 31 - 1) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("heads_", [2 ** 31 - 1, 2 ** 31 - 9, 2 ** 30 + 1, 2 ** 20 + 7])
+@pytest.mark.parametrize("other", [0, 1])
+def test_norms_of_very_many_heads(lib, heads_, other):
+    # one token: groups of 16 lanes that take up to 10 heads each, eight groups a block
+    many = heads(BASE, n=heads_ - other, row=0)
+    one = heads(1 << 50, n=other, row=0)
+    grid = (ctypes.c_uint * 3)()
+    for q, k in ((many, one), (one, many)):
+        lib.fake_set(0, 0, 0)
+        assert rotate(lib, q, k, T=1, pos=1 << 51, freq=1 << 52) == OK
+        lib.fake_grid(0, grid)
+        assert grid[0] == -(-(-(-(heads_ - other) // 10) + other) // 8)
