@@ -246,7 +246,8 @@ __device__ __forceinline__ void attn_steps4(const PagedAttentionParams& p, const
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
             const int e = min(max(int(__float_as_uint(top) >> 23), 20), 240) - 139;
-            const float down = copysignf(__uint_as_float(uint32_t(127 - e) << 23), p.sm_scale);
+            float down = copysignf(__uint_as_float(uint32_t(127 - e) << 23), p.sm_scale);
+            if (p.sm_scale != p.sm_scale) down = p.sm_scale;  // NaN in every score of a row that is there
             by = __uint_as_float(uint32_t(127 + e) << 23);
 #pragma unroll
             for (int s = 0; s < S::kMT; ++s)
@@ -255,11 +256,11 @@ __device__ __forceinline__ void attn_steps4(const PagedAttentionParams& p, const
                     qf[nt][s][j] = pack16<false>(__uint_as_float(qf[nt][s][j] << 16) * down,
                                                  __uint_as_float(qf[nt][s][j] & 0xFFFF0000u) * down);
         }
-        else if (p.sm_scale < 0.0f) {
+        else if (!(p.sm_scale >= 0.0f)) {  // (NaN too, as above)
 #pragma unroll
             for (int s = 0; s < S::kMT; ++s)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) qf[nt][s][j] ^= 0x80008000u;
+                for (int j = 0; j < 2; ++j) qf[nt][s][j] = p.sm_scale < 0.0f ? qf[nt][s][j] ^ 0x80008000u : 0x7FFF7FFFu;
         }
         // (above 0, so that -inf stays -inf: a scale of 0 counts as one that leaves nothing of the scores)
         const float c = fmaxf(fabsf(p.sm_scale) * 1.4426950408889634f * by, 1e-35f);
