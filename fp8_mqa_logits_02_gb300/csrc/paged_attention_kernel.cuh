@@ -183,7 +183,7 @@ __device__ __forceinline__ void attn_steps(const PagedAttentionParams& p, const 
                 }
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            const int e = min(max(int(__float_as_uint(top) >> 23), 20), 240) - 139;
+            const int e = min(max(int(__float_as_uint(top) >> 23), 20), 254) - 139;
             const float down = __uint_as_float(uint32_t(127 - e) << 23);
             by = __uint_as_float(uint32_t(127 + e) << 23);
 #pragma unroll

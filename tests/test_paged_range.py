@@ -38,3 +38,18 @@ def test_a_scale_that_is_nan(kind, dtype, q_heads):
     out, lse = fm.attention_paged(q, k, v, table, lens, sm_scale=float("nan"), return_lse=True, **more)
     assert out[[0, 2]].isnan().all() and lse[[0, 2]].isnan().all()
     assert (out[[1, 3]] == 0).all() and (lse[[1, 3]] == -float("inf")).all()      # no position, none that is there
+
+
+@pytest.mark.parametrize("q_heads", [8, 32])
+@pytest.mark.parametrize("kind", ["4 bits", "e4m3"])
+@pytest.mark.parametrize("e", [-80, 60, 112, 120])
+def test_large_and_small_bfloat16_queries(kind, e, q_heads):
+    # scores are sm_scale q . k: a power of two that goes from one to the other leaves every bit of the result
+    rng = np.random.default_rng(2)
+    k, v, more = caches(rng, kind)
+    table, lens = gpu(np.array([[0, 1], [2, 3], [4, 5]])).int(), gpu(np.array([33, 1, 64])).int()
+    q = torch.from_numpy(rng.standard_normal((3, q_heads, 128))).to(torch.bfloat16).cuda()
+    want = fm.attention_paged(q, k, v, table, lens, sm_scale=0.0625, return_lse=True, **more)
+    got = fm.attention_paged(q * 2.0 ** e, k, v, table, lens, sm_scale=0.0625 * 2.0 ** -e, return_lse=True, **more)
+    assert torch.isfinite(want[0]).all()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
