@@ -505,10 +505,11 @@ typedef struct fp8mqa_heads {
  *     out_a = y_a cos t - y_b sin t,  out_b = y_b cos t + y_a sin t,   t = positions[token] * inv_freq[i]
  *
  * for the pairs i < rotated / 2 of the first `rotated` values: (a, b) = (i, i + rotated / 2), or
- * (2i, 2i + 1) with interleaved = 1; the other values are y.  All in fp32 (t to fp32 precision of a turn at
- * any position), rounded once to x's type, or to E4M3 with a scale a row as fp8_mqa_cache_write does: the
- * q_fp8 of fp8_mqa_logits with dim 128, whose scales the caller multiplies into w.  Sums of squares are
- * fp32 and want values under 10^18.
+ * (2i, 2i + 1) with interleaved = 1; the other values are y.  All in fp32, rounded once to x's type, or to
+ * E4M3 with a scale a row as fp8_mqa_cache_write does: the q_fp8 of fp8_mqa_logits with dim 128, whose scales
+ * the caller multiplies into w.  Sums of squares are fp32 and want values under 10^18.  However many turns t
+ * is, it is off by little more than 2^-26 of a turn and by the frequency's own error, (1 + |f|) 2^-64 turns
+ * for f turns a position, times |position|: as exact as fp32 holds a turn up to positions of 2^39, not beyond.
  *
  *   q, k        the tensors; k may be NULL, and heads 0.
  *   x_type      FP8MQA_BF16, FP8MQA_F16 or FP8MQA_F32, of both.  out_type: x_type or FP8MQA_E4M3.

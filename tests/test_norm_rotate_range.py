@@ -1,4 +1,6 @@
 """Norms with rotation at the ends of the range.  Tolerances as in test_norm_rotate.py but where stated."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -7,6 +9,8 @@ import fp8_mqa_logits_02_gb300 as fm
 from test_norm_rotate import F8, TYPES, check, freq, rows
 
 pytestmark = pytest.mark.gpu
+
+TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -73,3 +77,26 @@ def test_a_frequency_that_is_not_finite_is_nan(at, interleaved, bad):
     assert torch.equal(got[..., rest], want[..., rest])
     v, s = fm.norm_rotate(x, None, pos, f, interleaved=interleaved, dtype=F8)[0]
     assert s.isnan().all() and v.float().isnan().all()
+
+
+def test_angles_of_positions_up_to_2_39():
+    # With f the frequency in turns, its 64-bit fraction is off by (1 + |f|) 2^-64 at most (what is cut off, and the
+    # rounding of 1 / 2 pi), so the angle by that times |position|: 2^-25 turns at 2^39 for a slow pair.  Cut to 2^-32
+    # of a turn and rounded to 24 bits of half a turn it is off by 2^-32 + 2^-26 more.  Sine and cosine are within
+    # 2 U (U = 2^-24), and the products and their difference take 3 U.  Nothing of it grows with the angle, which is up
+    # to 4e12 radians here.
+    rng = np.random.default_rng(3)
+    pos = [2 ** 39, -2 ** 39, 2 ** 39 - 1, 2 ** 38 + 12345, -(2 ** 36) - 7, 2 ** 33 + 1, 2 ** 31 - 1, -1]
+    x = rows(rng, len(pos), 2, 128, torch.float32)
+    f = freq(128)
+    f[3], f[5], f[9] = 7.5, -0.25, 1e-30
+    got, _ = fm.norm_rotate(x, None, torch.tensor(pos, dtype=torch.int64, device="cuda"), f)
+    freqs = [Fraction(v) for v in f.cpu().double().tolist()]
+    t = np.array([[float(p * v / TWO_PI % 1 * TWO_PI) for v in freqs] for p in pos])[:, None]
+    off = np.array([[float((1 + abs(v / TWO_PI)) * abs(p) / 2 ** 64) for v in freqs] for p in pos])[:, None]
+    err = 2 * np.pi * (off + 2.0 ** -26 + 2.0 ** -32) + 5 * 2.0 ** -24
+    assert err.max() < 20 * 2.0 ** -24
+    a, b = np.split(x.cpu().double().numpy(), 2, -1)
+    want = np.concatenate([a * np.cos(t) - b * np.sin(t), b * np.cos(t) + a * np.sin(t)], -1)
+    tol = np.concatenate([err * (np.abs(a) + np.abs(b))] * 2, -1)
+    assert np.all(np.abs(got.cpu().double().numpy() - want) <= tol), (np.abs(got.cpu().double().numpy() - want) / tol).max()
