@@ -114,8 +114,9 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid
 // ties of 16-bit inputs fall as in real arithmetic: rows are first scaled by a power of two that brings a to
 // [1, 2), and then, with y the correctly rounded reciprocal of b, q = y n is off by r = n - q b, which a fused
 // multiply-add gives exactly, and q + y r is the quotient rounded (P. Markstein, IBM J. Res. Dev. 34, 1990).
-// 16 thousand tokens x 8 heads of bfloat16 keys and values (86 MB): 18.6 us, 4.6 TB/s of 6.8, where some 200
-// instructions for 16 values decide (16.0 without the quotients).
+// 16 thousand tokens x 8 heads of bfloat16 keys and values (86 MB): 18.5 us, 4.7 TB/s of 6.8 (fp32 rows, 159 MB:
+// 23.4).  The quotients are 2.5 us of it, with some 200 instructions for 16 values (65 % of the issue slots), and loads
+// are what warps wait for most: 60 registers for both tensors leave 41 % of the warps.
 template <class X>
 struct alignas(16) Group {
     X v[kGroup];
@@ -279,7 +280,7 @@ __device__ __forceinline__ int64_t sequence_of(const Starts& starts, int64_t B, 
 }
 
 // A block packs block_rows consecutive output rows: first a thread a row finds where it lies, then all
-// threads copy their pieces, which are contiguous in the output.  66 thousand rows x 8 heads to bfloat16
+// threads copy their pieces, which are contiguous in the output.  75 thousand rows x 8 heads to bfloat16
 // (234 MB): 39 us, 5.9 TB/s of 6.7; a warp a row took 182, eight pieces under way instead of four 42.
 template <class Out, int kDim>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_constant__ CacheReadParams p)
@@ -377,7 +378,7 @@ __device__ __forceinline__ void store32(void* to, const uint32_t* w, bool aligne
     }
 }
 
-// The same from an E2M1 cache: a piece is a group, 16 values.  66 thousand rows x 8 heads to bfloat16 (175 MB): 36.8 us
+// The same from an E2M1 cache: a piece is a group, 16 values.  75 thousand rows x 8 heads to bfloat16 (201 MB): 36.8 us
 // (47 with two stores of 16 bytes instead of one of 32; 39 with two groups a thread under way, which leaves fewer
 // threads an SM, 58 with eight).
 template <class Out, int kDim>

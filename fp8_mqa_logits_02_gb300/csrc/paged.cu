@@ -249,7 +249,7 @@ cudaError_t write_rows(const CacheWriteParams& p, int32_t dim, int tensors, bool
 }
 
 // A block packs about kReadTurns x kReadPieces pieces a thread (finding the rows costs a block its
-// start: 66 thousand rows of 8 heads as stored take 25.3 us so and 28.6 in one turn), but no more
+// start: 75 thousand rows of 8 heads as stored take 25.3 us so and 28.6 in one turn), but no more
 // than leaves two blocks an SM.
 constexpr int64_t kReadTurns = 4, kReadTurns4 = 8;
 template <class Out>
@@ -273,7 +273,8 @@ cudaError_t read_rows(CacheReadParams& p, int32_t dim, bool four, int sm_count, 
 // that way (of sequences that fill the table), else one, with four steps of its positions and so fewer
 // partial results.  Measured with 1, 2 and 4 (us): 64 rows of up to 20001 positions, 8 heads: 229, 218,
 // 218; 16 such rows: 67, 66, 67; 8 rows: 40, 40, 44; 32 rows of up to 16385, 4 heads, 16 bits: 97 with 1,
-// 94 with 2; 16 of them: 54, 53, 58; 64 rows of 2048 selected: 44.5, 43.0, 49.6.
+// 94 with 2; 16 of them: 54, 53, 58; 64 rows of 2048 selected: 44.5, 43.0, 49.6.  (All of it and the next rules'
+// figures over E4M3 and 16-bit caches; E2M1 ones follow the same limits, without figures of their own.)
 constexpr int64_t kAttnHeadTiles = 8;
 
 // (The lengths lie on the device, so this rule and the next take the table's width for them.  A table of

@@ -38,7 +38,8 @@ __device__ __forceinline__ uint32_t twice(uint32_t x)
 }
 
 // Whether a warp looks up the pages of 32 steps at once where their positions share them.  Not for 16 heads, whose
-// registers are short (of 131072 positions 23.4 us with it, 22.5 without; of a batch with 8 heads a warp 149 and 154).
+// registers are short (one row of 131072 positions 23.4 us with it, 22.5 without; a batch with 8 heads a warp 149 and
+// 154; a batch with 16 was not measured).
 template <class S>
 constexpr bool kWholeSteps = S::kNT == 1;
 

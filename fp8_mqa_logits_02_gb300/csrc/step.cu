@@ -16,7 +16,8 @@ namespace {
 
 size_t pages_smem_bytes(int32_t B) { return 4 * size_t(B + 1) * sizeof(int32_t); }
 
-// A cluster for what it has the threads for, else a CTA for each kPagesTokens tokens and then the lengths.
+// A cluster for what it has the threads for, else a CTA for each kPagesTokens tokens and then the lengths.  By the rows
+// for new tokens alone, which the host knows; pages that come and go take what CTAs there are.
 constexpr int64_t kPagesTokens = 4 * kPagesThreads;
 constexpr unsigned kPagesCluster = 8;
 constexpr int64_t kPagesInCluster = 2 * kPagesCluster * kPagesTokens;

@@ -285,9 +285,10 @@ FP8MQA_API int fp8_mqa_topk_ex(const float* logits, int64_t M, int64_t N, int64_
  * are never read.  Table entries past a sequence's length are not read either.
  *
  * The first paged call on a device sets up its state (kernel attributes and a status word); make
- * it before any stream capture, as for fp8_mqa_logits.  Kernels are launched so that their set-up
- * overlaps the end of the kernel before them on the stream; what they read and write is ordered as
- * ever.
+ * it before any stream capture, as for fp8_mqa_logits.  Kernels are launched so that their set-up need
+ * not wait for the kernel before them on the stream: it overlaps the page tables', the norms' and the
+ * first of an attention call's, which let it in, and begins with the last block's end of the others; what
+ * they read and write is ordered as ever.
  *
  * Limits: dim is 64 or 128; data 16-byte aligned with strides of a multiple of 16 bytes; groups and
  * their strides a multiple of dim / 16 bytes;
